@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <string>
@@ -246,6 +247,137 @@ kda_status chunk_fwd(const kda_chunk_args* a, void* hip_stream, bool noalloc) {
   return ok();
 }
 
+// ---- paged caches -----------------------------------------------------------------------
+
+bool cache_dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16 || t == KDA_F8E4M3; }
+size_t cache_dsize(kda_dtype t) { return t == KDA_F32 ? 4 : t == KDA_BF16 ? 2 : 1; }
+constexpr int64_t kMaxStride = int64_t(1) << 40;  // bytes; keeps every address below 2^63
+
+// A stride (elements of `es` bytes) of an array read and written 16 bytes at a time.
+bool stride_ok(int64_t s, size_t es) {
+  return s >= 0 && s <= kMaxStride / (int64_t)es && s * (int64_t)es % 16 == 0;
+}
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Shapes, dtypes and strides of a paged cache beside activations of type `act`.
+kda_status validate_cache_shapes(const kda_page_cache& c, kda_dtype act) {
+  if (!cache_dtype_ok(c.dtype)) return fail(KDA_ERR_BAD_DTYPE, "unknown cache dtype");
+  if ((act == KDA_F32) != (c.dtype == KDA_F32))
+    return fail(KDA_ERR_BAD_DTYPE, "an F32 cache goes with F32 activations, BF16 and F8E4M3 with BF16");
+  if (c.num_pages < 1 || c.page_size < 1 || c.max_pages < 1)
+    return fail(KDA_ERR_BAD_SHAPE, "need num_pages, page_size, max_pages >= 1 (got %d, %d, %d)",
+                c.num_pages, c.page_size, c.max_pages);
+  return KDA_OK;
+}
+
+kda_status validate_cache(const kda_page_cache& c, int Hkv, int d, Range* k, Range* v) {
+  if (!c.k || !c.v || !c.block_table)
+    return fail(KDA_ERR_NULL_PTR, "cache k, v and block_table must be non-NULL");
+  if (c.dtype != KDA_F8E4M3 && (c.k_scale || c.v_scale))
+    return fail(KDA_ERR_UNSUPPORTED, "k_scale and v_scale are for F8E4M3 caches");
+  const size_t es = cache_dsize(c.dtype);
+  const int64_t strides[] = {c.k_page_stride, c.k_token_stride, c.k_head_stride,
+                             c.v_page_stride, c.v_token_stride, c.v_head_stride};
+  for (int64_t s : strides)
+    if (!stride_ok(s, es))
+      return fail(KDA_ERR_BAD_SHAPE, "cache strides must be >= 0 and multiples of 16 bytes");
+  if (!aligned16(c.k) || !aligned16(c.v))
+    return fail(KDA_ERR_BAD_SHAPE, "cache k and v must be 16-byte aligned");
+  if (c.table_stride < 0 || c.table_stride > kMaxStride)
+    return fail(KDA_ERR_BAD_SHAPE, "table_stride must be >= 0");
+  auto bytes = [&](int64_t page, int64_t token, int64_t head) {
+    const double top = (double)(c.num_pages - 1) * (double)page +
+                       (double)(c.page_size - 1) * (double)token + (double)(Hkv - 1) * (double)head;
+    if (top * (double)es > 0x1p60) return SIZE_MAX;
+    return (size_t)(((int64_t)(c.num_pages - 1) * page + (int64_t)(c.page_size - 1) * token +
+                     (int64_t)(Hkv - 1) * head + d) * (int64_t)es);
+  };
+  const size_t kb = bytes(c.k_page_stride, c.k_token_stride, c.k_head_stride);
+  const size_t vb = bytes(c.v_page_stride, c.v_token_stride, c.v_head_stride);
+  if (kb == SIZE_MAX || vb == SIZE_MAX) return fail(KDA_ERR_BAD_SHAPE, "cache too large");
+  *k = range("the key cache", c.k, kb);
+  *v = range("the value cache", c.v, vb);
+  return KDA_OK;
+}
+
+kda::PageCache page_cache(const kda_page_cache& c) {
+  const int64_t es = (int64_t)cache_dsize(c.dtype);
+  kda::PageCache r{};
+  r.k = static_cast<char*>(c.k);
+  r.v = static_cast<char*>(c.v);
+  r.num_pages = c.num_pages;
+  r.page_size = c.page_size;
+  // n / d = (n * m) >> s for n < 2^31: s = 31 + ceil(log2 d), m = floor(2^s / d) + 1 <= 2^32 - 1
+  // unless d = 1, where m = 2^31 + 1 serves as well
+  int up = 0;
+  while ((int64_t(1) << up) < c.page_size) ++up;
+  r.ps_shift = 31 + up;
+  r.ps_mul = (unsigned)((uint64_t(1) << r.ps_shift) / (uint64_t)c.page_size + 1);
+  r.k_page = c.k_page_stride * es, r.k_token = c.k_token_stride * es, r.k_head = c.k_head_stride * es;
+  r.v_page = c.v_page_stride * es, r.v_token = c.v_token_stride * es, r.v_head = c.v_head_stride * es;
+  r.table = c.block_table;
+  r.table_stride = c.table_stride;
+  r.max_pages = c.max_pages;
+  r.k_scale = c.k_scale;
+  r.v_scale = c.v_scale;
+  return r;
+}
+
+Range table_range(const kda_page_cache& c, int n_seq) {
+  return range("block_table", c.block_table,
+               sizeof(int32_t) * ((size_t)(n_seq - 1) * c.table_stride + c.max_pages));
+}
+
+// Rows of [tokens, heads, d] by strides (elements): what they span.
+size_t span_bytes(int64_t tokens, int64_t token_stride, int heads, int64_t head_stride, int d, size_t es) {
+  return tokens ? (size_t)((tokens - 1) * token_stride + (heads - 1) * head_stride + d) * es : 0;
+}
+bool span_ok(int64_t tokens, int64_t token_stride, int heads, int64_t head_stride) {
+  return (double)tokens * (double)token_stride + (double)heads * (double)head_stride < 0x1p58;
+}
+
+// Shapes of kda_paged_decode, and its launch.
+kda_status validate_decode_shapes(const kda_paged_decode_args* a, kda::PagedDecodePlan* p, size_t* ws) {
+  if (!a) return fail(KDA_ERR_NULL_PTR, "args is NULL");
+  if (a->N < 1 || a->m < 1 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv)
+    return fail(KDA_ERR_BAD_SHAPE, "need N, m, Hkv >= 1 and Hq a multiple of Hkv (got N=%d m=%d Hq=%d Hkv=%d)",
+                a->N, a->m, a->Hq, a->Hkv);
+  if (!head_dim_ok(a->d)) return fail(KDA_ERR_BAD_SHAPE, "d must be 32, 64 or 128 (got %d)", a->d);
+  if (!dtype_ok(a->act_dtype) || !dtype_ok(a->out_dtype)) return fail(KDA_ERR_BAD_DTYPE, "unknown dtype");
+  if (a->flags) return fail(KDA_ERR_UNSUPPORTED, "unknown flags 0x%x", a->flags);
+  kda_status s = validate_cache_shapes(a->cache, a->act_dtype);
+  if (s != KDA_OK) return s;
+  if (a->max_len < 1 || a->max_len > (int64_t)a->cache.max_pages * a->cache.page_size ||
+      a->max_len > (1 << 30))
+    return fail(KDA_ERR_BAD_SHAPE, "max_len must be in 1 .. max_pages * page_size, at most 2^30 (got %d)",
+                a->max_len);
+  if (a->window < 0) return fail(KDA_ERR_BAD_SHAPE, "window must be >= 0 (got %d)", a->window);
+  if ((int64_t)a->m * a->Hq > (1 << 24)) return fail(KDA_ERR_BAD_SHAPE, "m * Hq too large");
+  // one 256-work-item workgroup per (sequence, row block, head); a row block holds 16 rows or more
+  const int64_t pairs = (int64_t)a->N * a->Hkv * (((int64_t)a->m * (a->Hq / a->Hkv) + 15) / 16);
+  if (pairs > kMaxDecodePairs || (int64_t)a->N * a->m * a->Hq > (int64_t(1) << 40))
+    return fail(KDA_ERR_BAD_SHAPE, "N * m * Hq too large for one launch");
+  *p = kda::PagedDecodePlan{};
+  p->N = a->N, p->m = a->m, p->Hq = a->Hq, p->Hkv = a->Hkv, p->d = a->d;
+  p->act_bf16 = a->act_dtype == KDA_BF16;
+  p->out_bf16 = a->out_dtype == KDA_BF16;
+  p->cache_type = a->cache.dtype;
+  p->max_len = a->max_len;
+  p->window = a->window;
+  *ws = kda::plan_paged_decode(p);
+  return KDA_OK;
+}
+
+kda_status validate_verify_shapes(const kda_verify_args* a) {
+  if (!a) return fail(KDA_ERR_NULL_PTR, "args is NULL");
+  if (a->N < 1 || a->m < 1 || a->V < 1)
+    return fail(KDA_ERR_BAD_SHAPE, "need N, m, V >= 1 (got N=%d m=%d V=%d)", a->N, a->m, a->V);
+  if (!dtype_ok(a->dtype)) return fail(KDA_ERR_BAD_DTYPE, "unknown dtype");
+  if (a->V > (1 << 30) || kda::verify_blocks(a->N, a->V) > kMaxDecodePairs)
+    return fail(KDA_ERR_BAD_SHAPE, "N * V too large for one launch");
+  return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -365,6 +497,200 @@ kda_status kda_check_gates(const void* g, int64_t n_g, const void* beta, int64_t
     return fail(KDA_ERR_ALIAS, "counts overlaps g or beta");
   return run_gate_check(g, n_g, beta, n_beta, gate_dtype, counts, n_counts,
                         static_cast<hipStream_t>(hip_stream), n_bad);
+}
+
+kda_status kda_kv_append(const kda_kv_append_args* a, void* hip_stream) {
+  if (!a) return fail(KDA_ERR_NULL_PTR, "args is NULL");
+  if (a->B < 1 || a->T < 0 || a->Hq < 0 || a->Hkv < 1)
+    return fail(KDA_ERR_BAD_SHAPE, "need B >= 1, T >= 0, Hq >= 0, Hkv >= 1 (got B=%d T=%d Hq=%d Hkv=%d)",
+                a->B, a->T, a->Hq, a->Hkv);
+  if (!head_dim_ok(a->d)) return fail(KDA_ERR_BAD_SHAPE, "d must be 32, 64 or 128 (got %d)", a->d);
+  if (a->cu_seqlens && (a->B != 1 || a->N < 1))
+    return fail(KDA_ERR_BAD_SHAPE, "cu_seqlens requires B == 1 and N >= 1 (got B=%d N=%d)", a->B, a->N);
+  if (!dtype_ok(a->act_dtype)) return fail(KDA_ERR_BAD_DTYPE, "unknown dtype");
+  if (a->flags & ~KDA_APPEND_PAIRS) return fail(KDA_ERR_UNSUPPORTED, "unknown flags 0x%x", a->flags);
+  if (a->rot < 0 || a->rot > a->d || a->rot % 16)
+    return fail(KDA_ERR_BAD_SHAPE, "rot must be a multiple of 16 in 0 .. d (got %d)", a->rot);
+  kda_status s = validate_cache_shapes(a->cache, a->act_dtype);
+  if (s != KDA_OK) return s;
+  const int64_t tok = (int64_t)a->B * a->T;
+  const int n_seq = a->cu_seqlens ? a->N : a->B;
+  const int Hq = a->q ? a->Hq : 0;
+  if (tok > kMaxDecodePairs || tok * ((int64_t)Hq + a->Hkv) * a->d > (int64_t(1) << 42) ||
+      (int64_t)Hq + 2 * (int64_t)a->Hkv > (1 << 24))
+    return fail(KDA_ERR_BAD_SHAPE, "too many tokens or heads for one launch");
+  if ((a->rot > 0) != (a->inv_freq != nullptr))
+    return fail(KDA_ERR_NULL_PTR, "inv_freq goes with rot > 0, and NULL with rot = 0");
+  if ((a->q != nullptr) != (a->q_out != nullptr) && tok > 0)
+    return fail(KDA_ERR_NULL_PTR, "q and q_out go together");
+  if (a->q && Hq < 1) return fail(KDA_ERR_BAD_SHAPE, "q needs Hq >= 1");
+  Range kc{}, vc{};
+  s = validate_cache(a->cache, a->Hkv, a->d, &kc, &vc);
+  if (s != KDA_OK) return s;
+  if (!a->start || (tok > 0 && (!a->k || !a->v)))
+    return fail(KDA_ERR_NULL_PTR, "k, v and start must be non-NULL");
+  const size_t es = dsize(a->act_dtype);
+  const int64_t strides[] = {a->k_token_stride, a->k_head_stride, a->v_token_stride, a->v_head_stride,
+                             a->q ? a->q_token_stride : 0, a->q ? a->q_head_stride : 0};
+  for (int64_t x : strides)
+    if (!stride_ok(x, es))
+      return fail(KDA_ERR_BAD_SHAPE, "q, k and v strides must be >= 0 and multiples of 16 bytes");
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->q_out))
+    return fail(KDA_ERR_BAD_SHAPE, "q, k, v and q_out must be 16-byte aligned");
+  if (!span_ok(tok, a->k_token_stride, a->Hkv, a->k_head_stride) ||
+      !span_ok(tok, a->v_token_stride, a->Hkv, a->v_head_stride) ||
+      (a->q && !span_ok(tok, a->q_token_stride, Hq, a->q_head_stride)))
+    return fail(KDA_ERR_BAD_SHAPE, "q, k or v too large");
+  const Range in[] = {
+      range("q", a->q, a->q ? span_bytes(tok, a->q_token_stride, Hq, a->q_head_stride, a->d, es) : 0),
+      range("k", a->k, span_bytes(tok, a->k_token_stride, a->Hkv, a->k_head_stride, a->d, es)),
+      range("v", a->v, span_bytes(tok, a->v_token_stride, a->Hkv, a->v_head_stride, a->d, es)),
+      range("start", a->start, sizeof(int32_t) * (size_t)n_seq),
+      range("inv_freq", a->inv_freq, a->inv_freq ? sizeof(float) * (a->rot / 2) : 0),
+      range("cu_seqlens", a->cu_seqlens, a->cu_seqlens ? sizeof(int32_t) * ((size_t)a->N + 1) : 0),
+      range("k_scale", a->cache.k_scale, a->cache.k_scale ? sizeof(float) * a->Hkv : 0),
+      range("v_scale", a->cache.v_scale, a->cache.v_scale ? sizeof(float) * a->Hkv : 0),
+      table_range(a->cache, n_seq)};
+  const Range qo = range("q_out", a->q_out, a->q ? (size_t)tok * Hq * a->d * es : 0);
+  const bool in_place = a->q_out == a->q && a->q_head_stride == a->d &&
+                        a->q_token_stride == (int64_t)Hq * a->d;
+  for (const Range& r : in) {
+    if (overlap(kc, r) || overlap(vc, r)) return fail(KDA_ERR_ALIAS, "the cache overlaps %s", r.name);
+    if (overlap(qo, r) && !(in_place && std::strcmp(r.name, "q") == 0))
+      return fail(KDA_ERR_ALIAS, "q_out overlaps %s", r.name);
+  }
+  if (overlap(kc, qo) || overlap(vc, qo)) return fail(KDA_ERR_ALIAS, "the cache overlaps q_out");
+  kda::KvAppendPlan p{};
+  p.B = a->B, p.T = a->T, p.Hq = Hq, p.Hkv = a->Hkv, p.d = a->d, p.rot = a->rot, p.n_seq = n_seq;
+  p.cu_seqlens = a->cu_seqlens;
+  p.act_bf16 = a->act_dtype == KDA_BF16;
+  p.pairs = (a->flags & KDA_APPEND_PAIRS) != 0;
+  p.cache_type = a->cache.dtype;
+  p.q = static_cast<const char*>(a->q);
+  p.k = static_cast<const char*>(a->k);
+  p.v = static_cast<const char*>(a->v);
+  const int64_t e = (int64_t)es;
+  p.q_token = strides[4] * e, p.q_head = strides[5] * e;
+  p.k_token = a->k_token_stride * e, p.k_head = a->k_head_stride * e;
+  p.v_token = a->v_token_stride * e, p.v_head = a->v_head_stride * e;
+  p.q_out = static_cast<char*>(a->q_out);
+  p.start = a->start;
+  p.inv_freq = a->inv_freq;
+  p.c = page_cache(a->cache);
+  const hipError_t err = kda::launch_kv_append(p, static_cast<hipStream_t>(hip_stream));
+  if (err != hipSuccess) return fail(KDA_ERR_HIP, "kda_kv_append launch: %s", hipGetErrorString(err));
+  return ok();
+}
+
+size_t kda_paged_decode_workspace_bytes(const kda_paged_decode_args* a) {
+  kda::PagedDecodePlan p;
+  size_t ws = 0;
+  if (validate_decode_shapes(a, &p, &ws) != KDA_OK) return SIZE_MAX;
+  ok();
+  return ws;
+}
+
+kda_status kda_paged_decode(const kda_paged_decode_args* a, void* hip_stream) {
+  kda::PagedDecodePlan p;
+  size_t need = 0;
+  kda_status s = validate_decode_shapes(a, &p, &need);
+  if (s != KDA_OK) return s;
+  if (!a->q || !a->seq_lens || !a->o)
+    return fail(KDA_ERR_NULL_PTR, "q, seq_lens and o must be non-NULL");
+  if (!std::isfinite(a->scale)) return fail(KDA_ERR_BAD_SHAPE, "scale must be finite");
+  Range kc{}, vc{};
+  s = validate_cache(a->cache, a->Hkv, a->d, &kc, &vc);
+  if (s != KDA_OK) return s;
+  const size_t es = dsize(a->act_dtype), os = dsize(a->out_dtype);
+  const int64_t tok = (int64_t)a->N * a->m;
+  if (!stride_ok(a->q_token_stride, es) || !stride_ok(a->q_head_stride, es))
+    return fail(KDA_ERR_BAD_SHAPE, "q strides must be >= 0 and multiples of 16 bytes");
+  if (!aligned16(a->q) || !aligned16(a->o))
+    return fail(KDA_ERR_BAD_SHAPE, "q and o must be 16-byte aligned");
+  if (!span_ok(tok, a->q_token_stride, a->Hq, a->q_head_stride))
+    return fail(KDA_ERR_BAD_SHAPE, "q too large");
+  if (need && (!a->workspace || a->workspace_bytes < need))
+    return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                a->workspace ? a->workspace_bytes : (size_t)0);
+  if (reinterpret_cast<uintptr_t>(a->workspace) % 256)
+    return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const Range in[] = {
+      range("q", a->q, span_bytes(tok, a->q_token_stride, a->Hq, a->q_head_stride, a->d, es)),
+      kc, vc, table_range(a->cache, a->N), range("seq_lens", a->seq_lens, sizeof(int32_t) * (size_t)a->N),
+      range("k_scale", a->cache.k_scale, a->cache.k_scale ? sizeof(float) * a->Hkv : 0),
+      range("v_scale", a->cache.v_scale, a->cache.v_scale ? sizeof(float) * a->Hkv : 0)};
+  const Range out[] = {range("o", a->o, (size_t)tok * a->Hq * a->d * os),
+                       range("lse", a->lse, a->lse ? (size_t)tok * a->Hq * sizeof(float) : 0),
+                       range("workspace", a->workspace, need)};
+  for (const Range& w : out)
+    for (const Range& r : in)
+      if (overlap(w, r)) return fail(KDA_ERR_ALIAS, "%s overlaps %s", w.name, r.name);
+  if (overlap(out[0], out[1]) || overlap(out[0], out[2]) || overlap(out[1], out[2]))
+    return fail(KDA_ERR_ALIAS, "o, lse and workspace must not overlap");
+  p.q = static_cast<const char*>(a->q);
+  p.q_token = a->q_token_stride * (int64_t)es;
+  p.q_head = a->q_head_stride * (int64_t)es;
+  p.c = page_cache(a->cache);
+  p.seq_lens = a->seq_lens;
+  p.scale = a->scale;
+  p.o = a->o;
+  p.lse = a->lse;
+  p.part_o = static_cast<float*>(a->workspace);
+  p.part_ml = p.part_o + (size_t)p.split * 2 * 16 * p.tiles * a->d;
+  const hipError_t e = kda::launch_paged_decode(p, static_cast<hipStream_t>(hip_stream));
+  if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_paged_decode launch: %s", hipGetErrorString(e));
+  return ok();
+}
+
+size_t kda_verify_drafts_workspace_bytes(const kda_verify_args* a) {
+  if (validate_verify_shapes(a) != KDA_OK) return SIZE_MAX;
+  ok();
+  return kda::verify_workspace_bytes(a->N, a->V);
+}
+
+kda_status kda_verify_drafts(const kda_verify_args* a, void* hip_stream) {
+  kda_status s = validate_verify_shapes(a);
+  if (s != KDA_OK) return s;
+  if (!a->p || !a->drafts || !a->uniform || !a->accept || !a->tokens)
+    return fail(KDA_ERR_NULL_PTR, "p, drafts, uniform, accept and tokens must be non-NULL");
+  const int64_t most = int64_t(1) << 42;  // elements: keeps every offset below 2^63
+  auto rows_ok = [&](int64_t seq, int64_t row, int rows) {
+    return row >= 0 && seq >= 0 && row <= most && seq <= most &&
+           (double)(a->N - 1) * (double)seq + (double)(rows - 1) * (double)row < 0x1p58;
+  };
+  if (!rows_ok(a->p_seq_stride, a->p_row_stride, a->m + 1) ||
+      (a->q && !rows_ok(a->q_seq_stride, a->q_row_stride, a->m)))
+    return fail(KDA_ERR_BAD_SHAPE, "p and q strides must be >= 0 and in range");
+  const size_t es = dsize(a->dtype);
+  auto rows_bytes = [&](int64_t seq, int64_t row, int rows) {
+    return (size_t)((a->N - 1) * seq + (int64_t)(rows - 1) * row + a->V) * es;
+  };
+  const size_t need = kda::verify_workspace_bytes(a->N, a->V);
+  if (!a->workspace || a->workspace_bytes < need)
+    return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                a->workspace ? a->workspace_bytes : (size_t)0);
+  if (reinterpret_cast<uintptr_t>(a->workspace) % 256)
+    return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const size_t nm = (size_t)a->N * a->m, nm1 = nm + a->N;
+  const Range in[] = {range("p", a->p, rows_bytes(a->p_seq_stride, a->p_row_stride, a->m + 1)),
+                      range("q", a->q, a->q ? rows_bytes(a->q_seq_stride, a->q_row_stride, a->m) : 0),
+                      range("drafts", a->drafts, nm * sizeof(int32_t)),
+                      range("n_drafts", a->n_drafts, a->n_drafts ? a->N * sizeof(int32_t) : 0),
+                      range("uniform", a->uniform, nm1 * sizeof(float))};
+  const Range out[] = {range("accept", a->accept, a->N * sizeof(int32_t)),
+                       range("tokens", a->tokens, nm1 * sizeof(int32_t)),
+                       range("workspace", a->workspace, need)};
+  for (const Range& w : out)
+    for (const Range& r : in)
+      if (overlap(w, r)) return fail(KDA_ERR_ALIAS, "%s overlaps %s", w.name, r.name);
+  if (overlap(out[0], out[1]) || overlap(out[0], out[2]) || overlap(out[1], out[2]))
+    return fail(KDA_ERR_ALIAS, "accept, tokens and workspace must not overlap");
+  const kda::VerifyPlan p{a->N, a->m, a->V, a->dtype == KDA_BF16, a->p, a->q,
+                          a->p_seq_stride, a->p_row_stride, a->q_seq_stride, a->q_row_stride,
+                          a->drafts, a->n_drafts, a->uniform, a->accept, a->tokens, a->workspace};
+  const hipError_t e = kda::launch_verify(p, static_cast<hipStream_t>(hip_stream));
+  if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_verify_drafts launch: %s", hipGetErrorString(e));
+  return ok();
 }
 
 const char* kda_status_string(kda_status s) {

@@ -63,6 +63,69 @@ hipError_t launch_chunk_fast(const ChunkPlan& p, hipStream_t stream);
 size_t noalloc_scratch_bytes();
 hipError_t noalloc_scratch(void** ptr);
 
+// A paged cache as the kernels take it (validated; strides in bytes).
+struct PageCache {
+  char *k, *v;
+  int num_pages, page_size;
+  unsigned ps_mul;  // token / page_size = (token * ps_mul) >> ps_shift for 0 <= token < 2^31
+  int ps_shift;
+  int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+  const int32_t* table;
+  int64_t table_stride;
+  int max_pages;
+  const float *k_scale, *v_scale;
+};
+
+struct KvAppendPlan {
+  int B, T, Hq, Hkv, d, rot, n_seq;
+  const int32_t* cu_seqlens;
+  bool act_bf16, pairs;
+  int cache_type;                // a kda_dtype
+  const char *q, *k, *v;         // strides in bytes
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  char* q_out;
+  const int32_t* start;
+  const float* inv_freq;
+  PageCache c;
+};
+hipError_t launch_kv_append(const KvAppendPlan& p, hipStream_t stream);
+
+struct PagedDecodePlan {
+  int N, m, Hq, Hkv, d;
+  int group, rows;               // Hq / Hkv; m * group query rows per key/value head
+  int row_blocks;                // blocks of 16 * tiles rows
+  int tiles;                     // 16-row tiles a workgroup carries
+  bool act_bf16, out_bf16;
+  int cache_type;
+  const char* q;                 // strides in bytes
+  int64_t q_token, q_head;
+  PageCache c;
+  const int32_t* seq_lens;
+  int max_len, window;
+  float scale;
+  void* o;
+  float* lse;
+  int split;                     // workgroups that share all work evenly; 0: one per (n, rows, head)
+  float *part_o, *part_ml;       // workspace: partial results of shared (n, rows, head)s
+};
+// Fills in the launch shape (tiles, row_blocks, split) and returns the workspace bytes.
+size_t plan_paged_decode(PagedDecodePlan* p);
+hipError_t launch_paged_decode(const PagedDecodePlan& p, hipStream_t stream);
+
+struct VerifyPlan {
+  int N, m, V;
+  bool bf16;
+  const void *p, *q;
+  int64_t p_seq, p_row, q_seq, q_row;  // elements
+  const int32_t *drafts, *n_drafts;
+  const float* uniform;
+  int32_t *accept, *tokens;
+  void* workspace;
+};
+size_t verify_workspace_bytes(int N, int V);
+int64_t verify_blocks(int N, int V);  // workgroups of its larger launch
+hipError_t launch_verify(const VerifyPlan& p, hipStream_t stream);
+
 // Device check of g in [-5, 0] and beta in [0, 1] over n_blocks workgroups (1 .. check_blocks());
 // writes each workgroup's count of violations into counts[0 .. n_blocks).
 int check_blocks();

@@ -11,7 +11,7 @@
  * which is why per-device states cannot simply be summed (same page, section
  * "Die Rechnung landet in der Bereitstellungsinfrastruktur").
  *
- * Two calls:
+ * Two core calls (decode_multi and the calls for the layers beside KDA are declared below):
  *   kda_chunk_fwd    - prefill: the whole sequence(s), chunkwise parallel. Chunks are split
  *                      into 16-token tiles whose cumulative log-decay stays in [-80, 0]
  *                      because each step's log-decay is >= -5 (section "Eine Untergrenze,
@@ -74,7 +74,8 @@ typedef enum {
     KDA_ERR_ALIAS = 8         /* an output overlaps an input it must not overlap */
 } kda_status;
 
-typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
+/* KDA_F8E4M3 (OCP e4m3, largest value 448) is offered for paged caches only (kda_page_cache). */
+typedef enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_F8E4M3 = 2 } kda_dtype;
 
 /* Arguments of kda_chunk_fwd (prefill).
  *
@@ -249,6 +250,185 @@ kda_status kda_decode_multi(const kda_decode_multi_args* args, void* hip_stream)
 kda_status kda_check_gates(const void* g, int64_t n_g, const void* beta, int64_t n_beta,
                            kda_dtype gate_dtype, int64_t* counts, int n_counts,
                            void* hip_stream, int64_t* n_bad);
+
+/* ---- The other half of a serving step -------------------------------------------------
+ *
+ * A hybrid stack puts global attention layers between the KDA layers (three KDA layers to one;
+ * orkas.ai Kimi K3 page, section "Sequenz"). Their memory grows with the context and is kept in
+ * pages per token (same page, serving-infrastructure section). kda_kv_append fills such a paged
+ * cache, kda_paged_decode attends to it for the new tokens, and kda_verify_drafts decides how
+ * many drafted tokens stand, which is the `accept` of kda_decode_multi.
+ *
+ * Values that live on the device cannot be checked on the host. The three calls below read and
+ * write nothing out of bounds whatever block tables, lengths, positions, counts and token ids
+ * hold; what such a value means is said at its field.
+ */
+
+/* A paged key/value cache of one layer.
+ *   k, v         num_pages pages of page_size tokens of Hkv heads of d channels each: element
+ *                (page, slot, head, c) lies at page * page_stride + slot * token_stride +
+ *                head * head_stride + c, strides in elements (>= 0). Pages with the token
+ *                outermost or the head outermost, and k and v interleaved in one allocation, are
+ *                all a matter of strides. k, v and every stride are multiples of 16 bytes.
+ *   dtype        KDA_BF16 or KDA_F8E4M3 beside bf16 activations, KDA_F32 beside fp32 ones.
+ *   page_size    tokens per page, >= 1. Multiples of 16 are read faster than others.
+ *   block_table  device int32: page p of sequence n is block_table[n * table_stride + p],
+ *                p < max_pages. Entries past a sequence's last page are not read. A page id
+ *                outside [0, num_pages) is no page: nothing is written to it, and its tokens
+ *                are seen by no query.
+ *   k_scale, v_scale
+ *                device fp32 [Hkv], or NULL for ones: a stored value times its head's scale is
+ *                the value meant. Finite and positive. Only with KDA_F8E4M3 (NULL otherwise).
+ */
+typedef struct {
+    void *k, *v;
+    kda_dtype dtype;
+    int num_pages, page_size;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    const int32_t* block_table;
+    int64_t table_stride;
+    int max_pages;
+    const float *k_scale, *v_scale;
+} kda_page_cache;
+
+/* Arguments of kda_kv_append: new tokens' keys and values into a paged cache, rotated by
+ * position on the way; queries rotated alongside.
+ *   B, T, cu_seqlens, N
+ *              dense batch of B sequences with T new tokens each, or packed sequences, as in
+ *              kda_chunk_args (T = 0 is allowed; tokens at or past cu_seqlens[N] are left alone,
+ *              their rows of q_out included). n_seq = B or N.
+ *   Hq, Hkv, d heads of q and of k and v, channels per head: d in {32, 64, 128}.
+ *   act_dtype  of q, k, v and q_out: KDA_F32 or KDA_BF16.
+ *   q, k, v    [B, T, heads, d]: token t = b * T + j of head h begins at t * token_stride +
+ *              h * head_stride (elements), so views of a fused projection can be passed. The
+ *              pointers and strides are multiples of 16 bytes. q may be NULL.
+ *   q_out      [B, T, Hq, d] contiguous, 16-byte aligned, NULL exactly if q is. May be q itself
+ *              if q is contiguous; otherwise it overlaps no input.
+ *   start      device int32 [n_seq]: tokens of each sequence in the cache so far. New token j
+ *              has position start[n] + j, and goes to slot position % page_size of page
+ *              position / page_size. Tokens whose position is negative or at or past
+ *              max_pages * page_size are not stored; their q_out is written all the same. Two
+ *              new tokens must not go to the same slot of the same page.
+ *   inv_freq   device fp32 [rot / 2], or NULL with rot = 0 (no rotation: k is stored and q
+ *              copied as they are). Channel pair i < rot / 2 of a token at position p is turned
+ *              by the angle p * inv_freq[i] (exact product, reduced in 64 bits):
+ *                  x' = x cos - y sin,   y' = y cos + x sin.
+ *   rot        channels that turn, a multiple of 16, 0 <= rot <= d. Channels rot .. d - 1 stay.
+ *   flags      0: pair i is channels (i, i + rot / 2). KDA_APPEND_PAIRS: (2i, 2i + 1).
+ *   cache      where k and v go. With KDA_F8E4M3 a value is divided by its scale, limited to
+ *              [-448, 448] and rounded to nearest even; NaN stays NaN. The k and v arrays
+ *              overlap no other argument.
+ */
+#define KDA_APPEND_PAIRS 1u
+typedef struct {
+    int B, T, Hq, Hkv, d;
+    const int32_t* cu_seqlens;
+    int N;
+    kda_dtype act_dtype;
+    const void *q, *k, *v;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    void* q_out;
+    const int32_t* start;
+    const float* inv_freq;
+    int rot;
+    unsigned flags;
+    kda_page_cache cache;
+} kda_kv_append_args;
+
+/* Arguments of kda_paged_decode: attention of m new tokens of each of N sequences (m = 1: plain
+ * decode; m drafts for speculative decoding) over a paged cache that already holds them.
+ *   Hq, Hkv, d Hq is a multiple of Hkv: query head h reads key/value head h / (Hq / Hkv).
+ *              d in {32, 64, 128}.
+ *   act_dtype  of q: KDA_F32 or KDA_BF16.   out_dtype  of o, either.
+ *   q          [N, m, Hq, d] by q_token_stride (from (n, j) to the next, n * m + j counted) and
+ *              q_head_stride; 16-byte aligned like kda_kv_append's.
+ *   seq_lens   device int32 [N]: tokens of each sequence in the cache, the new ones included.
+ *              Values outside [0, max_len] are taken as the nearer bound.
+ *   max_len    no length is larger; 1 <= max_len <= max_pages * page_size. The launch is shaped
+ *              by it, so a tight one is faster; the result does not depend on it.
+ *   window     0, or the number of latest tokens that a query sees (its own included).
+ *   scale      finite; o = softmax(scale * q k^T) v. New token j of sequence n sees positions
+ *              t < hi = seq_lens[n] - m + 1 + j, with a window t >= hi - window too. What it does
+ *              not see does not reach it, NaN and infinities included. If it sees none, its o
+ *              is 0 and its lse -inf.
+ *   o          [N, m, Hq, d] contiguous, out_dtype, 16-byte aligned.
+ *   lse        fp32 [N, m, Hq], or NULL: natural logarithm of sum_t e^{scale q k_t} (for joining
+ *              results over parts of a context).
+ *   workspace  device scratch of at least kda_paged_decode_workspace_bytes() bytes, 256-byte
+ *              aligned; contents on entry are ignored. (NULL when that is 0.) Calls that overlap
+ *              in time need one each.
+ *   flags      0.
+ */
+typedef struct {
+    int N, m, Hq, Hkv, d;
+    kda_dtype act_dtype, out_dtype;
+    const void* q;
+    int64_t q_token_stride, q_head_stride;
+    kda_page_cache cache;
+    const int32_t* seq_lens;
+    int max_len, window;
+    float scale;
+    void* o;
+    float* lse;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned flags;
+} kda_paged_decode_args;
+
+/* Arguments of kda_verify_drafts: how many of m drafted tokens of each of N sequences stand
+ * against the target model's probabilities, and the token that follows them, so that the
+ * tokens are distributed as if drawn from the target alone.
+ *   m, V       drafts per sequence and vocabulary size, >= 1.   dtype  of p and q: KDA_F32 or KDA_BF16.
+ *   p          target probabilities [N, m + 1, V]: row j of sequence n, for the token after j
+ *              drafts, begins at n * p_seq_stride + j * p_row_stride (elements).
+ *   q          probabilities the drafts were drawn from, [N, m, V] by its strides; or NULL if the
+ *              drafts were picked, not drawn (looked up, or the most probable ones): q is then
+ *              one at the draft and zero elsewhere.
+ *   drafts     device int32 [N, m].   n_drafts  device int32 [N] or NULL: sequence n has only the
+ *              first clamp(n_drafts[n], 0, m) drafts.
+ *   uniform    device fp32 [N, m + 1], uniform random numbers in [0, 1) (values below 0 and NaN
+ *              are taken as 0, values of 1 and above as the largest below 1). Draft j stands if
+ *              those before it do and
+ *                  uniform[n, j] * q_j(x_j) < p_j(x_j)
+ *              (in 64 bits, where the product is exact). A draft outside [0, V), or
+ *              whose p or q is not finite, does not stand.
+ *              uniform[n, m] picks the token that follows.
+ *   accept     int32 [N]: drafts that stand, a: the `accept` of a kda_decode_multi whose tokens
+ *              are the drafts (a + 1 for one whose tokens are the last token and the drafts).
+ *   tokens     int32 [N, m + 1]: the a drafts, then the following token, then -1. The following
+ *              token is the smallest i with sum_{i' <= i} w_i' > uniform[n, m] * sum w (sums in
+ *              64 bits, the same on every run), where w = max(p_a - q_a, 0) if a draft fell, and
+ *              w = p_a if all stood or if no w is positive. Probabilities that are negative or
+ *              not finite count as 0 in w. If p_a has nothing positive either, the token is -1.
+ *   workspace  device scratch of at least kda_verify_drafts_workspace_bytes() bytes, 256-byte
+ *              aligned; contents on entry are ignored. Calls that overlap in time need one each.
+ */
+typedef struct {
+    int N, m, V;
+    kda_dtype dtype;
+    const void *p, *q;
+    int64_t p_seq_stride, p_row_stride, q_seq_stride, q_row_stride;
+    const int32_t *drafts, *n_drafts;
+    const float* uniform;
+    int32_t *accept, *tokens;
+    void* workspace;
+    size_t workspace_bytes;
+} kda_verify_args;
+
+/* New keys and values into a paged cache (see kda_kv_append_args). */
+kda_status kda_kv_append(const kda_kv_append_args* args, void* hip_stream);
+
+/* Attention of new tokens over a paged cache (see kda_paged_decode_args). The workspace query
+ * looks at shapes, dtypes and max_len, not at pointers; SIZE_MAX when they are invalid. */
+size_t kda_paged_decode_workspace_bytes(const kda_paged_decode_args* args);
+kda_status kda_paged_decode(const kda_paged_decode_args* args, void* hip_stream);
+
+/* Verification of drafted tokens (see kda_verify_args). The workspace query looks at N, m, V and
+ * dtype only; SIZE_MAX when they are invalid. */
+size_t kda_verify_drafts_workspace_bytes(const kda_verify_args* args);
+kda_status kda_verify_drafts(const kda_verify_args* args, void* hip_stream);
 
 const char* kda_status_string(kda_status s);
 const char* kda_last_error(void);   /* detail of the last failure on this thread */

@@ -1,0 +1,244 @@
+"""Host-side behaviour of kda_kv_append, kda_paged_decode and kda_verify_drafts, without a GPU:
+every call here is refused before any launch, and no pointer is dereferenced. Then the plain
+64-bit forms that the GPU tests compare with, against worked examples."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+from tests import paged_ref
+
+FAKE = 1 << 40
+NULL_PTR, BAD_SHAPE, BAD_DTYPE, UNSUPPORTED, WORKSPACE, ALIAS = 1, 2, 3, 4, 6, 8
+
+
+@pytest.fixture(scope="module")
+def b():
+    from gated_delta_rule_59_amd import binding
+    if not os.path.exists(binding.LIB_PATH):
+        pytest.skip("libkda not built")
+    binding.lib()
+    return binding
+
+
+def call(b, name, a):
+    rc = getattr(b.lib(), "kda_" + name)(ctypes.byref(a), None)
+    return rc, b.lib().kda_last_error().decode()
+
+
+def put(a, **kw):
+    for k, v in kw.items():
+        o = a
+        *path, last = k.split("__")
+        for p in path:
+            o = getattr(o, p)
+        setattr(o, last, v)
+    return a
+
+
+def cache(b, Hkv=2, d=128, es=2, dtype=1):
+    c = b.PageCache()
+    c.k, c.v, c.dtype = FAKE + (8 << 32), FAKE + (9 << 32), dtype
+    c.num_pages, c.page_size, c.max_pages = 100, 16, 20
+    c.k_page_stride = c.v_page_stride = 16 * Hkv * d
+    c.k_token_stride = c.v_token_stride = Hkv * d
+    c.k_head_stride = c.v_head_stride = d
+    c.block_table, c.table_stride = FAKE + (10 << 32), 20
+    return c
+
+
+def append_args(b, **kw):
+    a = b.KvAppendArgs()
+    a.B, a.T, a.Hq, a.Hkv, a.d, a.act_dtype, a.rot = 4, 3, 4, 2, 128, 1, 128
+    a.q, a.k, a.v, a.q_out = (FAKE + (i << 32) for i in range(4))
+    a.q_token_stride, a.q_head_stride = 4 * 128, 128
+    a.k_token_stride = a.v_token_stride = 2 * 128
+    a.k_head_stride = a.v_head_stride = 128
+    a.start, a.inv_freq = FAKE + (4 << 32), FAKE + (5 << 32)
+    a.cache = cache(b)
+    return put(a, **kw)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(B=0), BAD_SHAPE), (dict(T=-1), BAD_SHAPE), (dict(Hkv=0), BAD_SHAPE), (dict(d=96), BAD_SHAPE),
+    (dict(act_dtype=2), BAD_DTYPE), (dict(act_dtype=0), BAD_DTYPE), (dict(cache__dtype=5), BAD_DTYPE),
+    (dict(cache__dtype=0), BAD_DTYPE), (dict(flags=2), UNSUPPORTED), (dict(rot=24), BAD_SHAPE),
+    (dict(rot=144), BAD_SHAPE), (dict(rot=-16), BAD_SHAPE), (dict(rot=0), NULL_PTR),
+    (dict(inv_freq=None), NULL_PTR), (dict(q_out=None), NULL_PTR), (dict(q=None), NULL_PTR),
+    (dict(k=None), NULL_PTR), (dict(v=None), NULL_PTR), (dict(start=None), NULL_PTR),
+    (dict(Hq=0), BAD_SHAPE), (dict(cache__k=None), NULL_PTR), (dict(cache__block_table=None), NULL_PTR),
+    (dict(cache__num_pages=0), BAD_SHAPE), (dict(cache__page_size=0), BAD_SHAPE),
+    (dict(cache__max_pages=0), BAD_SHAPE), (dict(cache__k_token_stride=-128), BAD_SHAPE),
+    (dict(cache__v_page_stride=4100), BAD_SHAPE), (dict(cache__k=FAKE + 8), BAD_SHAPE),
+    (dict(cache__k_scale=FAKE), UNSUPPORTED), (dict(cache__table_stride=-1), BAD_SHAPE),
+    (dict(k_token_stride=257), BAD_SHAPE), (dict(q_head_stride=-8), BAD_SHAPE),
+    (dict(v=FAKE + (2 << 32) + 2), BAD_SHAPE), (dict(cu_seqlens=FAKE + (6 << 32), N=3), BAD_SHAPE),
+    (dict(B=1, cu_seqlens=FAKE + (6 << 32), N=0), BAD_SHAPE), (dict(B=1 << 20, T=1 << 20), BAD_SHAPE),
+    (dict(q_out=FAKE + (1 << 32)), ALIAS), (dict(cache__k=FAKE + (1 << 32)), ALIAS),
+    (dict(cache__v=FAKE + (4 << 32)), ALIAS), (dict(cache__v=FAKE + (3 << 32)), ALIAS),
+    (dict(q_out=FAKE, q_token_stride=1024), ALIAS), (dict(start=FAKE + (3 << 32) + 64), ALIAS),
+])
+def test_append_refusals(b, change, status):
+    rc, msg = call(b, "kv_append", append_args(b, **change))
+    assert rc == status and msg, (rc, msg)
+
+
+def test_append_null_args(b):
+    assert b.lib().kda_kv_append(None, None) == NULL_PTR
+
+
+def test_append_of_no_tokens_is_a_no_op(b):
+    a = append_args(b, T=0, q=None, k=None, v=None, q_out=None)
+    assert call(b, "kv_append", a)[0] == 0
+
+
+def decode_args(b, **kw):
+    a = b.PagedDecodeArgs()
+    a.N, a.m, a.Hq, a.Hkv, a.d, a.act_dtype, a.out_dtype = 4, 2, 8, 2, 128, 1, 0
+    a.q, a.q_token_stride, a.q_head_stride = FAKE, 8 * 128, 128
+    a.cache = cache(b)
+    a.seq_lens, a.max_len, a.scale = FAKE + (1 << 32), 320, 0.1
+    a.o, a.workspace, a.workspace_bytes = FAKE + (2 << 32), FAKE + (3 << 32), 0
+    return put(a, **kw)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(N=0), BAD_SHAPE), (dict(m=0), BAD_SHAPE), (dict(Hq=7), BAD_SHAPE), (dict(Hkv=0), BAD_SHAPE),
+    (dict(d=256), BAD_SHAPE), (dict(act_dtype=0), BAD_DTYPE), (dict(out_dtype=2), BAD_DTYPE),
+    (dict(cache__dtype=0), BAD_DTYPE), (dict(flags=1), UNSUPPORTED), (dict(max_len=0), BAD_SHAPE),
+    (dict(max_len=321), BAD_SHAPE), (dict(window=-1), BAD_SHAPE), (dict(m=1 << 22), BAD_SHAPE),
+    (dict(N=1 << 24), BAD_SHAPE), (dict(q=None), NULL_PTR), (dict(seq_lens=None), NULL_PTR),
+    (dict(o=None), NULL_PTR), (dict(scale=float("nan")), BAD_SHAPE), (dict(scale=float("inf")), BAD_SHAPE),
+    (dict(cache__v=None), NULL_PTR), (dict(cache__v_scale=FAKE), UNSUPPORTED),
+    (dict(q_token_stride=-8), BAD_SHAPE), (dict(q_head_stride=129), BAD_SHAPE),
+    (dict(o=FAKE + (2 << 32) + 4), BAD_SHAPE), (dict(o=FAKE), ALIAS),
+    (dict(o=FAKE + (8 << 32)), ALIAS), (dict(lse=FAKE + (2 << 32)), ALIAS),
+    (dict(lse=FAKE + (1 << 32)), ALIAS),
+])
+def test_decode_refusals(b, change, status):
+    rc, msg = call(b, "paged_decode", decode_args(b, **change))
+    assert rc == status and msg, (rc, msg)
+
+
+def test_decode_workspace(b):
+    q = lambda a: b.lib().kda_paged_decode_workspace_bytes(ctypes.byref(a))  # noqa: E731
+    assert q(decode_args(b, d=96)) == b.SIZE_MAX and b.lib().kda_paged_decode_workspace_bytes(None) == b.SIZE_MAX
+    long = dict(cache__max_pages=10000, max_len=160000)
+    need = q(decode_args(b, **long))
+    assert 0 < need < 64 << 20
+    # a bound on the lengths or a window that one workgroup covers needs no workspace
+    assert q(decode_args(b, **long, window=100)) == 0
+    assert q(decode_args(b, max_len=128)) == 0
+    for change, status in ((dict(workspace_bytes=need - 1), WORKSPACE),
+                           (dict(workspace_bytes=need, workspace=None), WORKSPACE),
+                           (dict(workspace_bytes=need, workspace=FAKE + (3 << 32) + 16), WORKSPACE),
+                           (dict(workspace_bytes=need, workspace=FAKE + (2 << 32)), ALIAS),
+                           (dict(workspace_bytes=need, workspace=FAKE + (8 << 32)), ALIAS)):
+        assert call(b, "paged_decode", decode_args(b, **long, **change))[0] == status
+
+
+def verify_args(b, **kw):
+    a = b.VerifyArgs()
+    a.N, a.m, a.V, a.dtype = 4, 3, 1000, 0
+    a.p, a.q = FAKE, FAKE + (1 << 32)
+    a.p_seq_stride, a.p_row_stride, a.q_seq_stride, a.q_row_stride = 4000, 1000, 3000, 1000
+    a.drafts, a.uniform = FAKE + (2 << 32), FAKE + (3 << 32)
+    a.accept, a.tokens = FAKE + (4 << 32), FAKE + (5 << 32)
+    a.workspace, a.workspace_bytes = FAKE + (6 << 32), 1 << 20
+    return put(a, **kw)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(N=0), BAD_SHAPE), (dict(m=0), BAD_SHAPE), (dict(V=0), BAD_SHAPE), (dict(V=2 ** 31 - 1), BAD_SHAPE),
+    (dict(N=1 << 30, V=1 << 20), BAD_SHAPE), (dict(dtype=2), BAD_DTYPE), (dict(p=None), NULL_PTR),
+    (dict(drafts=None), NULL_PTR), (dict(uniform=None), NULL_PTR), (dict(accept=None), NULL_PTR),
+    (dict(tokens=None), NULL_PTR), (dict(p_row_stride=-1), BAD_SHAPE), (dict(q_seq_stride=-1), BAD_SHAPE),
+    (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=1), WORKSPACE),
+    (dict(workspace=FAKE + (6 << 32) + 8), WORKSPACE), (dict(accept=FAKE + (2 << 32)), ALIAS),
+    (dict(tokens=FAKE + (3 << 32) + 4), ALIAS), (dict(workspace=FAKE), ALIAS),
+    (dict(tokens=FAKE + (4 << 32)), ALIAS), (dict(n_drafts=FAKE + (4 << 32)), ALIAS),
+])
+def test_verify_refusals(b, change, status):
+    rc, msg = call(b, "verify_drafts", verify_args(b, **change))
+    assert rc == status and msg, (rc, msg)
+
+
+def test_verify_workspace(b):
+    q = lambda a: b.lib().kda_verify_drafts_workspace_bytes(ctypes.byref(a))  # noqa: E731
+    assert 0 < q(verify_args(b)) < 1 << 20
+    assert q(verify_args(b, V=0)) == b.SIZE_MAX
+    assert b.lib().kda_verify_drafts_workspace_bytes(None) == b.SIZE_MAX
+    assert b.lib().kda_paged_decode(None, None) == NULL_PTR
+    assert b.lib().kda_verify_drafts(None, None) == NULL_PTR
+
+
+def test_page_division(b):
+    """token / page_size by one multiplication (the numbers that kda_api.cpp hands the kernels)."""
+    rng = np.random.default_rng(1)
+    for ps in [1, 2, 3, 5, 7, 16, 20, 48, 100, 255, 1000, 4097, 2 ** 20 + 7, 2 ** 30, 2 ** 31 - 1]:
+        up = (ps - 1).bit_length()
+        mul = (1 << (31 + up)) // ps + 1
+        assert mul < 1 << 32
+        n = [0, 1, ps - 1, min(ps, 2 ** 31 - 1), 2 ** 31 - 1, 2 ** 31 - 2] + [int(x) for x in rng.integers(0, 2 ** 31, 2000)]
+        n += [min(2 ** 31 - 1, max(0, k * ps + e)) for k in rng.integers(0, 2 ** 31 // ps + 1, 500).tolist() for e in (-1, 0)]
+        assert all((x * mul) >> (31 + up) == x // ps for x in n), ps
+
+
+def test_binding_checks_tensors_first(b):
+    """Tensors on the CPU, wrong types and shapes raise before the library is called."""
+    import torch
+    z = torch.zeros
+    i32 = dict(dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        b.kv_append(z(1, 1, 1, 32), z(1, 1, 1, 32), z(1, 16, 1, 32), z(1, 16, 1, 32), z(1, 1, **i32), z(1, **i32))
+    with pytest.raises(ValueError, match="GPU"):
+        b.paged_decode(z(1, 1, 1, 32), z(1, 16, 1, 32), z(1, 16, 1, 32), z(1, 1, **i32), z(1, **i32))
+    with pytest.raises(ValueError, match="GPU"):
+        b.verify_drafts(z(1, 2, 5), z(1, 1, 5), z(1, 1, **i32), z(1, 2))
+    with pytest.raises(TypeError, match="int32"):
+        b._page_cache(z(1, 16, 1, 32), z(1, 16, 1, 32), z(1, 1), None, None, 1, 1, 32)
+    with pytest.raises(ValueError, match="evenly"):
+        b._heads("k", z(4, 5, 2, 32)[:, :3], torch.float32, (4, 3), 32)
+    assert b._heads("k", z(4, 3, 6, 32)[:, :, 2:4], torch.float32, (4, 3), 32) == (192, 32)
+    assert b._heads("k", z(4, 1, 6, 32)[:, :, 2:4], torch.float32, (4, 1), 32) == (192, 32)
+    assert b._heads("k", z(1, 1, 1, 32), torch.float32, (1, 1), 32) == (32, 32)
+
+
+def test_reference_attention_worked_example():
+    """Two tokens with scores log 1 and log 3: weights 1/4 and 3/4; nothing seen gives 0."""
+    q = np.zeros((1, 2, 1, 2))
+    q[..., 0] = 1.0
+    k = [np.array([[[0.0, 5.0]], [[np.log(3.0), -2.0]]])]
+    v = [np.array([[[8.0, 0.0]], [[0.0, 4.0]]])]
+    o, lse = paged_ref.attend(q, k, v, [np.ones(2, bool)], [2], 1.0, 0)
+    assert np.allclose(o[0, 1, 0], [2.0, 3.0]) and np.isclose(lse[0, 1, 0], np.log(4.0))
+    assert np.allclose(o[0, 0, 0], [8.0, 0.0])
+    o, lse = paged_ref.attend(q, k, v, [np.ones(2, bool)], [2], 1.0, 1)
+    assert np.allclose(o[0, 1, 0], [0.0, 4.0])
+    o, lse = paged_ref.attend(q, k, v, [np.ones(2, bool)], [1], 1.0, 0)
+    assert (o[0, 0] == 0).all() and np.isneginf(lse[0, 0]).all()
+
+
+def test_reference_rotation_worked_example():
+    x = np.array([[1.0, 2.0, 3.0, 4.0]])
+    f = np.array([np.pi / 2], np.float64)
+    assert np.allclose(paged_ref.rotate(x, 1, f, True), [[-2.0, 1.0, 3.0, 4.0]])
+    f2 = np.array([np.pi / 2, np.pi])
+    assert np.allclose(paged_ref.rotate(x, 1, f2, False), [[-3.0, -2.0, 1.0, -4.0]])
+
+
+def test_reference_verification_worked_example():
+    """p = (.5, .25, .25), q = (.25, .75, 0): draft 1 stands below a third, else the following token
+    comes from max(p - q, 0) = (.25, 0, .25)."""
+    p = np.array([[[0.5, 0.25, 0.25], [0.2, 0.2, 0.6]]])
+    q = np.array([[[0.25, 0.75, 0.0]]])
+    x = np.array([[1]], np.int32)
+    a, t = paged_ref.verify(p, q, x, np.array([[0.3, 0.3]], np.float32), [1])
+    assert a[0] == 1 and list(t[0]) == [1, 1]
+    a, t = paged_ref.verify(p, q, x, np.array([[0.4, 0.4]], np.float32), [1])
+    assert a[0] == 0 and list(t[0]) == [0, -1]
+    a, t = paged_ref.verify(p, q, x, np.array([[0.4, 0.6]], np.float32), [1])
+    assert a[0] == 0 and list(t[0]) == [2, -1]
+    a, t = paged_ref.verify(p, None, x, np.array([[0.4, 0.9]], np.float32), [1])
+    assert a[0] == 0 and list(t[0]) == [2, -1]
