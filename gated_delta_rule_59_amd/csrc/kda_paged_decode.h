@@ -131,20 +131,27 @@ __device__ __forceinline__ bf16x8 e4m3_operand(uint32_t w0, uint32_t w1) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// Channel x of one cached value row, as a float.
-template <int CT>
-__device__ __forceinline__ float cache_value(const char* row, int x) {
-  if constexpr (CT == kF32) return reinterpret_cast<const float*>(row)[x];
-  if constexpr (CT == kBF16) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[x]);
+// The VEC channels of a lane's words of a value row, as floats.
+template <int CT, int VEC>
+__device__ __forceinline__ float word_value(const uint32_t* w, int x) {
+  if constexpr (CT == kF32) return __uint_as_float(w[x]);
+  if constexpr (CT == kBF16) return __uint_as_float(x & 1 ? w[x / 2] & 0xffff0000u : w[x / 2] << 16);
   if constexpr (CT == kF8) {
-    const uint32_t w = reinterpret_cast<const uint8_t*>(row)[x];
-    return e4m3_pair<false>(w).x;
+    const floatx2 v = x & 2 ? e4m3_pair<true>(w[x / 4]) : e4m3_pair<false>(w[x / 4]);
+    return x & 1 ? v.y : v.x;
   }
+}
+template <int VB>
+__device__ __forceinline__ void load_bytes(const char* p, uint32_t* w) {
+  if constexpr (VB == 2)
+    w[0] = *reinterpret_cast<const uint16_t*>(p);
+  else
+    load_words<VB / 4>(p, w);
 }
 
 // P16: page_size is a multiple of 16, so 16 aligned tokens have one page.
 template <int CT, int D, int NT, bool P16>
-__global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void paged_decode_kernel(
+__global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     const PagedDecodePlan p, const int32_t* __restrict__ block_table) {
   using TY = Types<CT, D>;
   constexpr int VEC = TY::VEC;
@@ -210,7 +217,6 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void paged_decode_kernel(
   }
 
   const float log2_scale = p.scale * kLog2e;
-  const int es_ps = p.c.page_size;
 
   // ---- one (row block, head) of one sequence after the other
   while (left > 0) {
@@ -284,93 +290,72 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void paged_decode_kernel(
     const char* vh = p.c.v + h * p.c.v_head;
     const int last = any_hi - 1;  // the newest token that some row sees (>= 0 if i0 < i1)
 
-    // where a tile's rows lie; tokens past `last` take its place (they are masked below)
-    struct Where {
-      int64_t k[2], v[8];  // byte offsets (P16: of 16 tokens' page; v[0], v[1])
-      uint32_t have;       // bit i: token slot i of this lane lies on a page
-    };
-    auto page_of = [&](int tok) { return pages[div_page(p.c, (unsigned)tok)]; };
-    auto locate = [&](int tb, int pg0, int pg1) {
-      Where w;
-      if constexpr (P16) {
-        w.have = 0;
+    // Where a tile's rows lie. Tokens past `last` give their place to it or to a slot of its page,
+    // and ids of no page to page 0; what they read is masked below.
+    // P16: 16 tokens have one page, so the rows' base is uniform and a lane adds 32 bits to it.
+    constexpr int IDS = P16 ? 2 : 10;  // page ids: of the two halves, or of the lane's 2 + 8 rows
+    const unsigned k_lane = (unsigned)(r * (int)p.c.k_token) + g * 4 * TY::KC;
+    const unsigned v_lane = (unsigned)(4 * g * (int)p.c.v_token) + r * TY::VB;
+    // token of key row s (s = 0, 1), and of value row i (i = 0 .. 7)
+    auto k_token = [&](int tb, int s) { return min(tb + 16 * s + (P16 ? 0 : r), P16 ? last & ~15 : last); };
+    auto v_token = [&](int tb, int i) { return min(tb + 16 * (i >> 2) + 4 * g + (i & 3), last); };
+    auto page_at = [&](int tok) { return pages[div_page(p.c, (unsigned)tok)]; };
+    auto is_page = [&](int id) { return (unsigned)id < (unsigned)p.c.num_pages; };
+    auto look_up = [&](int tb, int* id) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          int pg = s ? pg1 : pg0;
-          const int tok = min(tb + 16 * s, last & ~15);
-          const bool in = (unsigned)pg < (unsigned)p.c.num_pages;
-          w.have |= in ? 0xfu << (4 * s) : 0u;
-          pg = in ? pg : 0;
-          const int slot = tok - div_page(p.c, (unsigned)tok) * es_ps;
-          w.k[s] = pg * p.c.k_page + slot * p.c.k_token;
-          w.v[s] = pg * p.c.v_page + slot * p.c.v_token;
-        }
-      } else {
-        w.have = 0;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int tok = min(tb + 16 * s + r, last), pi = div_page(p.c, (unsigned)tok);
-          const int pg = pages[pi];
-          const bool in = (unsigned)pg < (unsigned)p.c.num_pages;
-          w.k[s] = (in ? pg : 0) * p.c.k_page + (tok - pi * es_ps) * p.c.k_token;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tok = min(tb + 4 * g + (i & 3) + 16 * (i >> 2), last);
-          const int pi = div_page(p.c, (unsigned)tok);
-          const int pg = pages[pi];
-          const bool in = (unsigned)pg < (unsigned)p.c.num_pages;
-          w.have |= in ? 1u << i : 0u;
-          w.v[i] = (in ? pg : 0) * p.c.v_page + (tok - pi * es_ps) * p.c.v_token;
-        }
+      for (int s = 0; s < 2; ++s) {
+        id[s] = page_at(k_token(tb, s));
+        if (P16) id[s] = __builtin_amdgcn_readfirstlane(id[s]);
       }
-      return w;
+      if constexpr (!P16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) id[2 + i] = page_at(v_token(tb, i));
+      }
     };
-    auto tile_page = [&](int tb, int s) {  // P16: page id of 16 tokens
-      return __builtin_amdgcn_readfirstlane(page_of(min(tb + 16 * s, last)));
+    auto row_at = [&](int id, int tok, int64_t page, int64_t token) {
+      const int slot = tok - div_page(p.c, (unsigned)tok) * p.c.page_size;
+      return (is_page(id) ? id : 0) * page + slot * token;
     };
 
     uint32_t kw[2][TY::KW], vw[8][TY::VW];
-    auto load_k = [&](const Where& w) {
+    auto load_k = [&](int tb, const int* id) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const char* row = kh + w.k[s] + (P16 ? (int64_t)r * p.c.k_token : 0);
+        const char* row = kh + row_at(id[s], k_token(tb, s), p.c.k_page, p.c.k_token);
+        const unsigned off = P16 ? k_lane : g * 4 * TY::KC;
 #pragma unroll
         for (int c = 0; c < TY::NKL; ++c)
-          load_words<TY::KC>(row + c * 16 * TY::KC + g * 4 * TY::KC, &kw[s][c * TY::KC]);
+          load_words<TY::KC>(row + off + c * 16 * TY::KC, &kw[s][c * TY::KC]);
       }
     };
-    auto load_v = [&](const Where& w) {
+    auto load_v = [&](int tb, const int* id) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const char* row = P16 ? vh + w.v[i >> 2] + (int64_t)(4 * g + (i & 3)) * p.c.v_token
-                              : vh + w.v[i];
-        if constexpr (TY::VB == 2)
-          vw[i][0] = *reinterpret_cast<const uint16_t*>(row + r * TY::VB);
+        const char* row;
+        if constexpr (P16)
+          row = vh + row_at(id[i >> 2], k_token(tb, i >> 2), p.c.v_page, p.c.v_token) +
+                (i & 3) * p.c.v_token + v_lane;
         else
-          load_words<TY::VW>(row + r * TY::VB, vw[i]);
+          row = vh + row_at(id[2 + i], v_token(tb, i), p.c.v_page, p.c.v_token) + r * TY::VB;
+        load_bytes<TY::VB>(row, vw[i]);
       }
     };
 
-    Where cur{}, nxt{};
-    int pg0 = 0, pg1 = 0;
+    int ids[IDS], ids1[IDS], ids2[P16 ? IDS : 1];  // of this tile, the next, the one after
     if (i0 < i1) {
-      if constexpr (P16) {
-        pg0 = tile_page(base + kUnit * i0, 0);
-        pg1 = tile_page(base + kUnit * i0, 1);
-      }
-      cur = locate(base + kUnit * i0, pg0, pg1);
-      load_k(cur);
-      if constexpr (P16) {
-        if (i0 + 1 < i1) {
-          pg0 = tile_page(base + kUnit * (i0 + 1), 0);
-          pg1 = tile_page(base + kUnit * (i0 + 1), 1);
-        }
-      }
+      look_up(base + kUnit * i0, ids1);
+      load_k(base + kUnit * i0, ids1);
+      if constexpr (P16) look_up(base + kUnit * (i0 + 1), ids2);
     }
     for (int i = i0; i < i1; ++i) {
       const int tb = base + kUnit * i;
-      load_v(cur);
+#pragma unroll
+      for (int x = 0; x < IDS; ++x) {
+        ids[x] = ids1[x];
+        if constexpr (P16) ids1[x] = ids2[x];
+      }
+      load_v(tb, ids);
+      if constexpr (!P16) look_up(tb + kUnit, ids1);
 
       // S^T = K Q^T
       floatx4 s[NT][2];
@@ -405,42 +390,44 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void paged_decode_kernel(
           }
       }
 
-      // the next tile's keys, and the page ids of the one after
-      if (i + 1 < i1) {
-        nxt = locate(tb + kUnit, pg0, pg1);
-        load_k(nxt);
-        if constexpr (P16) {
-          if (i + 2 < i1) {
-            pg0 = tile_page(tb + 2 * kUnit, 0);
-            pg1 = tile_page(tb + 2 * kUnit, 1);
-          }
-        }
-      }
+      // the next tile's keys, and the page ids of the one after. Past the last tile too (the
+      // newest row once more): behind a branch, the wait for V would wait for these as well.
+      load_k(tb + kUnit, ids1);
+      if constexpr (P16) look_up(tb + 2 * kUnit, ids2);
 
       // tokens that not every row sees, or that are on no page
-      const bool plain = tb >= all_lo && tb + 32 <= all_hi && __all(cur.have == 0xffu);
-      if (plain) {
+      bool on_pages = true;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int x = P16 ? 0 : 2; x < IDS; ++x) on_pages = on_pages && is_page(ids[x]);
+      const bool plain = tb >= all_lo && tb + 32 <= all_hi && (P16 ? on_pages : __all(on_pages));
+      // Bit i of `sees` / `shared`: this lane's row / every row sees token slot i. Applied in
+      // every tile: a branch around them would make copies of the values, which waits for them.
+      unsigned sees[NT], shared = 0xffu;
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+      for (int nt = 0; nt < NT; ++nt) sees[nt] = 0xffu;
+      if (!plain) {
+        shared = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][u][e] *= CT == kF32 ? 1.f : to_log2;
-      } else {
+        for (int nt = 0; nt < NT; ++nt) sees[nt] = 0;
 #pragma unroll
         for (int i8 = 0; i8 < 8; ++i8) {
           const int tok = tb + 4 * g + (i8 & 3) + 16 * (i8 >> 2);
-          const bool in = (cur.have >> i8) & 1;
+          const bool in = is_page(ids[P16 ? i8 >> 2 : 2 + i8]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const bool sees = in && tok >= lo[nt] && tok < hi[nt];
-            s[nt][i8 >> 2][i8 & 3] =
-                sees ? s[nt][i8 >> 2][i8 & 3] * (CT == kF32 ? 1.f : to_log2) : -INFINITY;
-          }
-          const bool shared = in && tok >= all_lo && tok < all_hi;
-#pragma unroll
-          for (int e = 0; e < TY::VW; ++e) vw[i8][e] = shared ? vw[i8][e] : 0u;
+          for (int nt = 0; nt < NT; ++nt)
+            sees[nt] |= in && tok >= lo[nt] && tok < hi[nt] ? 1u << i8 : 0u;
+          shared |= in && tok >= all_lo && tok < all_hi ? 1u << i8 : 0u;
         }
+      }
+#pragma unroll
+      for (int i8 = 0; i8 < 8; ++i8) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          s[nt][i8 >> 2][i8 & 3] = sees[nt] >> i8 & 1 ? s[nt][i8 >> 2][i8 & 3] * (CT == kF32 ? 1.f : to_log2)
+                                                      : -INFINITY;
+        const uint32_t keep = 0u - (shared >> i8 & 1);
+#pragma unroll
+        for (int e = 0; e < TY::VW; ++e) vw[i8][e] &= keep;
       }
 
       // running maximum and sum of each row
@@ -535,27 +522,25 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void paged_decode_kernel(
           const int pi = div_page(p.c, (unsigned)tok);
           const int pg = pages[pi];
           if ((unsigned)pg >= (unsigned)p.c.num_pages) continue;
-          const char* row = vh + pg * p.c.v_page + (tok - pi * es_ps) * p.c.v_token;
-          float w[NT];
-          bool sees[NT];
+          const char* row = vh + pg * p.c.v_page + (tok - pi * p.c.page_size) * p.c.v_token;
+          uint32_t x[4][TY::VW];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) load_bytes<TY::VB>(row + (4 * g + e) * TY::VB, x[e]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            w[nt] = ps[(tok - tb) * COLS + nt * 16 + r];
-            sees[nt] = tok >= lo[nt] && tok < hi[nt];
+            const float w = ps[(tok - tb) * COLS + nt * 16 + r];
+            const bool mine = tok >= lo[nt] && tok < hi[nt];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float y = fmaf(w, word_value<CT, VEC>(x[e], j), acc[nt][j][e]);
+                acc[nt][j][e] = mine ? y : acc[nt][j][e];
+              }
           }
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = cache_value<CT>(row, VEC * (4 * g + e) + j);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                acc[nt][j][e] = sees[nt] ? fmaf(w[nt], x, acc[nt][j][e]) : acc[nt][j][e];
-            }
         }
         __builtin_amdgcn_wave_barrier();
       }
-      cur = nxt;
     }
 
     // ---- the four waves' parts of each row become one
@@ -697,7 +682,8 @@ template <int CT, int D>
 hipError_t launch_d(const PagedDecodePlan& p, hipStream_t stream) {
   const int64_t all = (int64_t)p.N * p.row_blocks * p.Hkv;
   const dim3 grid((unsigned)(p.split ? p.split : all));
-  const bool p16 = p.c.page_size % 16 == 0;
+  // one page per 16 aligned tokens, whose rows lie within 32 bits of each other
+  const bool p16 = p.c.page_size % 16 == 0 && p.c.k_token < (1 << 26) && p.c.v_token < (1 << 26);
   auto kern = p.tiles == 1 ? (p16 ? paged_decode_kernel<CT, D, 1, true> : paged_decode_kernel<CT, D, 1, false>)
                            : (p16 ? paged_decode_kernel<CT, D, 2, true> : paged_decode_kernel<CT, D, 2, false>);
   hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, p, p.c.table);

@@ -9,7 +9,7 @@ namespace kda {
 namespace {
 // Workgroups that share the work evenly: those that the 256 CUs hold at once (three each with
 // one row tile, two with two).
-constexpr int kShared1 = 256 * 3, kShared2 = 256 * 2;
+constexpr int kShared1 = 256 * 2, kShared2 = 256 * 2;
 // Up to this many units of 128 tokens a (sequence, row block, head) is done by one workgroup.
 constexpr int64_t kAlone = 4;
 }  // namespace
