@@ -315,6 +315,7 @@ kda::PageCache page_cache(const kda_page_cache& c) {
   r.ps_mul = (unsigned)((uint64_t(1) << r.ps_shift) / (uint64_t)c.page_size + 1);
   r.k_page = c.k_page_stride * es, r.k_token = c.k_token_stride * es, r.k_head = c.k_head_stride * es;
   r.v_page = c.v_page_stride * es, r.v_token = c.v_token_stride * es, r.v_head = c.v_head_stride * es;
+  r.k_page16 = (unsigned)(r.k_page / 16), r.v_page16 = (unsigned)(r.v_page / 16);
   r.table = c.block_table;
   r.table_stride = c.table_stride;
   r.max_pages = c.max_pages;
@@ -635,8 +636,7 @@ kda_status kda_paged_decode(const kda_paged_decode_args* a, void* hip_stream) {
   p.scale = a->scale;
   p.o = a->o;
   p.lse = a->lse;
-  p.part_o = static_cast<float*>(a->workspace);
-  p.part_ml = p.part_o + (size_t)p.split * 2 * 16 * p.tiles * a->d;
+  kda::paged_decode_workspace(&p, a->workspace);
   const hipError_t e = kda::launch_paged_decode(p, static_cast<hipStream_t>(hip_stream));
   if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_paged_decode launch: %s", hipGetErrorString(e));
   return ok();

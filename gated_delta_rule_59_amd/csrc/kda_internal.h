@@ -70,6 +70,7 @@ struct PageCache {
   unsigned ps_mul;  // token / page_size = (token * ps_mul) >> ps_shift for 0 <= token < 2^31
   int ps_shift;
   int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+  unsigned k_page16, v_page16;  // page strides in 16 bytes (where they fit)
   const int32_t* table;
   int64_t table_stride;
   int max_pages;
@@ -105,11 +106,18 @@ struct PagedDecodePlan {
   float scale;
   void* o;
   float* lse;
-  int split;                     // workgroups that share all work evenly; 0: one per (n, rows, head)
-  float *part_o, *part_ml;       // workspace: partial results of shared (n, rows, head)s
+  int heads;                     // neighbouring key/value heads a workgroup carries: 1, 2 or 4
+  int split;                     // workgroups that share all work evenly; 0: one per (n, row
+                                 // block, head group)
+  int part_rows;                 // rows of a part
+  float *part_o, *part_ml;       // workspace: parts of shared groups, [split][2][heads][part_rows]
+                                 // of d values, and of (maximum, sum)
+  int* part_of;                  // [n][row block][head group]: first and last workgroup
 };
-// Fills in the launch shape (tiles, row_blocks, split) and returns the workspace bytes.
+// Fills in the launch shape (tiles to part_rows) and returns the workspace bytes; and the
+// workspace's arrays.
 size_t plan_paged_decode(PagedDecodePlan* p);
+void paged_decode_workspace(PagedDecodePlan* p, void* workspace);
 hipError_t launch_paged_decode(const PagedDecodePlan& p, hipStream_t stream);
 
 struct VerifyPlan {

@@ -31,6 +31,9 @@
 
 #include <math.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "kda_device.h"
 #include "kda_internal.h"
 #include "kda_paged.h"
@@ -38,8 +41,16 @@
 namespace kda {
 namespace paged {
 
-constexpr int kUnit = 128;  // tokens a workgroup takes at a time: 32 by each of four waves
-
+// Work is counted in units: a workgroup's four waves carry p.heads (1, 2 or 4) neighbouring
+// key/value heads, 4 / p.heads waves each, and take 32 tokens per wave at a time, so a unit is
+// 128 / p.heads tokens of p.heads heads. The heads of a token lie side by side in a cache with the
+// token outermost, and reading 1 KiB of each token at a time runs nearer to what HBM delivers than
+// 256 B (4 contexts of 65k tokens, 8 heads: 222 us with one head per workgroup, 188 with four).
+//
+// Workgroups with the same number of waves per head share (sequence, row block, head group)s
+// evenly: workgroup w takes units [start(w), start(w + 1)) of all, in order. Where it begins or ends
+// inside a group it leaves a part in the workspace.
+__device__ __forceinline__ int unit_tokens(const PagedDecodePlan& p) { return 128 / p.heads; }
 // The new tokens of sequence n see positions [0, len); with a window, the first of them begins
 // at len - m + 1 - window.
 __device__ __forceinline__ int seq_len(const PagedDecodePlan& p, int n) {
@@ -48,36 +59,12 @@ __device__ __forceinline__ int seq_len(const PagedDecodePlan& p, int n) {
 __device__ __forceinline__ int first_unit(const PagedDecodePlan& p, int len) {
   if (!p.window) return 0;
   const int64_t lo = (int64_t)len - p.m + 1 - p.window;
-  return lo > 0 ? (int)(lo / kUnit) : 0;
+  return lo > 0 ? (int)lo / unit_tokens(p) : 0;
 }
-// Units of kUnit tokens that a sequence's workgroups walk; one at least, which writes zeros.
+// Units that a sequence's workgroups walk per group; one at least, which writes zeros.
 __device__ __forceinline__ int seq_units(const PagedDecodePlan& p, int len) {
-  return max(1, (len + kUnit - 1) / kUnit - first_unit(p, len));
-}
-
-// Sum over the workgroup's 256 threads (every thread gets it).
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* s4) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s4[threadIdx.x >> 6] = x;
-  __syncthreads();
-  return s4[0] + s4[1] + s4[2] + s4[3];
-}
-
-// How the units of all (sequence, row block, head)s are shared: workgroup w of `gd` takes units
-// [start(w), start(w + 1)) of the total.
-struct Share {
-  int64_t total;
-  int gd;
-  __device__ __forceinline__ int64_t start(int64_t w) const { return total * w / gd; }
-  // the workgroup that has unit u
-  __device__ __forceinline__ int owner(int64_t u) const {
-    return (int)(((u + 1) * gd + total - 1) / total) - 1;
-  }
-};
-__device__ __forceinline__ Share make_share(const PagedDecodePlan& p, int64_t total) {
-  return Share{total, (int)(total < p.split ? total : (int64_t)p.split)};
+  const int u = unit_tokens(p);
+  return max(1, (len + u - 1) / u - first_unit(p, len));
 }
 
 template <int CT, int D>
@@ -92,17 +79,19 @@ struct Types {
   static constexpr int QW = CT == kF32 ? D / 4 : D / 8;  // words of a query row per lane
 };
 
+// Streamed: each cached value is read once (4 contexts of 65k tokens: 222 -> 213 us; a plain read
+// of 4 GiB runs at 7.1 TB/s with such loads, at 6.2 without).
 template <int W>
 __device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
   if constexpr (W == 1) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
+    w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
   } else if constexpr (W == 2) {
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     w[0] = x[0]; w[1] = x[1];
   } else {
 #pragma unroll
     for (int c = 0; c < W; c += 4) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(p + 4 * c);
+      const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 4 * c));
       w[c] = x[0]; w[c + 1] = x[1]; w[c + 2] = x[2]; w[c + 3] = x[3];
     }
   }
@@ -149,6 +138,24 @@ __device__ __forceinline__ void load_bytes(const char* p, uint32_t* w) {
     load_words<VB / 4>(p, w);
 }
 
+// Four channels (d ..) of a finished row: o and l are sums of e^{s - now}-weighted values.
+template <int D>
+__device__ __forceinline__ void write_row(const PagedDecodePlan& p, int n, int h, int row, int d,
+                                          float now, float l, floatx4 o) {
+  const int j = row / p.group, head = h * p.group + row % p.group;
+  const int64_t dst = ((int64_t)n * p.m + j) * p.Hq + head;
+  const float inv = (p.c.v_scale ? p.c.v_scale[h] : 1.f) / l;
+  if (l == 0.f) o = floatx4{0.f, 0.f, 0.f, 0.f};  // nothing was seen
+  else o = floatx4{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+  if (p.out_bf16)
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.o) + dst * D + d) =
+        u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+  else
+    *reinterpret_cast<floatx4*>(static_cast<float*>(p.o) + dst * D + d) = o;
+  if (p.lse && d == 0)
+    p.lse[dst] = l == 0.f ? -INFINITY : (now + log2f(l)) * 0.6931471805599453f;
+}
+
 // P16: page_size is a multiple of 16, so 16 aligned tokens have one page.
 template <int CT, int D, int NT, bool P16>
 __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
@@ -165,7 +172,10 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
 
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int per_seq = p.row_blocks * p.Hkv;
+  const int groups = p.Hkv / p.heads, per_seq = p.row_blocks * groups;
+  const int wph = 4 / p.heads;                      // waves per head
+  const int head_at = wv / wph, part_at = wv % wph;  // this wave's head of the group, share of a unit
+  const int unit = unit_tokens(p);
 
   // ---- this workgroup's units
   int n;
@@ -196,10 +206,10 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       if (i < wv) before += s_scan[i];
       total += s_scan[i];
     }
-    const Share share = make_share(p, total);
-    if ((int)blockIdx.x >= share.gd) return;
-    const int64_t u0 = share.start(blockIdx.x);
-    left = share.start(blockIdx.x + 1) - u0;
+    const int64_t share = min(total, (int64_t)p.split);  // workgroups that have any
+    if (blockIdx.x >= share) return;
+    const int64_t u0 = total * blockIdx.x / share;
+    left = total * (blockIdx.x + 1) / share - u0;
     int64_t excl = before + incl - mine;
     if (excl <= u0 && u0 < excl + mine) {
       int i = t * c;
@@ -226,7 +236,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     const int pair = __builtin_amdgcn_readfirstlane((int)(at / un));
     const int u_first = __builtin_amdgcn_readfirstlane((int)(at % un));
     const int cnt = __builtin_amdgcn_readfirstlane((int)min((int64_t)(un - u_first), left));
-    const int rb = pair / p.Hkv, h = pair % p.Hkv;
+    const int rb = pair / groups, h0 = pair % groups * p.heads, h = h0 + head_at;
     const int row0 = rb * COLS;
     const int rows = min(COLS, p.rows - row0);
 
@@ -280,10 +290,10 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       for (int j = 0; j < VEC; ++j) acc[nt][j] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // ---- this wave's tiles: tokens [base + 128 i, + 32), those that some row sees
-    const int base = (first_unit(p, len) + u_first) * kUnit + 32 * wv;
-    int i0 = any_lo > base + 31 ? (any_lo - base - 32) / kUnit + 1 : 0;
-    int i1 = any_hi > base ? min(cnt, (any_hi - base - 1) / kUnit + 1) : 0;
+    // ---- this wave's tiles: tokens [base + unit i, + 32), those that some row sees
+    const int base = (first_unit(p, len) + u_first) * unit + 32 * part_at;
+    const int i0 = any_lo > base + 31 ? (any_lo - base - 32) / unit + 1 : 0;
+    const int i1 = any_hi > base ? min(cnt, (any_hi - base - 1) / unit + 1) : 0;
 
     const int32_t* pages = block_table + n * p.c.table_stride;
     const char* kh = p.c.k + h * p.c.k_head;
@@ -292,70 +302,122 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
 
     // Where a tile's rows lie. Tokens past `last` give their place to it or to a slot of its page,
     // and ids of no page to page 0; what they read is masked below.
-    // P16: 16 tokens have one page, so the rows' base is uniform and a lane adds 32 bits to it.
-    constexpr int IDS = P16 ? 2 : 10;  // page ids: of the two halves, or of the lane's 2 + 8 rows
-    const unsigned k_lane = (unsigned)(r * (int)p.c.k_token) + g * 4 * TY::KC;
-    const unsigned v_lane = (unsigned)(4 * g * (int)p.c.v_token) + r * TY::VB;
-    // token of key row s (s = 0, 1), and of value row i (i = 0 .. 7)
-    auto k_token = [&](int tb, int s) { return min(tb + 16 * s + (P16 ? 0 : r), P16 ? last & ~15 : last); };
-    auto v_token = [&](int tb, int i) { return min(tb + 16 * (i >> 2) + 4 * g + (i & 3), last); };
     auto page_at = [&](int tok) { return pages[div_page(p.c, (unsigned)tok)]; };
     auto is_page = [&](int id) { return (unsigned)id < (unsigned)p.c.num_pages; };
-    auto look_up = [&](int tb, int* id) {
+    // P16: 16 tokens have one page, so the rows' base is uniform and a lane adds 32 bits to it.
+    // Half s of a tile: the page id and the slot of its first token; (page index, slot) of the
+    // tile two ahead, whose ids are being fetched, is carried along without dividing.
+    struct Halves {
+      int id[2], slot[2];
+    };
+    const unsigned k_lane = (unsigned)(r * (int)p.c.k_token) + g * 4 * TY::KC;
+    const unsigned v_lane = (unsigned)(4 * g * (int)p.c.v_token) + r * TY::VB;
+    const int end = last & ~15;  // the newest half
+    const int end_page = div_page(p.c, (unsigned)max(end, 0)), end_slot = end - end_page * p.c.page_size;
+    const int step_pages = div_page(p.c, (unsigned)unit), step_slots = unit - step_pages * p.c.page_size;
+    int ahead[2], ahead_page[2], ahead_slot[2];  // token, page index, slot of the halves looked up next
+    auto look_up = [&]() {
+      Halves x;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        id[s] = page_at(k_token(tb, s));
-        if (P16) id[s] = __builtin_amdgcn_readfirstlane(id[s]);
+        const bool past = ahead[s] > end;
+        x.slot[s] = past ? end_slot : ahead_slot[s];
+        x.id[s] = __builtin_amdgcn_readfirstlane(pages[past ? end_page : ahead_page[s]]);
+        ahead[s] += unit;
+        ahead_page[s] += step_pages;
+        ahead_slot[s] += step_slots;
+        if (ahead_slot[s] >= p.c.page_size) {
+          ahead_slot[s] -= p.c.page_size;
+          ++ahead_page[s];
+        }
       }
-      if constexpr (!P16) {
+      return x;
+    };
+    auto half_at = [&](const Halves& x, int s, unsigned page16, int64_t token) {
+      const unsigned id = is_page(x.id[s]) ? x.id[s] : 0;
+      return (int64_t)(((uint64_t)id * page16) << 4) + (int64_t)x.slot[s] * (int)token;
+    };
+    // else: every row by itself
+    struct Rows {
+      int id[10];  // page ids of the lane's 2 key rows and 8 value rows
+    };
+    auto k_token = [&](int tb, int s) { return min(tb + 16 * s + r, last); };
+    auto v_token = [&](int tb, int i) { return min(tb + 16 * (i >> 2) + 4 * g + (i & 3), last); };
+    auto look_up_rows = [&](int tb) {
+      Rows x;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) id[2 + i] = page_at(v_token(tb, i));
-      }
+      for (int s = 0; s < 2; ++s) x.id[s] = page_at(k_token(tb, s));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x.id[2 + i] = page_at(v_token(tb, i));
+      return x;
     };
     auto row_at = [&](int id, int tok, int64_t page, int64_t token) {
       const int slot = tok - div_page(p.c, (unsigned)tok) * p.c.page_size;
       return (is_page(id) ? id : 0) * page + slot * token;
     };
+    typedef std::conditional_t<P16, Halves, Rows> Ids;
 
     uint32_t kw[2][TY::KW], vw[8][TY::VW];
-    auto load_k = [&](int tb, const int* id) {
+    auto load_k = [&](int tb, const Ids& x) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const char* row = kh + row_at(id[s], k_token(tb, s), p.c.k_page, p.c.k_token);
-        const unsigned off = P16 ? k_lane : g * 4 * TY::KC;
+        const char* row;
+        unsigned off;
+        if constexpr (P16) {
+          row = kh + half_at(x, s, p.c.k_page16, p.c.k_token);
+          off = k_lane;
+          asm volatile("" : "+v"(off));  // keeps base and offset apart: scalar base + 32 bits
+        } else {
+          row = kh + row_at(x.id[s], k_token(tb, s), p.c.k_page, p.c.k_token);
+          off = g * 4 * TY::KC;
+        }
 #pragma unroll
         for (int c = 0; c < TY::NKL; ++c)
           load_words<TY::KC>(row + off + c * 16 * TY::KC, &kw[s][c * TY::KC]);
       }
     };
-    auto load_v = [&](int tb, const int* id) {
+    auto load_v = [&](int tb, const Ids& x) {
+      if constexpr (P16) {
+        unsigned off = v_lane;
+        asm volatile("" : "+v"(off));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const char* row;
-        if constexpr (P16)
-          row = vh + row_at(id[i >> 2], k_token(tb, i >> 2), p.c.v_page, p.c.v_token) +
-                (i & 3) * p.c.v_token + v_lane;
-        else
-          row = vh + row_at(id[2 + i], v_token(tb, i), p.c.v_page, p.c.v_token) + r * TY::VB;
-        load_bytes<TY::VB>(row, vw[i]);
+        for (int s = 0; s < 2; ++s) {
+          const char* row = vh + half_at(x, s, p.c.v_page16, p.c.v_token);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load_bytes<TY::VB>(row + i * p.c.v_token + off, vw[4 * s + i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          load_bytes<TY::VB>(vh + row_at(x.id[2 + i], v_token(tb, i), p.c.v_page, p.c.v_token) + r * TY::VB,
+                             vw[i]);
       }
     };
 
-    int ids[IDS], ids1[IDS], ids2[P16 ? IDS : 1];  // of this tile, the next, the one after
+    Ids now, next, after;  // of this tile, the next, the one after (P16)
     if (i0 < i1) {
-      look_up(base + kUnit * i0, ids1);
-      load_k(base + kUnit * i0, ids1);
-      if constexpr (P16) look_up(base + kUnit * (i0 + 1), ids2);
+      const int tb = base + unit * i0;
+      if constexpr (P16) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          ahead[s] = tb + 16 * s;
+          ahead_page[s] = div_page(p.c, (unsigned)ahead[s]);
+          ahead_slot[s] = ahead[s] - ahead_page[s] * p.c.page_size;
+        }
+        next = look_up();
+        load_k(tb, next);
+        after = look_up();
+      } else {
+        next = look_up_rows(tb);
+        load_k(tb, next);
+      }
     }
     for (int i = i0; i < i1; ++i) {
-      const int tb = base + kUnit * i;
-#pragma unroll
-      for (int x = 0; x < IDS; ++x) {
-        ids[x] = ids1[x];
-        if constexpr (P16) ids1[x] = ids2[x];
-      }
-      load_v(tb, ids);
-      if constexpr (!P16) look_up(tb + kUnit, ids1);
+      const int tb = base + unit * i;
+      now = next;
+      if constexpr (P16) next = after;
+      load_v(tb, now);
+      if constexpr (!P16) next = look_up_rows(tb + unit);
 
       // S^T = K Q^T
       floatx4 s[NT][2];
@@ -392,13 +454,13 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
 
       // the next tile's keys, and the page ids of the one after. Past the last tile too (the
       // newest row once more): behind a branch, the wait for V would wait for these as well.
-      load_k(tb + kUnit, ids1);
-      if constexpr (P16) look_up(tb + 2 * kUnit, ids2);
+      load_k(tb + unit, next);
+      if constexpr (P16) after = look_up();
 
       // tokens that not every row sees, or that are on no page
       bool on_pages = true;
 #pragma unroll
-      for (int x = P16 ? 0 : 2; x < IDS; ++x) on_pages = on_pages && is_page(ids[x]);
+      for (int x = P16 ? 0 : 2; x < (P16 ? 2 : 10); ++x) on_pages = on_pages && is_page(now.id[x]);
       const bool plain = tb >= all_lo && tb + 32 <= all_hi && (P16 ? on_pages : __all(on_pages));
       // Bit i of `sees` / `shared`: this lane's row / every row sees token slot i. Applied in
       // every tile: a branch around them would make copies of the values, which waits for them.
@@ -412,7 +474,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
 #pragma unroll
         for (int i8 = 0; i8 < 8; ++i8) {
           const int tok = tb + 4 * g + (i8 & 3) + 16 * (i8 >> 2);
-          const bool in = is_page(ids[P16 ? i8 >> 2 : 2 + i8]);
+          const bool in = is_page(now.id[P16 ? i8 >> 2 : 2 + i8]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             sees[nt] |= in && tok >= lo[nt] && tok < hi[nt] ? 1u << i8 : 0u;
@@ -437,10 +499,10 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
                          fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-        const float now = fmaxf(top[nt], mx);
-        const float ref = now == -INFINITY ? 0.f : now;
+        const float most = fmaxf(top[nt], mx);
+        const float ref = most == -INFINITY ? 0.f : most;
         const float fade = __builtin_amdgcn_exp2f(top[nt] - ref);
-        top[nt] = now;
+        top[nt] = most;
         float part = 0.f;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -543,7 +605,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       }
     }
 
-    // ---- the four waves' parts of each row become one
+    // ---- the waves' parts of each head's rows become one
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       sum[nt] += __shfl_xor(sum[nt], 16, 64);
@@ -557,7 +619,8 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int c = nt * 16 + r;
-      const float now = fmaxf(fmaxf(s_m[0][c], s_m[1][c]), fmaxf(s_m[2][c], s_m[3][c]));
+      float now = top[nt];
+      for (int w = wv - part_at; w < wv - part_at + wph; ++w) now = fmaxf(now, s_m[w][c]);
       const float fade = __builtin_amdgcn_exp2f(top[nt] - (now == -INFINITY ? 0.f : now));
       float* dst = &s_o[wv][c * OS + g * (D / 4)];
 #pragma unroll
@@ -577,38 +640,28 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     __syncthreads();
     const bool whole = cnt == un;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (u_first == 0 ? 1 : 0);
-    for (int x = t; x < rows * (D / 4); x += 256) {
-      const int c = x / (D / 4), d = x % (D / 4) * 4;
+    for (int x = t; x < p.heads * rows * (D / 4); x += 256) {
+      const int y = x / (D / 4), d = x % (D / 4) * 4, hh = y / rows, c = y % rows;
       float now = -INFINITY, l = 0.f;
       floatx4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) now = fmaxf(now, s_m[w][c]);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = hh * wph; w < (hh + 1) * wph; ++w) now = fmaxf(now, s_m[w][c]);
+      for (int w = hh * wph; w < (hh + 1) * wph; ++w) {
         l += s_l[w][c] * __builtin_amdgcn_exp2f(s_m[w][c] - (now == -INFINITY ? 0.f : now));
         o += *reinterpret_cast<const floatx4*>(&s_o[w][c * OS + d]);
       }
       if (whole) {
-        const float inv = l == 0.f ? 0.f : (p.c.v_scale ? p.c.v_scale[h] : 1.f) / l;
-        const int row = row0 + c, j = row / p.group, head = h * p.group + row % p.group;
-        const int64_t dst = (((int64_t)n * p.m + j) * p.Hq + head) * D + d;
-        if (l == 0.f) o = floatx4{0.f, 0.f, 0.f, 0.f};
-        else o = floatx4{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-        if (p.out_bf16)
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.o) + dst) =
-              u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
-        else
-          *reinterpret_cast<floatx4*>(static_cast<float*>(p.o) + dst) = o;
-        if (p.lse && d == 0)
-          p.lse[((int64_t)n * p.m + j) * p.Hq + head] =
-              l == 0.f ? -INFINITY : (now + log2f(l)) * 0.6931471805599453f;
+        write_row<D>(p, n, h0 + hh, row0 + c, d, now, l, o);
       } else {
-        *reinterpret_cast<floatx4*>(p.part_o + (slot * COLS + c) * D + d) = o;
-        if (d == 0) {
-          p.part_ml[(slot * COLS + c) * 2] = now;
-          p.part_ml[(slot * COLS + c) * 2 + 1] = l;
-        }
+        const int64_t part = (slot * p.heads + hh) * p.part_rows + c;
+        *reinterpret_cast<floatx4*>(p.part_o + part * D + d) = o;
+        if (d == 0) *reinterpret_cast<floatx2*>(p.part_ml + part * 2) = floatx2{now, l};
       }
+    }
+    // which workgroups have the group's first and last units
+    if (p.split && t == 0) {
+      int* of = p.part_of + 2 * ((int64_t)n * per_seq + pair);
+      if (u_first == 0) of[0] = blockIdx.x;
+      if (u_first + cnt == un) of[1] = blockIdx.x;
     }
     __syncthreads();  // s_o, s_m and s_l are free again
 
@@ -621,75 +674,104 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
   }
 }
 
-// Joins the parts of the (sequence, row block, head)s that several workgroups shared. One
-// workgroup each; those that one workgroup did alone are finished already.
+// Joins the parts of the heads that several workgroups shared; a head that one workgroup did
+// alone is finished already. A workgroup takes `rows` rows of one (sequence, row block, head):
+// D / 4 threads read a part's row, and the 1024 / D such sets are given to the parts of a row
+// first, so that they are read at the same time, and to further rows.
 template <int D>
-__global__ __launch_bounds__(256) void paged_join_kernel(const PagedDecodePlan p) {
-  __shared__ int64_t s_scan[4];
-  const int t = threadIdx.x;
-  const int per_seq = p.row_blocks * p.Hkv, cols = 16 * p.tiles;
-  const int n = blockIdx.x / per_seq, pair = blockIdx.x % per_seq;
-  const int rb = pair / p.Hkv, h = pair % p.Hkv;
-  int64_t before = 0, total = 0;
-  for (int i = t; i < p.N; i += 256) {
-    const int u = seq_units(p, seq_len(p, i));
-    total += u;
-    if (i < n) before += u;
-  }
-  total = block_sum(total, s_scan) * per_seq;
-  before = block_sum(before, s_scan) * per_seq;
-  const int un = seq_units(p, seq_len(p, n));
-  const Share share = make_share(p, total);
-  const int64_t u0 = before + (int64_t)pair * un;
-  const int w0 = share.owner(u0), w1 = share.owner(u0 + un - 1);
-  if (w0 == w1) return;
+__global__ __launch_bounds__(256, 6) void paged_join_kernel(const PagedDecodePlan p, int rows) {
+  constexpr int Q = D / 4, SETS = 256 / Q;
+  __shared__ floatx4 s_o[256];
+  __shared__ floatx2 s_ml[256];
+  const int t = threadIdx.x, d = t % Q * 4, set = t / Q;
+  const int groups = p.Hkv / p.heads, cols = 16 * p.tiles;
+  const int h = blockIdx.x % p.Hkv, nrb = blockIdx.x / p.Hkv;
+  const int rb = nrb % p.row_blocks, n = nrb / p.row_blocks;
+  const int* of = p.part_of + 2 * (((int64_t)n * p.row_blocks + rb) * groups + h / p.heads);
+  const int w0 = of[0], count = of[1] - w0 + 1;
+  if (count == 1) return;
 
-  const int row0 = rb * cols, rows = min(cols, p.rows - row0);
-  for (int x = t; x < rows * (D / 4); x += 256) {
-    const int c = x / (D / 4), d = x % (D / 4) * 4;
-    // part of workgroup w: the first one begins the head (slot 1), the others continue it (slot 0)
-    auto slot = [&](int w) { return (2 * (int64_t)w + (w == w0 ? 1 : 0)) * cols + c; };
-    float now = -INFINITY;
-    for (int w = w0; w <= w1; ++w) now = fmaxf(now, p.part_ml[slot(w) * 2]);
-    const float ref = now == -INFINITY ? 0.f : now;
-    float l = 0.f;
+  int lanes = SETS;  // sets per row, a power of two: four parts or more each
+  while (lanes > 1 && lanes * 2 >= count) lanes /= 2;
+  const int lane = set % lanes, at_once = SETS / lanes;
+  const int row0 = rb * cols, c1 = min(min(cols, p.rows - row0), ((int)blockIdx.y + 1) * rows);
+  for (int c0 = blockIdx.y * rows; c0 < c1; c0 += at_once) {
+    const int c = c0 + set / lanes;
+    const bool there = c < c1;
+    float top = -INFINITY, l = 0.f;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int w = w0; w <= w1; ++w) {
-      const int64_t s = slot(w);
-      const float fade = __builtin_amdgcn_exp2f(p.part_ml[s * 2] - ref);
-      l += p.part_ml[s * 2 + 1] * fade;
-      const floatx4 y = *reinterpret_cast<const floatx4*>(p.part_o + s * D + d);
+    for (int x0 = lane; there && x0 < count; x0 += 4 * lanes) {  // four parts at a time
+      floatx2 ml[4];
+      floatx4 y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = fmaf(y[e], fade, o[e]);
+      for (int k = 0; k < 4; ++k) {
+        const int x = min(x0 + k * lanes, count - 1);
+        // the first workgroup's part begins the head (slot 1), the others continue it (slot 0)
+        const int64_t part =
+            ((2 * (int64_t)(w0 + x) + (x == 0 ? 1 : 0)) * p.heads + h % p.heads) * p.part_rows + c;
+        ml[k] = *reinterpret_cast<const floatx2*>(p.part_ml + 2 * part);
+        y[k] = *reinterpret_cast<const floatx4*>(p.part_o + part * D + d);
+      }
+      float most = top;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) most = fmaxf(most, ml[k].x);
+      const float ref = most == -INFINITY ? 0.f : most;
+      const float fade = __builtin_amdgcn_exp2f(top - ref);
+      top = most;
+      l *= fade;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= fade;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (x0 + k * lanes >= count) continue;
+        const float f = __builtin_amdgcn_exp2f(ml[k].x - ref);
+        l = fmaf(ml[k].y, f, l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(y[k][e], f, o[e]);
+      }
     }
-    const int row = row0 + c, j = row / p.group, head = h * p.group + row % p.group;
-    const int64_t dst = (((int64_t)n * p.m + j) * p.Hq + head) * D + d;
-    const float inv = (p.c.v_scale ? p.c.v_scale[h] : 1.f) / l;
-    if (l == 0.f) o = floatx4{0.f, 0.f, 0.f, 0.f};
-    else o = floatx4{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-    if (p.out_bf16)
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.o) + dst) =
-          u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
-    else
-      *reinterpret_cast<floatx4*>(static_cast<float*>(p.o) + dst) = o;
-    if (p.lse && d == 0)
-      p.lse[((int64_t)n * p.m + j) * p.Hq + head] =
-          l == 0.f ? -INFINITY : (now + log2f(l)) * 0.6931471805599453f;
+    if (lanes > 1) {
+      __syncthreads();
+      s_o[t] = o;
+      s_ml[t] = floatx2{top, l};
+      __syncthreads();
+      if (lane == 0) {
+        for (int x = 1; x < lanes; ++x) top = fmaxf(top, s_ml[t + x * Q].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float own = __builtin_amdgcn_exp2f(s_ml[t].x - ref);
+        l *= own;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= own;
+        for (int x = 1; x < lanes; ++x) {
+          const float f = __builtin_amdgcn_exp2f(s_ml[t + x * Q].x - ref);
+          const floatx4 y = s_o[t + x * Q];
+          l = fmaf(s_ml[t + x * Q].y, f, l);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(y[e], f, o[e]);
+        }
+      }
+    }
+    if (there && lane == 0) write_row<D>(p, n, h, row0 + c, d, top, l, o);
   }
 }
 
 template <int CT, int D>
 hipError_t launch_d(const PagedDecodePlan& p, hipStream_t stream) {
   const int64_t all = (int64_t)p.N * p.row_blocks * p.Hkv;
-  const dim3 grid((unsigned)(p.split ? p.split : all));
+  const dim3 grid((unsigned)(p.split ? p.split : all / p.heads));
   // one page per 16 aligned tokens, whose rows lie within 32 bits of each other
-  const bool p16 = p.c.page_size % 16 == 0 && p.c.k_token < (1 << 26) && p.c.v_token < (1 << 26);
+  const bool p16 = p.c.page_size % 16 == 0 && p.c.k_token < (1 << 26) && p.c.v_token < (1 << 26) &&
+                   p.c.k_page < (int64_t(1) << 36) && p.c.v_page < (int64_t(1) << 36);
   auto kern = p.tiles == 1 ? (p16 ? paged_decode_kernel<CT, D, 1, true> : paged_decode_kernel<CT, D, 1, false>)
                            : (p16 ? paged_decode_kernel<CT, D, 2, true> : paged_decode_kernel<CT, D, 2, false>);
   hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, p, p.c.table);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.split) {
-    hipLaunchKernelGGL(paged_join_kernel<D>, dim3((unsigned)all), dim3(256), 0, stream, p);
+    // fewer rows per workgroup where there are few heads
+    const int64_t chunks = std::min<int64_t>(p.part_rows, (512 + all - 1) / all);
+    const int rows = (int)((p.part_rows + chunks - 1) / chunks);
+    hipLaunchKernelGGL(paged_join_kernel<D>, dim3((unsigned)all, (unsigned)((p.part_rows + rows - 1) / rows)),
+                       dim3(256), 0, stream, p, rows);
     e = hipGetLastError();
   }
   return e;
