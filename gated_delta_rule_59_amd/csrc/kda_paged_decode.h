@@ -17,10 +17,12 @@
 //   within the lane. Tile j then holds channels {VEC r + j}, so lane (r, g) ends with the D / 4
 //   consecutive channels from g D / 4 on of row r.
 //
-// Rounding: products and sums are held in 32 bits. P is split into two bf16 parts (16
-// significant bits, an error of 2^-17 of each weight), which costs a second V product that
-// hides under the loads; one part alone (2^-9) would double the error of a bf16 result. An e4m3
-// value is a bf16 value exactly. fp32 caches take the fp32 matrix instruction throughout.
+// Rounding: products and sums are held in 32 bits. Over a bf16 cache P is split into two bf16
+// parts (16 significant bits, an error of 2^-17 of each weight), which costs a second V product
+// that hides under the loads; one part alone (2^-9) would add as much error to a bf16 result as
+// its own rounding. An e4m3 value is exact in bf16 (K) and in fp16 (V), so over an e4m3 cache P is
+// fp16: one part for a bf16 result (2^-12 of each weight, an eighth of the result's own rounding),
+// two for an fp32 one (2^-23). fp32 caches take the fp32 matrix instruction throughout.
 //
 // Who sees what. Rows of a block differ in what they see only near the newest token and the
 // window's far edge. The tokens that all of them see go through the matrix product; for the
@@ -109,15 +111,19 @@ template <bool H>
 __device__ __forceinline__ floatx2 e4m3_pair(uint32_t w) {
   return __builtin_amdgcn_cvt_pk_f32_fp8((int)w, H);
 }
-// Eight e4m3 values as a bf16 operand (exact: the dropped halves are zero).
+// Two e4m3 values as bf16 or fp16 (both exact), elements 2h and 2h + 1.
+template <bool H>
+__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, H));
+}
+template <bool H>
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, H));
+}
+// Eight e4m3 values as a bf16 operand.
 __device__ __forceinline__ bf16x8 e4m3_operand(uint32_t w0, uint32_t w1) {
-  const floatx2 a = e4m3_pair<false>(w0), b = e4m3_pair<true>(w0);
-  const floatx2 c = e4m3_pair<false>(w1), d = e4m3_pair<true>(w1);
-  const u32x4 v = {halves_hi(__float_as_uint(a.x), __float_as_uint(a.y)),
-                   halves_hi(__float_as_uint(b.x), __float_as_uint(b.y)),
-                   halves_hi(__float_as_uint(c.x), __float_as_uint(c.y)),
-                   halves_hi(__float_as_uint(d.x), __float_as_uint(d.y))};
-  return __builtin_bit_cast(bf16x8, v);
+  return __builtin_bit_cast(bf16x8, u32x4{e4m3_bf16<false>(w0), e4m3_bf16<true>(w0),
+                                          e4m3_bf16<false>(w1), e4m3_bf16<true>(w1)});
 }
 
 // The VEC channels of a lane's words of a value row, as floats.
@@ -157,11 +163,16 @@ __device__ __forceinline__ void write_row(const PagedDecodePlan& p, int n, int h
 }
 
 // P16: page_size is a multiple of 16, so 16 aligned tokens have one page.
-template <int CT, int D, int NT, bool P16>
+// ONE: the weights in one fp16 part (e4m3 caches only).
+template <int CT, int D, int NT, bool P16, bool ONE>
 __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     const PagedDecodePlan p, const int32_t* __restrict__ block_table) {
   using TY = Types<CT, D>;
+  static_assert(!ONE || CT == kF8, "V must be exact in fp16");
   constexpr int VEC = TY::VEC;
+  // Weights that become fp16 are held 2^14 times as large (at most 16384): the smallest fp16 step
+  // is then 2^-38 of the largest weight, and a long tail of small weights is not lost.
+  constexpr float kLift = CT == kF8 ? 14.f : 0.f, kUnlift = CT == kF8 ? 0x1p-14f : 1.f;
   constexpr int COLS = 16 * NT;
   constexpr int OS = D + 4;  // floats per row of s_o (staggered over the LDS banks)
   __shared__ __align__(16) float s_o[4][COLS * OS];
@@ -462,34 +473,25 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
 #pragma unroll
       for (int x = P16 ? 0 : 2; x < (P16 ? 2 : 10); ++x) on_pages = on_pages && is_page(now.id[x]);
       const bool plain = tb >= all_lo && tb + 32 <= all_hi && (P16 ? on_pages : __all(on_pages));
-      // Bit i of `sees` / `shared`: this lane's row / every row sees token slot i. Applied in
-      // every tile: a branch around them would make copies of the values, which waits for them.
-      unsigned sees[NT], shared = 0xffu;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sees[nt] = 0xffu;
+      for (int i8 = 0; i8 < 8; ++i8)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][i8 >> 2][i8 & 3] *= CT == kF32 ? 1.f : to_log2;
       if (!plain) {
-        shared = 0;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sees[nt] = 0;
 #pragma unroll
         for (int i8 = 0; i8 < 8; ++i8) {
           const int tok = tb + 4 * g + (i8 & 3) + 16 * (i8 >> 2);
           const bool in = is_page(now.id[P16 ? i8 >> 2 : 2 + i8]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            sees[nt] |= in && tok >= lo[nt] && tok < hi[nt] ? 1u << i8 : 0u;
-          shared |= in && tok >= all_lo && tok < all_hi ? 1u << i8 : 0u;
+          for (int nt = 0; nt < NT; ++nt) {
+            const bool sees = in && tok >= lo[nt] && tok < hi[nt];
+            s[nt][i8 >> 2][i8 & 3] = sees ? s[nt][i8 >> 2][i8 & 3] : -INFINITY;
+          }
+          const uint32_t keep = in && tok >= all_lo && tok < all_hi ? ~0u : 0u;
+          // In place: the compiler would copy the values on the other way round, and wait there.
+#pragma unroll
+          for (int e = 0; e < TY::VW; ++e) asm volatile("v_and_b32 %0, %1, %0" : "+v"(vw[i8][e]) : "v"(keep));
         }
-      }
-#pragma unroll
-      for (int i8 = 0; i8 < 8; ++i8) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          s[nt][i8 >> 2][i8 & 3] = sees[nt] >> i8 & 1 ? s[nt][i8 >> 2][i8 & 3] * (CT == kF32 ? 1.f : to_log2)
-                                                      : -INFINITY;
-        const uint32_t keep = 0u - (shared >> i8 & 1);
-#pragma unroll
-        for (int e = 0; e < TY::VW; ++e) vw[i8][e] &= keep;
       }
 
       // running maximum and sum of each row
@@ -500,8 +502,8 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         const float most = fmaxf(top[nt], mx);
-        const float ref = most == -INFINITY ? 0.f : most;
-        const float fade = __builtin_amdgcn_exp2f(top[nt] - ref);
+        const float peak = most == -INFINITY ? 0.f : most, ref = peak - kLift;
+        const float fade = __builtin_amdgcn_exp2f(top[nt] - peak);
         top[nt] = most;
         float part = 0.f;
 #pragma unroll
@@ -531,22 +533,36 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
               acc[nt][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
                   __uint_as_float(vw[i8][j]), s[nt][i8 >> 2][i8 & 3], acc[nt][j], 0, 0, 0);
       } else {
-        bf16x8 p_hi[NT], p_lo[NT];
+        typedef std::conditional_t<CT == kF8, half8, bf16x8> operand;
+        operand p_hi[NT], p_lo[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i8 = 0; i8 < 8; ++i8) {
-            __bf16 a, b;
-            split_bf16(s[nt][i8 >> 2][i8 & 3], a, b);
-            p_hi[nt][i8] = a;
-            p_lo[nt][i8] = b;
+            const float w = s[nt][i8 >> 2][i8 & 3];
+            if constexpr (CT == kBF16) {
+              __bf16 a, b;
+              split_bf16(w, a, b);
+              p_hi[nt][i8] = a;
+              p_lo[nt][i8] = b;
+            } else {
+              _Float16 a, b;
+              split_f16(w, a, b);
+              p_hi[nt][i8] = a;
+              p_lo[nt][i8] = b;
+            }
           }
         auto product = [&](int j, const u32x4& frag) {
-          const bf16x8 a = __builtin_bit_cast(bf16x8, frag);
+          const operand a = __builtin_bit_cast(operand, frag);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][j] = mfma_bf16(a, p_hi[nt], acc[nt][j]);
-            acc[nt][j] = mfma_bf16(a, p_lo[nt], acc[nt][j]);
+            if constexpr (CT == kBF16) {
+              acc[nt][j] = mfma_bf16(a, p_hi[nt], acc[nt][j]);
+              acc[nt][j] = mfma_bf16(a, p_lo[nt], acc[nt][j]);
+            } else {
+              acc[nt][j] = mfma_f16(a, p_hi[nt], acc[nt][j]);
+              if constexpr (!ONE) acc[nt][j] = mfma_f16(a, p_lo[nt], acc[nt][j]);
+            }
           }
         };
 #pragma unroll
@@ -554,15 +570,16 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
           u32x4 f0, f1;
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
+            uint32_t x, y;  // channels j, j + 1 of two tokens
             if constexpr (CT == kBF16) {
-              f0[a] = halves_lo(vw[2 * a][j / 2], vw[2 * a + 1][j / 2]);
-              f1[a] = halves_hi(vw[2 * a][j / 2], vw[2 * a + 1][j / 2]);
+              x = vw[2 * a][j / 2];
+              y = vw[2 * a + 1][j / 2];
             } else {
-              const floatx2 x = j & 2 ? e4m3_pair<true>(vw[2 * a][j / 4]) : e4m3_pair<false>(vw[2 * a][j / 4]);
-              const floatx2 y = j & 2 ? e4m3_pair<true>(vw[2 * a + 1][j / 4]) : e4m3_pair<false>(vw[2 * a + 1][j / 4]);
-              f0[a] = halves_hi(__float_as_uint(x.x), __float_as_uint(y.x));
-              f1[a] = halves_hi(__float_as_uint(x.y), __float_as_uint(y.y));
+              x = j & 2 ? e4m3_f16<true>(vw[2 * a][j / 4]) : e4m3_f16<false>(vw[2 * a][j / 4]);
+              y = j & 2 ? e4m3_f16<true>(vw[2 * a + 1][j / 4]) : e4m3_f16<false>(vw[2 * a + 1][j / 4]);
             }
+            f0[a] = halves_lo(x, y);
+            f1[a] = halves_hi(x, y);
           }
           product(j, f0);
           product(j + 1, f1);
@@ -610,6 +627,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     for (int nt = 0; nt < NT; ++nt) {
       sum[nt] += __shfl_xor(sum[nt], 16, 64);
       sum[nt] += __shfl_xor(sum[nt], 32, 64);
+      sum[nt] *= kUnlift;
       if (g == 0) {
         s_m[wv][nt * 16 + r] = top[nt];
         s_l[wv][nt * 16 + r] = sum[nt];
@@ -621,7 +639,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       const int c = nt * 16 + r;
       float now = top[nt];
       for (int w = wv - part_at; w < wv - part_at + wph; ++w) now = fmaxf(now, s_m[w][c]);
-      const float fade = __builtin_amdgcn_exp2f(top[nt] - (now == -INFINITY ? 0.f : now));
+      const float fade = kUnlift * __builtin_amdgcn_exp2f(top[nt] - (now == -INFINITY ? 0.f : now));
       float* dst = &s_o[wv][c * OS + g * (D / 4)];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -762,8 +780,14 @@ hipError_t launch_d(const PagedDecodePlan& p, hipStream_t stream) {
   // one page per 16 aligned tokens, whose rows lie within 32 bits of each other
   const bool p16 = p.c.page_size % 16 == 0 && p.c.k_token < (1 << 26) && p.c.v_token < (1 << 26) &&
                    p.c.k_page < (int64_t(1) << 36) && p.c.v_page < (int64_t(1) << 36);
-  auto kern = p.tiles == 1 ? (p16 ? paged_decode_kernel<CT, D, 1, true> : paged_decode_kernel<CT, D, 1, false>)
-                           : (p16 ? paged_decode_kernel<CT, D, 2, true> : paged_decode_kernel<CT, D, 2, false>);
+  auto pick = [&](auto one) {
+    constexpr bool ONE = decltype(one)::value;
+    return p.tiles == 1 ? (p16 ? paged_decode_kernel<CT, D, 1, true, ONE> : paged_decode_kernel<CT, D, 1, false, ONE>)
+                        : (p16 ? paged_decode_kernel<CT, D, 2, true, ONE> : paged_decode_kernel<CT, D, 2, false, ONE>);
+  };
+  auto kern = pick(std::false_type{});
+  if constexpr (CT == kF8)
+    if (p.out_bf16) kern = pick(std::true_type{});
   hipLaunchKernelGGL(kern, grid, dim3(256), 0, stream, p, p.c.table);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.split) {
