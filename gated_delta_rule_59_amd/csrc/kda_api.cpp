@@ -307,12 +307,7 @@ kda::PageCache page_cache(const kda_page_cache& c) {
   r.v = static_cast<char*>(c.v);
   r.num_pages = c.num_pages;
   r.page_size = c.page_size;
-  // n / d = (n * m) >> s for n < 2^31: s = 31 + ceil(log2 d), m = floor(2^s / d) + 1 <= 2^32 - 1
-  // unless d = 1, where m = 2^31 + 1 serves as well
-  int up = 0;
-  while ((int64_t(1) << up) < c.page_size) ++up;
-  r.ps_shift = 31 + up;
-  r.ps_mul = (unsigned)((uint64_t(1) << r.ps_shift) / (uint64_t)c.page_size + 1);
+  kda::divide_by(c.page_size, &r.ps_mul, &r.ps_shift);
   r.k_page = c.k_page_stride * es, r.k_token = c.k_token_stride * es, r.k_head = c.k_head_stride * es;
   r.v_page = c.v_page_stride * es, r.v_token = c.v_token_stride * es, r.v_head = c.v_head_stride * es;
   r.k_page16 = (unsigned)(r.k_page / 16), r.v_page16 = (unsigned)(r.v_page / 16);
@@ -356,8 +351,9 @@ kda_status validate_decode_shapes(const kda_paged_decode_args* a, kda::PagedDeco
   if ((int64_t)a->m * a->Hq > (1 << 24)) return fail(KDA_ERR_BAD_SHAPE, "m * Hq too large");
   // one 256-work-item workgroup per (sequence, row block, head); a row block holds 16 rows or more
   const int64_t pairs = (int64_t)a->N * a->Hkv * (((int64_t)a->m * (a->Hq / a->Hkv) + 15) / 16);
-  if (pairs > kMaxDecodePairs || (int64_t)a->N * a->m * a->Hq > (int64_t(1) << 40))
-    return fail(KDA_ERR_BAD_SHAPE, "N * m * Hq too large for one launch");
+  if (pairs > kMaxDecodePairs || (int64_t)a->N * a->m * a->Hq > (int64_t(1) << 40) ||
+      pairs / a->N * (a->max_len / 32 + 1) > 0x7fffffffLL)
+    return fail(KDA_ERR_BAD_SHAPE, "N * m * Hq or max_len * m * Hq too large for one launch");
   *p = kda::PagedDecodePlan{};
   p->N = a->N, p->m = a->m, p->Hq = a->Hq, p->Hkv = a->Hkv, p->d = a->d;
   p->act_bf16 = a->act_dtype == KDA_BF16;

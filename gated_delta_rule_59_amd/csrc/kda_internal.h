@@ -63,6 +63,15 @@ hipError_t launch_chunk_fast(const ChunkPlan& p, hipStream_t stream);
 size_t noalloc_scratch_bytes();
 hipError_t noalloc_scratch(void** ptr);
 
+// n / d = (n * mul) >> shift for 0 <= n < 2^31, d >= 1: shift = 31 + ceil(log2 d) and mul =
+// floor(2^shift / d) + 1, which is below 2^32.
+inline void divide_by(int d, unsigned* mul, int* shift) {
+  int up = 0;
+  while ((int64_t(1) << up) < d) ++up;
+  *shift = 31 + up;
+  *mul = (unsigned)((uint64_t(1) << *shift) / (uint64_t)d + 1);
+}
+
 // A paged cache as the kernels take it (validated; strides in bytes).
 struct PageCache {
   char *k, *v;
@@ -106,7 +115,11 @@ struct PagedDecodePlan {
   float scale;
   void* o;
   float* lse;
-  int heads;                     // neighbouring key/value heads a workgroup carries: 1, 2 or 4
+  int heads, groups;             // neighbouring key/value heads a workgroup carries (1, 2 or 4),
+                                 // Hkv / heads
+  int unit_log;                  // log2 of the tokens that its waves take at a time
+  unsigned group_mul;            // row / group = (row * group_mul) >> group_shift
+  int group_shift;
   int split;                     // workgroups that share all work evenly; 0: one per (n, row
                                  // block, head group)
   int part_rows;                 // rows of a part

@@ -25,10 +25,11 @@
 // two for an fp32 one (2^-23). fp32 caches take the fp32 matrix instruction throughout.
 //
 // Who sees what. Rows of a block differ in what they see only near the newest token and the
-// window's far edge. The tokens that all of them see go through the matrix product; for the
-// others ("private" ones, at most m - 1 at each end) V enters it as zero and they are added by
-// predicated multiply-adds, so a NaN or an infinity in a value that a row does not see never
-// meets that row, not even multiplied by zero. Values no row sees are replaced by zero as well.
+// window's far edge ("private" tokens, at most m - 1 at each end). A row that does not see a token
+// has weight 0 for it in the matrix product, which is exact as long as the value is finite. Where
+// a private value is not, the tile's private values enter the product as zero and are added
+// row by row with predicated multiply-adds instead, so that a NaN or an infinity that a row does
+// not see never meets it. Values that no row sees are replaced by zero.
 #pragma once
 
 #include <math.h>
@@ -45,14 +46,17 @@ namespace paged {
 
 // Work is counted in units: a workgroup's four waves carry p.heads (1, 2 or 4) neighbouring
 // key/value heads, 4 / p.heads waves each, and take 32 tokens per wave at a time, so a unit is
-// 128 / p.heads tokens of p.heads heads. The heads of a token lie side by side in a cache with the
+// 2^p.unit_log = 128 / p.heads tokens of p.heads heads. The heads of a token lie side by side in a cache with the
 // token outermost, and reading 1 KiB of each token at a time runs nearer to what HBM delivers than
 // 256 B (4 contexts of 65k tokens, 8 heads: 222 us with one head per workgroup, 188 with four).
 //
 // Workgroups with the same number of waves per head share (sequence, row block, head group)s
-// evenly: workgroup w takes units [start(w), start(w + 1)) of all, in order. Where it begins or ends
+// evenly: each takes equally many units (or one more), in order. Where it begins or ends
 // inside a group it leaves a part in the workspace.
-__device__ __forceinline__ int unit_tokens(const PagedDecodePlan& p) { return 128 / p.heads; }
+// row / p.group, for 0 <= row < 2^24
+__device__ __forceinline__ int div_group(const PagedDecodePlan& p, int row) {
+  return (int)(((uint64_t)(unsigned)row * p.group_mul) >> p.group_shift);
+}
 // The new tokens of sequence n see positions [0, len); with a window, the first of them begins
 // at len - m + 1 - window.
 __device__ __forceinline__ int seq_len(const PagedDecodePlan& p, int n) {
@@ -61,12 +65,11 @@ __device__ __forceinline__ int seq_len(const PagedDecodePlan& p, int n) {
 __device__ __forceinline__ int first_unit(const PagedDecodePlan& p, int len) {
   if (!p.window) return 0;
   const int64_t lo = (int64_t)len - p.m + 1 - p.window;
-  return lo > 0 ? (int)lo / unit_tokens(p) : 0;
+  return lo > 0 ? (int)lo >> p.unit_log : 0;
 }
 // Units that a sequence's workgroups walk per group; one at least, which writes zeros.
 __device__ __forceinline__ int seq_units(const PagedDecodePlan& p, int len) {
-  const int u = unit_tokens(p);
-  return max(1, (len + u - 1) / u - first_unit(p, len));
+  return max(1, ((len + (1 << p.unit_log) - 1) >> p.unit_log) - first_unit(p, len));
 }
 
 template <int CT, int D>
@@ -126,6 +129,17 @@ __device__ __forceinline__ bf16x8 e4m3_operand(uint32_t w0, uint32_t w1) {
                                           e4m3_bf16<false>(w1), e4m3_bf16<true>(w1)});
 }
 
+// Whether a word of cached values holds an infinity or a NaN.
+template <int CT>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  if constexpr (CT == kF32) return (w & 0x7f800000u) == 0x7f800000u;
+  if constexpr (CT == kBF16) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+  // e4m3 has no infinities; NaN is all ones but the sign
+  if constexpr (CT == kF8)
+    return (w & 0x7fu) == 0x7fu || (w & 0x7f00u) == 0x7f00u || (w & 0x7f0000u) == 0x7f0000u ||
+           (w & 0x7f000000u) == 0x7f000000u;
+}
+
 // The VEC channels of a lane's words of a value row, as floats.
 template <int CT, int VEC>
 __device__ __forceinline__ float word_value(const uint32_t* w, int x) {
@@ -144,13 +158,36 @@ __device__ __forceinline__ void load_bytes(const char* p, uint32_t* w) {
     load_words<VB / 4>(p, w);
 }
 
-// Four channels (d ..) of a finished row: o and l are sums of e^{s - now}-weighted values.
+// N consecutive channels, as fp32 or rounded to bf16.
+template <int N, typename T>
+__device__ __forceinline__ void store_channels(T* p, const float* x) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (N == 2) {
+      *reinterpret_cast<floatx2*>(p) = floatx2{x[0], x[1]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<floatx4*>(p + i) = floatx4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+    }
+  } else {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+    if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+    if constexpr (N == 4) *reinterpret_cast<u32x2*>(p) = u32x2{w[0], w[1]};
+    if constexpr (N == 8) *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+  }
+}
+
+// A row of o: of query row `row` of key/value head h of sequence n.
+__device__ __forceinline__ int64_t out_row(const PagedDecodePlan& p, int n, int h, int row) {
+  const int j = div_group(p, row);
+  return ((int64_t)n * p.m + j) * p.Hq + h * p.group + row - j * p.group;
+}
+// Four channels (d ..) of a finished row: o and l are sums weighted by 2^{s - now}.
 template <int D>
-__device__ __forceinline__ void write_row(const PagedDecodePlan& p, int n, int h, int row, int d,
+__device__ __forceinline__ void write_row(const PagedDecodePlan& p, int64_t dst, int d, float scale,
                                           float now, float l, floatx4 o) {
-  const int j = row / p.group, head = h * p.group + row % p.group;
-  const int64_t dst = ((int64_t)n * p.m + j) * p.Hq + head;
-  const float inv = (p.c.v_scale ? p.c.v_scale[h] : 1.f) / l;
+  const float inv = scale / l;
   if (l == 0.f) o = floatx4{0.f, 0.f, 0.f, 0.f};  // nothing was seen
   else o = floatx4{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
   if (p.out_bf16)
@@ -178,25 +215,24 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
   __shared__ __align__(16) float s_o[4][COLS * OS];
   __shared__ float s_m[4][COLS], s_l[4][COLS];
   __shared__ int64_t s_scan[4];
-  __shared__ int s_n;
-  __shared__ int64_t s_at;
+  __shared__ int s_at[3];
 
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int groups = p.Hkv / p.heads, per_seq = p.row_blocks * groups;
+  const int per_seq = p.row_blocks * p.groups;
   const int wph = 4 / p.heads;                      // waves per head
   const int head_at = wv / wph, part_at = wv % wph;  // this wave's head of the group, share of a unit
-  const int unit = unit_tokens(p);
+  const int unit = 1 << p.unit_log;
 
-  // ---- this workgroup's units
-  int n;
-  int64_t at;    // unit within sequence n (units of its first (row block, head) first)
-  int64_t left;  // units to do
+  // ---- this workgroup's units: `left` of them, from unit u_first of (row block, head group)
+  //      `pair` of sequence n on
+  int n, pair, u_first = 0, len;
+  int64_t left;
   if (p.split == 0) {
     n = blockIdx.x / per_seq;
-    const int un = seq_units(p, seq_len(p, n));
-    at = (int64_t)(blockIdx.x % per_seq) * un;
-    left = un;
+    pair = blockIdx.x - n * per_seq;
+    len = seq_len(p, n);
+    left = seq_units(p, len);
   } else {
     const int c = (p.N + 255) / 256;
     int64_t mine = 0;
@@ -217,37 +253,45 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       if (i < wv) before += s_scan[i];
       total += s_scan[i];
     }
-    const int64_t share = min(total, (int64_t)p.split);  // workgroups that have any
-    if (blockIdx.x >= share) return;
-    const int64_t u0 = total * blockIdx.x / share;
-    left = total * (blockIdx.x + 1) / share - u0;
+    const unsigned w = blockIdx.x;
+    const uint64_t each = (uint64_t)total / (unsigned)p.split;
+    const unsigned more = (unsigned)(total - (int64_t)(each * (unsigned)p.split));
+    left = (int64_t)each + (w < more ? 1 : 0);
+    if (left == 0) return;
+    const int64_t u0 = (int64_t)(each * w) + min(w, more);
     int64_t excl = before + incl - mine;
     if (excl <= u0 && u0 < excl + mine) {
       int i = t * c;
-      for (;; ++i) {
-        const int64_t ui = (int64_t)seq_units(p, seq_len(p, i)) * per_seq;
-        if (u0 < excl + ui || i + 1 == p.N) break;
-        excl += ui;
+      int un = seq_units(p, seq_len(p, i));
+      while (u0 - excl >= (int64_t)un * per_seq && i + 1 < p.N) {
+        excl += (int64_t)un * per_seq;
+        un = seq_units(p, seq_len(p, ++i));
       }
-      s_n = i;
-      s_at = u0 - excl;
+      const unsigned at = (unsigned)(u0 - excl);  // below 2^31
+      s_at[0] = i;
+      s_at[1] = at / (unsigned)un;
+      s_at[2] = at % (unsigned)un;
     }
     __syncthreads();
-    n = s_n;
-    at = s_at;
+    n = s_at[0];
+    pair = s_at[1];
+    u_first = s_at[2];
+    len = seq_len(p, n);
   }
 
   const float log2_scale = p.scale * kLog2e;
 
-  // ---- one (row block, head) of one sequence after the other
+  // ---- one (row block, head group) of one sequence after the other
   while (left > 0) {
     n = __builtin_amdgcn_readfirstlane(n);
-    const int len = __builtin_amdgcn_readfirstlane(seq_len(p, n));
+    pair = __builtin_amdgcn_readfirstlane(pair);
+    u_first = __builtin_amdgcn_readfirstlane(u_first);
+    len = __builtin_amdgcn_readfirstlane(len);
+    const int next_len = seq_len(p, min(n + 1, p.N - 1));
     const int un = seq_units(p, len);
-    const int pair = __builtin_amdgcn_readfirstlane((int)(at / un));
-    const int u_first = __builtin_amdgcn_readfirstlane((int)(at % un));
     const int cnt = __builtin_amdgcn_readfirstlane((int)min((int64_t)(un - u_first), left));
-    const int rb = pair / groups, h0 = pair % groups * p.heads, h = h0 + head_at;
+    const int rb = p.row_blocks == 1 ? 0 : pair / p.groups;
+    const int h0 = (pair - rb * p.groups) * p.heads, h = h0 + head_at;
     const int row0 = rb * COLS;
     const int rows = min(COLS, p.rows - row0);
 
@@ -256,7 +300,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     auto lo_of = [&](int j) {
       return p.window ? (int)max((int64_t)0, (int64_t)hi_of(j) - p.window) : 0;
     };
-    const int j_first = row0 / p.group, j_last = (row0 + rows - 1) / p.group;
+    const int j_first = div_group(p, row0), j_last = div_group(p, row0 + rows - 1);
     const int all_lo = lo_of(j_last), all_hi = hi_of(j_first);  // seen by every row
     const int any_lo = lo_of(j_first), any_hi = hi_of(j_last);  // seen by one at least
 
@@ -264,13 +308,14 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     // score then overflows only if it is itself out of range), bf16 ones keep their values and
     // the scores are scaled.
     const float to_log2 = log2_scale * (p.c.k_scale ? p.c.k_scale[h] : 1.f);
+    const float v_scale = p.c.v_scale ? p.c.v_scale[h] : 1.f;
     uint32_t q[NT][TY::QW];
     int lo[NT], hi[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = row0 + nt * 16 + r;
       const bool there = row < p.rows;
-      const int j = there ? row / p.group : 0, head = h * p.group + (there ? row % p.group : 0);
+      const int j = there ? div_group(p, row) : 0, head = h * p.group + (there ? row - j * p.group : 0);
       lo[nt] = there ? lo_of(j) : 0;
       hi[nt] = there ? hi_of(j) : 0;
       const char* qp = p.q + ((int64_t)n * p.m + j) * p.q_token + head * p.q_head;
@@ -477,17 +522,30 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       for (int i8 = 0; i8 < 8; ++i8)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][i8 >> 2][i8 & 3] *= CT == kF32 ? 1.f : to_log2;
+      bool careful = false;  // a private value is not finite
       if (!plain) {
+        auto token = [&](int i8) { return tb + 4 * g + (i8 & 3) + 16 * (i8 >> 2); };
+        auto on_page = [&](int i8) { return is_page(now.id[P16 ? i8 >> 2 : 2 + i8]); };
+        bool odd = false;
 #pragma unroll
         for (int i8 = 0; i8 < 8; ++i8) {
-          const int tok = tb + 4 * g + (i8 & 3) + 16 * (i8 >> 2);
-          const bool in = is_page(now.id[P16 ? i8 >> 2 : 2 + i8]);
+          const int tok = token(i8);
+          const bool in = on_page(i8);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const bool sees = in && tok >= lo[nt] && tok < hi[nt];
             s[nt][i8 >> 2][i8 & 3] = sees ? s[nt][i8 >> 2][i8 & 3] : -INFINITY;
           }
-          const uint32_t keep = in && tok >= all_lo && tok < all_hi ? ~0u : 0u;
+          const bool some = tok >= any_lo && tok < any_hi, all = tok >= all_lo && tok < all_hi;
+#pragma unroll
+          for (int e = 0; e < TY::VW; ++e) odd = odd || (in && some && !all && not_finite<CT>(vw[i8][e]));
+        }
+        careful = __any(odd);
+#pragma unroll
+        for (int i8 = 0; i8 < 8; ++i8) {
+          const int tok = token(i8);
+          const bool some = tok >= any_lo && tok < any_hi, all = tok >= all_lo && tok < all_hi;
+          const uint32_t keep = on_page(i8) && (careful ? all : some) ? ~0u : 0u;
           // In place: the compiler would copy the values on the other way round, and wait there.
 #pragma unroll
           for (int e = 0; e < TY::VW; ++e) asm volatile("v_and_b32 %0, %1, %0" : "+v"(vw[i8][e]) : "v"(keep));
@@ -587,8 +645,8 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       }
 
       // private tokens, row by row
-      const int pv0 = max(tb, any_lo), pv1 = min(tb + 32, any_hi);
-      if (!plain && (pv0 < all_lo || pv1 > all_hi)) {
+      if (careful) {
+        const int pv0 = max(tb, any_lo), pv1 = min(tb + 32, any_hi);
         float* ps = s_o[wv];  // [token][column]
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -622,58 +680,91 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       }
     }
 
-    // ---- the waves' parts of each head's rows become one
+    // ---- each head's rows, finished or as a part
+    const bool whole = cnt == un;
+    const int64_t slot = (2 * (int64_t)blockIdx.x + (u_first == 0 ? 1 : 0)) * p.heads * p.part_rows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       sum[nt] += __shfl_xor(sum[nt], 16, 64);
       sum[nt] += __shfl_xor(sum[nt], 32, 64);
       sum[nt] *= kUnlift;
-      if (g == 0) {
-        s_m[wv][nt * 16 + r] = top[nt];
-        s_l[wv][nt * 16 + r] = sum[nt];
-      }
     }
-    __syncthreads();
+    if (wph == 1) {
+      // a wave has all of its head: straight from the registers (through LDS this took a third of
+      // the time of a short segment with 16 rows)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int c = nt * 16 + r;
-      float now = top[nt];
-      for (int w = wv - part_at; w < wv - part_at + wph; ++w) now = fmaxf(now, s_m[w][c]);
-      const float fade = kUnlift * __builtin_amdgcn_exp2f(top[nt] - (now == -INFINITY ? 0.f : now));
-      float* dst = &s_o[wv][c * OS + g * (D / 4)];
+      for (int nt = 0; nt < NT; ++nt) {
+        const int c = nt * 16 + r;
+        if (c >= rows) continue;
+        const float l = sum[nt];
+        const int64_t part = slot + head_at * p.part_rows + c;
+        const int64_t dst = out_row(p, n, h, row0 + c);
+        if (g == 0) {
+          if (!whole)
+            *reinterpret_cast<floatx2*>(p.part_ml + part * 2) = floatx2{top[nt], l};
+          else if (p.lse)
+            p.lse[dst] = l == 0.f ? -INFINITY : (top[nt] + log2f(l)) * 0.6931471805599453f;
+        }
+        const float inv = kUnlift * (whole ? l == 0.f ? 0.f : v_scale / l : 1.f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (VEC >= 4) {
+        for (int e = 0; e < 4; ++e) {
+          float x[VEC];
 #pragma unroll
-          for (int j = 0; j < VEC; j += 4)
-            *reinterpret_cast<floatx4*>(dst + VEC * e + j) =
-                floatx4{acc[nt][j][e] * fade, acc[nt][j + 1][e] * fade, acc[nt][j + 2][e] * fade,
-                        acc[nt][j + 3][e] * fade};
-        } else {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) dst[VEC * e + j] = acc[nt][j][e] * fade;
+          for (int j = 0; j < VEC; ++j) x[j] = whole && l == 0.f ? 0.f : acc[nt][j][e] * inv;
+          const int d = g * (D / 4) + VEC * e;
+          if (!whole)
+            store_channels<VEC, float>(p.part_o + part * D + d, x);
+          else if (p.out_bf16)
+            store_channels<VEC, uint16_t>(static_cast<uint16_t*>(p.o) + dst * D + d, x);
+          else
+            store_channels<VEC, float>(static_cast<float*>(p.o) + dst * D + d, x);
         }
       }
-    }
-    __syncthreads();
-    const bool whole = cnt == un;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (u_first == 0 ? 1 : 0);
-    for (int x = t; x < p.heads * rows * (D / 4); x += 256) {
-      const int y = x / (D / 4), d = x % (D / 4) * 4, hh = y / rows, c = y % rows;
-      float now = -INFINITY, l = 0.f;
-      floatx4 o = {0.f, 0.f, 0.f, 0.f};
-      for (int w = hh * wph; w < (hh + 1) * wph; ++w) now = fmaxf(now, s_m[w][c]);
-      for (int w = hh * wph; w < (hh + 1) * wph; ++w) {
-        l += s_l[w][c] * __builtin_amdgcn_exp2f(s_m[w][c] - (now == -INFINITY ? 0.f : now));
-        o += *reinterpret_cast<const floatx4*>(&s_o[w][c * OS + d]);
+    } else {
+      // the waves' parts of a head meet in LDS
+      if (g == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          s_m[wv][nt * 16 + r] = top[nt];
+          s_l[wv][nt * 16 + r] = sum[nt];
+        }
       }
-      if (whole) {
-        write_row<D>(p, n, h0 + hh, row0 + c, d, now, l, o);
-      } else {
-        const int64_t part = (slot * p.heads + hh) * p.part_rows + c;
-        *reinterpret_cast<floatx4*>(p.part_o + part * D + d) = o;
-        if (d == 0) *reinterpret_cast<floatx2*>(p.part_ml + part * 2) = floatx2{now, l};
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int c = nt * 16 + r;
+        float now = top[nt];
+        for (int w = wv - part_at; w < wv - part_at + wph; ++w) now = fmaxf(now, s_m[w][c]);
+        const float fade = kUnlift * __builtin_amdgcn_exp2f(top[nt] - (now == -INFINITY ? 0.f : now));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[VEC];
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[j] = acc[nt][j][e] * fade;
+          store_channels<VEC, float>(&s_o[wv][c * OS + g * (D / 4) + VEC * e], x);
+        }
       }
+      __syncthreads();
+#pragma unroll 2
+      for (int x = t; x < p.heads * rows * (D / 4); x += 256) {
+        const int y = x / (D / 4), d = x % (D / 4) * 4, hh = p.heads == 1 ? 0 : y / rows, c = y - hh * rows;
+        const float scale = p.heads == 1 ? v_scale : p.c.v_scale ? p.c.v_scale[h0 + hh] : 1.f;
+        float now = -INFINITY, l = 0.f;
+        floatx4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int w = hh * wph; w < (hh + 1) * wph; ++w) now = fmaxf(now, s_m[w][c]);
+        for (int w = hh * wph; w < (hh + 1) * wph; ++w) {
+          l += s_l[w][c] * __builtin_amdgcn_exp2f(s_m[w][c] - (now == -INFINITY ? 0.f : now));
+          o += *reinterpret_cast<const floatx4*>(&s_o[w][c * OS + d]);
+        }
+        if (whole) {
+          write_row<D>(p, out_row(p, n, h0 + hh, row0 + c), d, scale, now, l, o);
+        } else {
+          const int64_t part = slot + hh * p.part_rows + c;
+          *reinterpret_cast<floatx4*>(p.part_o + part * D + d) = o;
+          if (d == 0) *reinterpret_cast<floatx2*>(p.part_ml + part * 2) = floatx2{now, l};
+        }
+      }
+      __syncthreads();  // s_o, s_m and s_l are free again
     }
     // which workgroups have the group's first and last units
     if (p.split && t == 0) {
@@ -681,13 +772,13 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       if (u_first == 0) of[0] = blockIdx.x;
       if (u_first + cnt == un) of[1] = blockIdx.x;
     }
-    __syncthreads();  // s_o, s_m and s_l are free again
 
     left -= cnt;
-    at += cnt;
-    if (at == (int64_t)un * per_seq) {
+    u_first = 0;
+    if (++pair == per_seq) {
+      pair = 0;
       ++n;
-      at = 0;
+      len = next_len;
     }
   }
 }
@@ -702,10 +793,11 @@ __global__ __launch_bounds__(256, 6) void paged_join_kernel(const PagedDecodePla
   __shared__ floatx4 s_o[256];
   __shared__ floatx2 s_ml[256];
   const int t = threadIdx.x, d = t % Q * 4, set = t / Q;
-  const int groups = p.Hkv / p.heads, cols = 16 * p.tiles;
+  const int cols = 16 * p.tiles;
   const int h = blockIdx.x % p.Hkv, nrb = blockIdx.x / p.Hkv;
   const int rb = nrb % p.row_blocks, n = nrb / p.row_blocks;
-  const int* of = p.part_of + 2 * (((int64_t)n * p.row_blocks + rb) * groups + h / p.heads);
+  const int* of = p.part_of + 2 * (((int64_t)n * p.row_blocks + rb) * p.groups + h / p.heads);
+  const float v_scale = p.c.v_scale ? p.c.v_scale[h] : 1.f;
   const int w0 = of[0], count = of[1] - w0 + 1;
   if (count == 1) return;
 
@@ -769,7 +861,7 @@ __global__ __launch_bounds__(256, 6) void paged_join_kernel(const PagedDecodePla
         }
       }
     }
-    if (there && lane == 0) write_row<D>(p, n, h, row0 + c, d, top, l, o);
+    if (there && lane == 0) write_row<D>(p, out_row(p, n, h, row0 + c), d, v_scale, top, l, o);
   }
 }
 

@@ -8,10 +8,14 @@ namespace kda {
 
 namespace {
 
-// Workgroups that share the work evenly: those that the 256 CUs hold at once, two each. Twice as
-// many measured 5 to 8 % slower, and three each on an e4m3 cache (where the registers allow it) 4 %:
-// each has its own start and leaves its own parts.
-constexpr int64_t kShared = 256 * 2;
+// Workgroups that share the work evenly: one per CU, whose four waves have 32 to 64 KiB of keys
+// and values in flight, or two where 32 tokens are only 4 KiB or less. More measured slower (each has its own
+// start and leaves its own parts, and more places of memory are open at a time): 4 contexts of 65k
+// tokens 178 us with 256 workgroups, 190 with 512; e4m3 heads of 64 channels 241 us with 512, 281 with 256.
+int64_t shared_workgroups(const PagedDecodePlan& p) {
+  const int tile = 2 * 32 * p.d * (p.cache_type == kF32 ? 4 : p.cache_type == kBF16 ? 2 : 1);
+  return 256 * (tile >= 8192 ? 1 : 2);
+}
 // Up to this many 128-token units, a (sequence, row block, head) is done by one workgroup, four
 // waves to a head, with nothing left to join.
 constexpr int64_t kAlone = 4;
@@ -27,6 +31,9 @@ size_t plan_paged_decode(PagedDecodePlan* p) {
   p->row_blocks = (p->rows + 16 * p->tiles - 1) / (16 * p->tiles);
   p->part_rows = std::min(p->rows, 16 * p->tiles);
   p->heads = 1;
+  p->groups = p->Hkv;
+  p->unit_log = 7;
+  divide_by(p->group, &p->group_mul, &p->group_shift);
   p->split = 0;
   int64_t span = p->max_len;
   if (p->window) span = std::min<int64_t>(span, (int64_t)p->window + p->m - 1 + 127);
@@ -34,8 +41,14 @@ size_t plan_paged_decode(PagedDecodePlan* p) {
   if (units <= kAlone) return 0;
   // Neighbouring heads together where every workgroup still has four units (of 128 tokens of one
   // head) or more; below that, the four waves of one head finish sooner.
-  if (all * units >= 4 * kShared) p->heads = p->Hkv % 4 == 0 ? 4 : p->Hkv % 2 == 0 ? 2 : 1;
-  p->split = (int)std::min(kShared, all * units);
+  const int64_t shared = shared_workgroups(*p);
+  if (all * units >= 4 * shared) {
+    const int log = p->Hkv % 4 == 0 ? 2 : p->Hkv % 2 == 0 ? 1 : 0;
+    p->heads = 1 << log;
+    p->groups = p->Hkv >> log;
+    p->unit_log = 7 - log;
+  }
+  p->split = (int)std::min(shared, all * units);
   return parts(*p) * (p->d + 2) * sizeof(float) + (size_t)(all / p->heads) * 2 * sizeof(int);
 }
 
