@@ -7,12 +7,15 @@
 // p_a as it is. The draw inverts the cumulative sum: the smallest i with C_i > u C_V.
 //
 // What has to be read is one row of p and, where a draft fell, one of q: HBM bounds it for a
-// batch, latency for one sequence. Two launches: the first sums the weights of every block of
-// kBlock tokens (grid over blocks and sequences, 64-bit sums), the second, one workgroup per
-// sequence, finds the block in the blocks' prefix sums and the token within the block.
+// batch, latency for one sequence. Two launches: in the first, every wave finds out which drafts
+// stand (a few gathered values) and sums the weights of its blocks of 1024 tokens; in the second,
+// one wave per sequence finds the block in the blocks' prefix sums and the token within the block.
+// No wave waits for another, so there are no barriers and no LDS.
 //
 // Sums are 64 bit in a fixed order: a token's share can be 10^-8 of the sum, less than 32 bits
 // resolve next to it, and the result is the same on every run.
+#include <algorithm>
+
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -20,47 +23,90 @@ namespace kda {
 
 namespace {
 
-constexpr int kBlock = 2048;  // tokens per block sum: 8 of each of 256 threads
+constexpr int kBlock = 1024;  // tokens per block sum: 16 of each lane
 
 __device__ __forceinline__ float weight_of(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
+__device__ __forceinline__ float uniform_of(float u) { return u > 0.f ? u < 1.f ? u : 0x1.fffffep-1f : 0.f; }
 
-// Drafts of sequence n that stand; every thread of the workgroup gets it. (Threads take drafts
-// t, t + 256, ...; the first that falls counts.)
+__device__ __forceinline__ int draft_count(const VerifyPlan& v, int n) {
+  return v.n_drafts ? min(max(v.n_drafts[n], 0), v.m) : v.m;
+}
+
+// Drafts of sequence n that stand; one wave, 64 drafts at a time.
 template <typename T>
-__device__ __forceinline__ int standing(const VerifyPlan& v, int n, int count, int* s_first) {
+__device__ __forceinline__ int standing(const VerifyPlan& v, int n, int count) {
   const T* p = static_cast<const T*>(v.p) + n * v.p_seq;
-  const T* q = static_cast<const T*>(v.q);
-  if (threadIdx.x == 0) *s_first = count;
-  __syncthreads();
-  for (int j = threadIdx.x; j < count; j += 256) {
-    const int x = v.drafts[(int64_t)n * v.m + j];
-    bool stands = x >= 0 && x < v.V;
-    if (stands) {
-      const float px = ld(p, j * v.p_row + x);
-      const float qx = q ? ld(q + n * v.q_seq, j * v.q_row + x) : 1.f;
-      float u = v.uniform[(int64_t)n * (v.m + 1) + j];
-      u = u > 0.f ? u < 1.f ? u : 0x1.fffffep-1f : 0.f;
-      stands = fabsf(px) < INFINITY && fabsf(qx) < INFINITY && (double)u * (double)qx < (double)px;
+  const T* q = v.q ? static_cast<const T*>(v.q) + n * v.q_seq : nullptr;
+  for (int j0 = 0; j0 < count; j0 += 64) {
+    const int j = j0 + (threadIdx.x & 63);
+    bool falls = false;
+    if (j < count) {
+      const int x = v.drafts[(int64_t)n * v.m + j];
+      const float u = uniform_of(v.uniform[(int64_t)n * (v.m + 1) + j]);
+      falls = x < 0 || x >= v.V;
+      if (!falls) {
+        const float px = ld(p, j * v.p_row + x), qx = q ? ld(q, j * v.q_row + x) : 1.f;
+        falls = !(fabsf(px) < INFINITY && fabsf(qx) < INFINITY && (double)u * (double)qx < (double)px);
+      }
     }
-    if (!stands) atomicMin(s_first, j);
+    const uint64_t fallen = __ballot(falls);
+    if (fallen) return j0 + __builtin_ctzll(fallen);
   }
-  __syncthreads();
-  return *s_first;
+  return count;
+}
+
+// N neighbouring values of a row as floats, whatever the row's alignment (streamed).
+template <int N>
+__device__ __forceinline__ void load_row(const float* p, float* x) {
+  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const vec y = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + i));
+    x[i] = y[0], x[i + 1] = y[1], x[i + 2] = y[2], x[i + 3] = y[3];
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_row(const uint16_t* p, float* x) {
+  typedef uint16_t vec __attribute__((ext_vector_type(N < 8 ? N : 8), aligned(2)));
+  constexpr int W = N < 8 ? N : 8;
+#pragma unroll
+  for (int i = 0; i < N; i += W) {
+    const vec y = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p + i));
+#pragma unroll
+    for (int k = 0; k < W; ++k) x[i + k] = bf16_bits_to_f32(y[k]);
+  }
 }
 
 // The weights that decide: w = max(p - q, 0), and p in case they are all zero.
 template <typename T>
 struct Weights {
-  const T *p, *q;  // rows; q NULL: nothing to take off, except at token x
+  const T *p, *q;  // rows; q NULL: nothing to take off, except 1 at token x
   int x;           // the draft that fell, if it was picked; -1 otherwise
-  __device__ __forceinline__ void at(int i, double& w, double& all) const {
-    const float pi = weight_of(ld(p, i));
-    all = pi;
-    if (q) {
-      const double d = (double)pi - (double)weight_of(ld(q, i));
-      w = d > 0.0 ? d : 0.0;
+  int V;
+  // of tokens i .. i + N - 1 (0 past the vocabulary)
+  template <int N>
+  __device__ __forceinline__ void at(int i, double* w, double* all) const {
+    float a[N], b[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) a[k] = b[k] = 0.f;
+    if (i + N <= V) {
+      load_row<N>(p + i, a);
+      if (q) load_row<N>(q + i, b);
     } else {
-      w = i == x ? fmax((double)pi - 1.0, 0.0) : (double)pi;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (i + k < V) {
+          a[k] = ld(p, i + k);
+          if (q) b[k] = ld(q, i + k);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const double pk = weight_of(a[k]);
+      const double d = pk - (double)(i + k == x ? 1.f : weight_of(b[k]));
+      w[k] = d > 0.0 ? d : 0.0;
+      all[k] = pk;
     }
   }
 };
@@ -71,11 +117,8 @@ __device__ __forceinline__ Weights<T> weights(const VerifyPlan& v, int n, int a,
   w.p = static_cast<const T*>(v.p) + n * v.p_seq + a * v.p_row;
   w.q = a < count && v.q ? static_cast<const T*>(v.q) + n * v.q_seq + a * v.q_row : nullptr;
   w.x = a < count && !v.q ? v.drafts[(int64_t)n * v.m + a] : -1;
+  w.V = v.V;
   return w;
-}
-
-__device__ __forceinline__ int draft_count(const VerifyPlan& v, int n) {
-  return v.n_drafts ? min(max(v.n_drafts[n], 0), v.m) : v.m;
 }
 
 __device__ __forceinline__ double wave_sum(double x) {
@@ -84,154 +127,116 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
-// Grid: x over blocks of kBlock tokens, then sequences. sums[n][block] = {sum w, sum p}.
+// Four waves per workgroup, `waves` per sequence; wave i of a sequence sums blocks i, i + waves, ...
+// into sums[n][block] = {sum of w, sum of p}.
 template <typename T>
-__global__ __launch_bounds__(256) void verify_sums_kernel(const VerifyPlan v, int blocks) {
-  __shared__ int s_first;
-  __shared__ double s_part[2][4];
-  const int n = blockIdx.x / blocks, b = blockIdx.x % blocks;
-  const int t = threadIdx.x;
+__global__ __launch_bounds__(256) void verify_sums_kernel(const VerifyPlan v, int blocks, int waves) {
+  constexpr int N = 8;  // tokens per lane and step: neighbouring lanes, neighbouring tokens
+  const int lane = threadIdx.x & 63;
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = (int)(wave / waves), first = (int)(wave - (int64_t)n * waves);
+  if (n >= v.N) return;
   const int count = draft_count(v, n);
-  const int a = standing<T>(v, n, count, &s_first);
+  const int a = __builtin_amdgcn_readfirstlane(standing<T>(v, n, count));
+  if (first == 0 && lane == 0) v.accept[n] = a;
   const Weights<T> row = weights<T>(v, n, a, count);
-  double w = 0.0, all = 0.0;
+  double* out = static_cast<double*>(v.workspace) + (int64_t)n * blocks * 2;
+  for (int b = first; b < blocks; b += waves) {
+    double w = 0.0, all = 0.0;
 #pragma unroll
-  for (int c = 0; c < kBlock / 256; ++c) {
-    const int i = b * kBlock + c * 256 + t;
-    if (i < v.V) {
-      double wi, pi;
-      row.at(i, wi, pi);
-      w += wi;
-      all += pi;
+    for (int c = 0; c < kBlock; c += 64 * N) {
+      double wk[N], pk[N];
+      row.template at<N>(b * kBlock + c + lane * N, wk, pk);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        w += wk[k];
+        all += pk[k];
+      }
     }
-  }
-  w = wave_sum(w);
-  all = wave_sum(all);
-  if ((t & 63) == 0) {
-    s_part[0][t >> 6] = w;
-    s_part[1][t >> 6] = all;
-  }
-  __syncthreads();
-  if (t < 2) {
-    double* out = static_cast<double*>(v.workspace) + ((int64_t)n * blocks + b) * 2;
-    out[t] = (s_part[t][0] + s_part[t][1]) + (s_part[t][2] + s_part[t][3]);
+    w = wave_sum(w);
+    all = wave_sum(all);
+    if (lane < 2) out[2 * (int64_t)b + lane] = lane ? all : w;
   }
 }
 
-// The first index i < count (in order) whose running sum base + x_0 + ... + x_i exceeds the
-// threshold; thread t holds elements [t * K, t * K + K). If none does, the last positive one; -1
-// if none is positive. *base_out: the sum before it. Every thread gets the result.
-template <int K>
-__device__ int find_first(const double* x, double base, double threshold, double* s_w, int* s_idx,
-                          double* base_out) {
-  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
-  double own = 0.0;
-#pragma unroll
-  for (int k = 0; k < K; ++k) own += x[k];
-  double incl = own;
+// Where a wave's running sum passes a threshold: the first lane with a positive x and base + x_0 +
+// ... + x_lane > threshold; if rounding lets none pass, the last with a positive x; -1 if there
+// is none. *before: base and the sum ahead of that lane.
+__device__ __forceinline__ int find_lane(double x, double base, double threshold, double* before) {
+  const int lane = threadIdx.x & 63;
+  double incl = x;
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
     const double y = __shfl_up(incl, s, 64);
     if (lane >= s) incl += y;
   }
-  if (lane == 63) s_w[wv] = incl;
-  if (t == 0) s_idx[0] = 0x7fffffff, s_idx[1] = -1;
-  __syncthreads();
-  double run = base;
-  for (int i = 0; i < wv; ++i) run += s_w[i];
-  run += incl - own;
-  double prev = run;
-  int hit = 0x7fffffff, lastpos = -1;
-  double hit_base = 0.0, last_base = 0.0;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (x[k] > 0.0) {
-      lastpos = t * K + k;
-      last_base = prev;
-      if (hit == 0x7fffffff && prev + x[k] > threshold) {
-        hit = t * K + k;
-        hit_base = prev;
-      }
-    }
-    prev += x[k];
-  }
-  if (hit != 0x7fffffff) atomicMin(&s_idx[0], hit);
-  if (lastpos >= 0) atomicMax(&s_idx[1], lastpos);
-  __syncthreads();
-  const int found = s_idx[0] != 0x7fffffff ? s_idx[0] : s_idx[1];
-  if (found >= 0 && found / K == t) s_w[4] = s_idx[0] != 0x7fffffff ? hit_base : last_base;
-  __syncthreads();
-  *base_out = s_w[4];
+  const uint64_t some = __ballot(x > 0.0), past = __ballot(x > 0.0 && base + incl > threshold);
+  if (!some) return -1;
+  const int found = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+  const double ahead = __shfl(incl, max(found - 1, 0), 64);
+  *before = base + (found ? ahead : 0.0);
   return found;
 }
 
-// One workgroup per sequence.
+// One wave per sequence.
 template <typename T>
-__global__ __launch_bounds__(256) void verify_pick_kernel(const VerifyPlan v, int blocks) {
-  __shared__ int s_first, s_idx[2];
-  __shared__ double s_w[5];
-  const int n = blockIdx.x, t = threadIdx.x;
-  const int count = draft_count(v, n);
-  const int a = standing<T>(v, n, count, &s_first);
-  const Weights<T> row = weights<T>(v, n, a, count);
+__global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyPlan v, int blocks) {
+  constexpr int K = kBlock / 64;
+  const int n = blockIdx.x, lane = threadIdx.x;
   const double* sums = static_cast<const double*>(v.workspace) + (int64_t)n * blocks * 2;
+  const int count = draft_count(v, n), a = v.accept[n];
+  const float u = uniform_of(v.uniform[(int64_t)n * (v.m + 1) + v.m]);
+  const Weights<T> row = weights<T>(v, n, a, count);
 
-  // totals, and whether w has anything
+  // each lane a run of blocks
+  const int per = (blocks + 63) / 64, b0 = min(lane * per, blocks), b1 = min(b0 + per, blocks);
   double w = 0.0, all = 0.0;
-  for (int i = t; i < blocks; i += 256) {
-    w += sums[2 * i];
-    all += sums[2 * i + 1];
+  for (int b = b0; b < b1; ++b) {
+    w += sums[2 * (int64_t)b];
+    all += sums[2 * (int64_t)b + 1];
   }
-  w = wave_sum(w);
-  all = wave_sum(all);
-  if ((t & 63) == 0) s_w[t >> 6] = w;
-  __syncthreads();
-  const double total_w = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
-  __syncthreads();
-  if ((t & 63) == 0) s_w[t >> 6] = all;
-  __syncthreads();
-  const double total_p = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
-  __syncthreads();
-  const int which = total_w > 0.0 ? 0 : 1;
-  const double total = which ? total_p : total_w;
+  const double total_w = wave_sum(w), total_p = wave_sum(all);
+  const int which = total_w > 0.0 ? 0 : 1;  // 1: no weight is positive, p itself
+  const double threshold = (double)u * (which ? total_p : total_w);
 
   int next = -1;
-  if (total > 0.0) {
-    float u = v.uniform[(int64_t)n * (v.m + 1) + v.m];
-    u = u > 0.f ? u < 1.f ? u : 0x1.fffffep-1f : 0.f;
-    const double threshold = (double)u * total;
-    // the block: 256 blocks at a time, each thread one. The first whose running sum passes the
-    // threshold, or (if rounding lets none pass) the last that has any weight.
-    double base = 0.0, block_base = 0.0;
+  double base;
+  const int owner = find_lane(which ? all : w, 0.0, threshold, &base);
+  if (owner >= 0) {
+    // the block among that lane's
     int block = -1;
-    for (int b0 = 0; b0 < blocks; b0 += 256) {
-      const double x = b0 + t < blocks ? sums[2 * (b0 + t) + which] : 0.0;
-      double before;
-      const int f = find_first<1>(&x, base, threshold, s_w, s_idx, &before);
-      if (f < 0) continue;
-      block = b0 + f;
-      block_base = before;
-      base = before + sums[2 * block + which];
-      if (base > threshold) break;
-    }
-    // the token within it
-    if (block >= 0) {
-      constexpr int K = kBlock / 256;
-      double x[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int i = block * kBlock + t * K + k;
-        double wi = 0.0, pi = 0.0;
-        if (i < v.V) row.at(i, wi, pi);
-        x[k] = which ? pi : wi;
+    double block_base = base;
+    for (int b = owner * per; b < min((owner + 1) * per, blocks); ++b) {
+      const double s = sums[2 * (int64_t)b + which];
+      if (s > 0.0) {
+        block = b;
+        block_base = base;
+        if (base + s > threshold) break;
       }
-      double before;
-      next = find_first<K>(x, block_base, threshold, s_w, s_idx, &before);
-      if (next >= 0) next += block * kBlock;
+      base += s;
     }
+    // the token within it: each lane K neighbouring ones
+    double wk[K], pk[K], sum = 0.0;
+    row.template at<K>(block * kBlock + lane * K, wk, pk);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      wk[k] = which ? pk[k] : wk[k];
+      sum += wk[k];
+    }
+    const int at = find_lane(sum, block_base, threshold, &base);
+    int mine = -1;
+    bool passed = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!passed && wk[k] > 0.0) {
+        mine = k;
+        passed = base + wk[k] > threshold;
+      }
+      base += wk[k];
+    }
+    next = block * kBlock + at * K + __shfl(mine, max(at, 0), 64);
   }
-  if (t == 0) v.accept[n] = a;
-  for (int j = t; j <= v.m; j += 256)
+  for (int j = lane; j <= v.m; j += 64)
     v.tokens[(int64_t)n * (v.m + 1) + j] =
         j < a ? v.drafts[(int64_t)n * v.m + j] : j == a ? next : -1;
 }
@@ -241,11 +246,13 @@ int64_t row_blocks(int V) { return ((int64_t)V + kBlock - 1) / kBlock; }
 template <typename T>
 hipError_t launch_t(const VerifyPlan& p, hipStream_t stream) {
   const int blocks = (int)row_blocks(p.V);
-  hipLaunchKernelGGL(verify_sums_kernel<T>, dim3((unsigned)((int64_t)blocks * p.N)), dim3(256), 0,
-                     stream, p, blocks);
+  // as many waves as the 256 CUs hold (32 each), and never more than there are blocks
+  const int waves = (int)std::min<int64_t>(blocks, std::max<int64_t>(1, 8192 / p.N));
+  hipLaunchKernelGGL(verify_sums_kernel<T>, dim3((unsigned)(((int64_t)waves * p.N + 3) / 4)), dim3(256), 0,
+                     stream, p, blocks, waves);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(verify_pick_kernel<T>, dim3((unsigned)p.N), dim3(256), 0, stream, p, blocks);
+  hipLaunchKernelGGL(verify_pick_kernel<T>, dim3((unsigned)p.N), dim3(64), 0, stream, p, blocks);
   return hipGetLastError();
 }
 
