@@ -369,95 +369,27 @@ def check_gates(g, beta, stream=None, counts=None) -> int:
     return int(n.value)
 
 
-# ---- the layers beside KDA: a paged key/value cache, and the verification of drafts
+# ---- the layers beside KDA: a paged key/value cache, and the verification of drafts. The tensors
+#      are marshalled in csrc/torch/marshal.cpp (built as _marshal.so).
 
-_CACHE_DTYPES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16,
-                 torch.float8_e4m3fn: KDA_F8E4M3}
-
-
-def _on(device: torch.device, **tensors):
-    """Every tensor given (None is skipped) lies on `device`, a GPU."""
-    if device.type != "cuda":
-        raise ValueError("tensors must be on the GPU")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+_ops = None
 
 
-def _contiguous(dtype: torch.dtype, shape, **tensors):
-    """Every tensor given (None is skipped) is contiguous, of this dtype and shape."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}")
-        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}")
-
-
-def _heads(name: str, t: torch.Tensor, dtype: torch.dtype, lead, d: int):
-    """(token stride, head stride) of a [*lead, heads, d] view whose tokens lie evenly apart."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != 4 or tuple(t.shape[:2]) != tuple(lead) or t.shape[3] != d:
-        raise ValueError(f"{name} must be of shape [{lead[0]}, {lead[1]}, heads, {d}]")
-    s0, s1, s2, s3 = t.stride()
-    B, T, H = t.shape[:3]
-    if t.numel() == 0:
-        return H * d, d
-    if s3 != 1 or (B > 1 and T > 1 and s0 != T * s1):
-        raise ValueError(f"{name} must have contiguous channels and evenly spaced tokens")
-    return (s1 if T > 1 else s0 if B > 1 else H * d), (s2 if H > 1 else d)
-
-
-def _page_cache(k_cache, v_cache, block_table, k_scale, v_scale, n_seq: int, Hkv: int, d: int):
-    if k_cache.dtype not in _CACHE_DTYPES or v_cache.dtype != k_cache.dtype:
-        raise TypeError("k_cache and v_cache must both be float32, bfloat16 or float8_e4m3fn")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or tuple(k_cache.shape[2:]) != (Hkv, d):
-        raise ValueError(f"k_cache and v_cache must be of shape [pages, page_size, {Hkv}, {d}]")
-    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
-        raise ValueError("k_cache and v_cache must have contiguous channels")
-    if block_table.dtype != torch.int32:
-        raise TypeError("block_table must be int32")
-    if block_table.dim() != 2 or block_table.shape[0] != n_seq or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError(f"block_table must be of shape [{n_seq}, max_pages], pages side by side")
-    _contiguous(torch.float32, (Hkv,), k_scale=k_scale, v_scale=v_scale)
-    ks, vs = k_cache.stride(), v_cache.stride()
-    return PageCache(k_cache.data_ptr(), v_cache.data_ptr(), _CACHE_DTYPES[k_cache.dtype],
-                     k_cache.shape[0], k_cache.shape[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                     block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
-                     None if k_scale is None else k_scale.data_ptr(),
-                     None if v_scale is None else v_scale.data_ptr())
-
-
-def _call(fn, args, device: torch.device, stream):
-    """Calls fn on the stream given, or the device's current one, with that device current."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(fn, args, device, stream)
-    s = torch.cuda.current_stream() if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"the stream must be of {device}")
-    _check(fn(ctypes.byref(args), s.cuda_stream))
-
-
-def _scratch(query, args, workspace, device: torch.device, stream):
-    """Sets args.workspace: the caller's, or a new one of the size asked for."""
-    if workspace is None:
-        n = query(ctypes.byref(args))
-        if n == SIZE_MAX:
-            return  # the call itself says what is wrong
-        if n == 0:
-            return
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
-        if stream is not None:  # its memory is not handed out again before that stream is done
-            workspace.record_stream(stream)
-    else:
-        _dev(workspace, "workspace")
-        _on(device, workspace=workspace)
-    args.workspace = workspace.data_ptr()
-    args.workspace_bytes = workspace.numel() * workspace.element_size()
+def _marshal():
+    """The built marshalling module, bound to the loaded libkda; raises if it has not been built."""
+    global _ops
+    if _ops is None:
+        L = lib()
+        try:
+            from . import _marshal as ops
+        except ImportError as e:
+            raise RuntimeError(f"the marshalling module is not built ({e}); run "
+                               "python -m gated_delta_rule_59_amd.build") from e
+        ops.bind(*[ctypes.cast(f, _P).value for f in (
+            L.kda_kv_append, L.kda_paged_decode, L.kda_paged_decode_workspace_bytes,
+            L.kda_verify_drafts, L.kda_verify_drafts_workspace_bytes, L.kda_last_error)], KDAError)
+        _ops = ops
+    return _ops
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, start, *, q=None, q_out=None, inv_freq=None,
@@ -470,76 +402,15 @@ def kv_append(k, v, k_cache, v_cache, block_table, start, *, q=None, q_out=None,
     in halves or, interleaved, in neighbouring pairs. Returns the turned q [B, T, Hq, d] (in q_out
     if given, which may be q), or None without q. k, v, q and the caches may be strided views with
     contiguous channels. See kda_kv_append_args for what out-of-range positions and pages mean."""
-    B, T, Hkv, d = k.shape
-    dev = k.device
-    _on(dev, v=v, q=q, q_out=q_out, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-        start=start, inv_freq=inv_freq, cu_seqlens=cu_seqlens, k_scale=k_scale, v_scale=v_scale)
-    n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    _contiguous(torch.int32, (n_seq,), start=start)
-    if cu_seqlens is not None:
-        _contiguous(torch.int32, (n_seq + 1,), cu_seqlens=cu_seqlens)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _contiguous(torch.float32, (rot // 2,), inv_freq=inv_freq)
-    a = KvAppendArgs()
-    a.B, a.T, a.Hkv, a.d = B, T, Hkv, d
-    a.act_dtype = _dtype_code(k.dtype)
-    a.k_token_stride, a.k_head_stride = _heads("k", k, k.dtype, (B, T), d)
-    a.v_token_stride, a.v_head_stride = _heads("v", v, k.dtype, (B, T), d)
-    if v.shape != k.shape:
-        raise ValueError("k and v must have the same shape")
-    a.k, a.v, a.start, a.rot = k.data_ptr(), v.data_ptr(), start.data_ptr(), rot
-    a.flags = KDA_APPEND_PAIRS if interleaved else 0
-    if rot:
-        a.inv_freq = inv_freq.data_ptr()
-    if cu_seqlens is not None:
-        a.cu_seqlens, a.N = cu_seqlens.data_ptr(), n_seq
-    if q is not None:
-        a.q_token_stride, a.q_head_stride = _heads("q", q, k.dtype, (B, T), d)
-        a.Hq = q.shape[2]
-        if q_out is None:
-            q_out = torch.empty((B, T, a.Hq, d), dtype=q.dtype, device=dev)
-            if stream is not None:
-                q_out.record_stream(stream)
-        else:
-            _contiguous(q.dtype, q.shape, q_out=q_out)
-        a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    a.cache = _page_cache(k_cache, v_cache, block_table, k_scale, v_scale, n_seq, Hkv, d)
-    _call(lib().kda_kv_append, a, dev, stream)
-    return q_out
-
-
-def _paged_decode_args(q, k_cache, v_cache, block_table, seq_lens, scale, window, max_len, k_scale,
-                       v_scale, out_dtype):
-    N, m, Hq, d = q.shape
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must be of shape [pages, page_size, Hkv, d]")
-    _on(q.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
-        k_scale=k_scale, v_scale=v_scale)
-    _contiguous(torch.int32, (N,), seq_lens=seq_lens)
-    a = PagedDecodeArgs()
-    a.N, a.m, a.Hq, a.Hkv, a.d = N, m, Hq, k_cache.shape[2], d
-    a.act_dtype, a.out_dtype = _dtype_code(q.dtype), _dtype_code(out_dtype)
-    a.q_token_stride, a.q_head_stride = _heads("q", q, q.dtype, (N, m), d)
-    a.cache = _page_cache(k_cache, v_cache, block_table, k_scale, v_scale, N, k_cache.shape[2], d)
-    a.q, a.seq_lens = q.data_ptr(), seq_lens.data_ptr()
-    room = block_table.shape[1] * k_cache.shape[1]
-    a.max_len = min(room, 1 << 30) if max_len is None else max_len
-    a.window = window
-    a.scale = d ** -0.5 if scale is None else scale
-    return a
+    return (_ops or _marshal()).kv_append(k, v, k_cache, v_cache, block_table, start, q, q_out, inv_freq,
+                                          interleaved, cu_seqlens, k_scale, v_scale, stream)
 
 
 def paged_decode_workspace_bytes(q, k_cache, v_cache, block_table, seq_lens, *, window=0,
-                                 max_len=None, **_) -> int:
+                                 max_len=None, k_scale=None, v_scale=None) -> int:
     """Bytes of workspace that paged_decode needs for these arguments."""
-    a = _paged_decode_args(q, k_cache, v_cache, block_table, seq_lens, None, window, max_len, None,
-                           None, torch.float32)
-    n = lib().kda_paged_decode_workspace_bytes(ctypes.byref(a))
-    if n == SIZE_MAX:
-        raise KDAError(2, lib().kda_last_error().decode())
-    return int(n)
+    return _marshal().paged_decode(q, k_cache, v_cache, block_table, seq_lens, None, window, max_len,
+                                   k_scale, v_scale, None, None, torch.float32, False, None)
 
 
 def paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, window=0, max_len=None,
@@ -552,34 +423,8 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale=None, wind
     them; a row that sees nothing gives 0. scale defaults to d^-0.5; max_len (a bound on seq_lens,
     by default what block_table holds) shapes the launch. lse fp32 [N, m, Hq], if given, receives
     the logarithm of the sum of exponentials. Returns o [N, m, Hq, d] of out_dtype."""
-    if o is not None:
-        out_dtype = o.dtype
-        _contiguous(out_dtype, q.shape, o=o)
-    a = _paged_decode_args(q, k_cache, v_cache, block_table, seq_lens, scale, window, max_len,
-                           k_scale, v_scale, out_dtype)
-    dev = q.device
-    if o is None:
-        o = torch.empty(q.shape, dtype=out_dtype, device=dev)
-        if stream is not None:
-            o.record_stream(stream)
-    _contiguous(torch.float32, q.shape[:3], lse=lse)
-    _on(dev, o=o, lse=lse)
-    a.o = o.data_ptr()
-    if lse is not None:
-        a.lse = lse.data_ptr()
-    L = lib()
-    _scratch(L.kda_paged_decode_workspace_bytes, a, workspace, dev, stream)
-    _call(L.kda_paged_decode, a, dev, stream)
-    return o
-
-
-def _rows(name: str, t: torch.Tensor, dtype, shape):
-    """(sequence stride, row stride) of a [N, rows, V] view with contiguous rows."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != shape or (shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be of shape {shape} with contiguous rows")
-    return t.stride(0), t.stride(1)
+    return (_ops or _marshal()).paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, window, max_len,
+                                             k_scale, v_scale, o, lse, out_dtype, workspace, stream)
 
 
 def verify_drafts(p, q, drafts, uniform, *, n_drafts=None, accept=None, tokens=None,
@@ -590,36 +435,4 @@ def verify_drafts(p, q, drafts, uniform, *, n_drafts=None, accept=None, tokens=N
     [N, m + 1] in [0, 1), n_drafts int32 [N]: how many of the m there are (default all).
     Returns (accept int32 [N], tokens int32 [N, m + 1]): the drafts that stand, and those drafts,
     the following token, then -1. accept is the `accept` of a decode_multi over the drafts."""
-    if p.dim() != 3 or drafts.dim() != 2:
-        raise ValueError("p must be [N, m + 1, V] and drafts [N, m]")
-    N, m = drafts.shape
-    V = p.shape[2]
-    dev = p.device
-    _on(dev, p=p, q=q, drafts=drafts, uniform=uniform, n_drafts=n_drafts, accept=accept,
-        tokens=tokens)
-    a = VerifyArgs()
-    a.N, a.m, a.V, a.dtype = N, m, V, _dtype_code(p.dtype)
-    a.p_seq_stride, a.p_row_stride = _rows("p", p, p.dtype, (N, m + 1, V))
-    a.p = p.data_ptr()
-    if q is not None:
-        a.q_seq_stride, a.q_row_stride = _rows("q", q, p.dtype, (N, m, V))
-        a.q = q.data_ptr()
-    _contiguous(torch.int32, (N, m), drafts=drafts)
-    _contiguous(torch.float32, (N, m + 1), uniform=uniform)
-    _contiguous(torch.int32, (N,), n_drafts=n_drafts, accept=accept)
-    _contiguous(torch.int32, (N, m + 1), tokens=tokens)
-    if accept is None:
-        accept = torch.empty((N,), dtype=torch.int32, device=dev)
-    if tokens is None:
-        tokens = torch.empty((N, m + 1), dtype=torch.int32, device=dev)
-    if stream is not None:
-        accept.record_stream(stream)
-        tokens.record_stream(stream)
-    a.drafts, a.uniform = drafts.data_ptr(), uniform.data_ptr()
-    a.accept, a.tokens = accept.data_ptr(), tokens.data_ptr()
-    if n_drafts is not None:
-        a.n_drafts = n_drafts.data_ptr()
-    L = lib()
-    _scratch(L.kda_verify_drafts_workspace_bytes, a, workspace, dev, stream)
-    _call(L.kda_verify_drafts, a, dev, stream)
-    return accept, tokens
+    return (_ops or _marshal()).verify_drafts(p, q, drafts, uniform, n_drafts, accept, tokens, workspace, stream)

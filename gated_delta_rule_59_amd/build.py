@@ -2,7 +2,8 @@
 
     python -m gated_delta_rule_59_amd.build
 
-hipcc compiles every source under csrc/ and links one shared library, libkda.so.
+hipcc compiles every source under csrc/ and links one shared library, libkda.so. The host
+compiler builds csrc/torch/marshal.cpp, which marshals torch tensors into it, as _marshal.so.
 """
 from __future__ import annotations
 
@@ -24,6 +25,24 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-munsafe-fp-at
          "-Wall", "-Wno-unused-function", "-I", INCLUDE]
 
 
+MARSHAL = os.path.join(HERE, "_marshal.so")
+CXX = os.environ.get("CXX", "g++")
+
+
+def marshal_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    lib = os.path.join(root, "lib")
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__",
+            "-DUSE_ROCM", "-Wall", "-Wno-attributes", "-I", INCLUDE, *[f"-isystem{d}" for d in dirs],
+            os.path.join(CSRC, "torch", "marshal.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10", "-lc10_hip", f"-Wl,-rpath,{lib}"]
+
+
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
@@ -32,6 +51,9 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     procs, objs = [], []
+    marshal = MARSHAL + ".tmp%d" % os.getpid()
+    procs.append(("marshal.cpp", subprocess.Popen(marshal_command(marshal), stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT)))
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         objs.append(obj)
@@ -46,6 +68,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    os.replace(marshal, MARSHAL)
     return LIB
 
 
@@ -56,7 +79,7 @@ def _wait(item):
     lines = [l for l in text.splitlines() if "packed-fp32-ops" not in l and l.strip()]
     if p.returncode != 0:
         sys.stderr.write(text)
-        raise RuntimeError(f"hipcc failed for {src}")
+        raise RuntimeError(f"the compiler failed for {src}")
     if lines:
         sys.stderr.write("\n".join(lines) + "\n")
 

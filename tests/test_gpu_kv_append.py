@@ -241,3 +241,32 @@ def test_captured_and_replayed_on_another_stream():
     q2 = binding.kv_append(**dev, stream=s)
     s.synchronize()
     assert torch.equal(q2, want) and torch.equal(dev["v_cache"], ref["v_cache"])
+
+
+def test_binding_refuses_what_it_cannot_pass_on():
+    import torch
+    from gated_delta_rule_59_amd import binding
+    dev, _ = make((58, 1), [4, 90], [3, 3], 4, 2, 64, 64, 16, "bf16", "bf16")
+    call = lambda **kw: binding.kv_append(**{**dev, **kw})  # noqa: E731
+    wide = torch.zeros((2, 5, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for error, match, kw in [
+            (ValueError, "evenly", dict(k=wide[:, :3])), (TypeError, "q must be", dict(q=dev["q"].float())),
+            (TypeError, "start", dict(start=dev["start"].long())), (ValueError, "start", dict(start=dev["start"][:1])),
+            (ValueError, "must be on", dict(start=dev["start"].cpu())),
+            (ValueError, "must be on", dict(k_cache=dev["k_cache"].cpu())),
+            (TypeError, "k_cache", dict(k_cache=dev["k_cache"].half())),
+            (ValueError, "k_cache", dict(k_cache=dev["k_cache"][:, :, :1])),
+            (ValueError, "channels", dict(v_cache=dev["v_cache"].transpose(2, 3).contiguous().transpose(2, 3))),
+            (TypeError, "block_table", dict(block_table=dev["block_table"].long())),
+            (ValueError, "block_table", dict(block_table=dev["block_table"][:1])),
+            (ValueError, "q_out", dict(q_out=torch.empty_like(wide))), (ValueError, "q_out needs q", dict(q=None, q_out=dev["q"])),
+            (binding.KDAError, "F8E4M3", dict(k_scale=torch.ones(2, device="cuda"))),
+            (binding.KDAError, "rot", dict(inv_freq=torch.ones(40, device="cuda"))),
+            (binding.KDAError, "overlaps", dict(q_out=dev["k_cache"].view(-1)[:dev["q"].numel()].view(dev["q"].shape)))]:
+        with pytest.raises(error, match=match):
+            call(**kw)
+    with pytest.raises(binding.KDAError) as e:
+        call(inv_freq=torch.ones(20, device="cuda"))
+    assert e.value.status == 2
+    torch.cuda.synchronize()
+    assert (dev["k_cache"] == FILL).all()

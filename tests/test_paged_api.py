@@ -196,13 +196,10 @@ def test_binding_checks_tensors_first(b):
         b.paged_decode(z(1, 1, 1, 32), z(1, 16, 1, 32), z(1, 16, 1, 32), z(1, 1, **i32), z(1, **i32))
     with pytest.raises(ValueError, match="GPU"):
         b.verify_drafts(z(1, 2, 5), z(1, 1, 5), z(1, 1, **i32), z(1, 2))
-    with pytest.raises(TypeError, match="int32"):
-        b._page_cache(z(1, 16, 1, 32), z(1, 16, 1, 32), z(1, 1), None, None, 1, 1, 32)
-    with pytest.raises(ValueError, match="evenly"):
-        b._heads("k", z(4, 5, 2, 32)[:, :3], torch.float32, (4, 3), 32)
-    assert b._heads("k", z(4, 3, 6, 32)[:, :, 2:4], torch.float32, (4, 3), 32) == (192, 32)
-    assert b._heads("k", z(4, 1, 6, 32)[:, :, 2:4], torch.float32, (4, 1), 32) == (192, 32)
-    assert b._heads("k", z(1, 1, 1, 32), torch.float32, (1, 1), 32) == (32, 32)
+    with pytest.raises(TypeError, match="k_cache"):
+        b.kv_append(z(1, 1, 1, 32), z(1, 1, 1, 32), None, z(1, 16, 1, 32), z(1, 1, **i32), z(1, **i32))
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        b.verify_drafts([[0.5]], None, z(1, 1, **i32), z(1, 2))
 
 
 def test_reference_attention_worked_example():
