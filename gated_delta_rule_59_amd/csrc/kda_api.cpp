@@ -524,6 +524,12 @@ kda_status kda_kv_append(const kda_kv_append_args* a, void* hip_stream) {
   Range kc{}, vc{};
   s = validate_cache(a->cache, a->Hkv, a->d, &kc, &vc);
   if (s != KDA_OK) return s;
+  // rows that are written lie apart (an expanded view's do not)
+  const kda_page_cache& c = a->cache;
+  if ((c.num_pages > 1 && std::min(c.k_page_stride, c.v_page_stride) < a->d) ||
+      (c.page_size > 1 && std::min(c.k_token_stride, c.v_token_stride) < a->d) ||
+      (a->Hkv > 1 && std::min(c.k_head_stride, c.v_head_stride) < a->d))
+    return fail(KDA_ERR_BAD_SHAPE, "cache rows overlap: strides below d = %d", a->d);
   if (!a->start || (tok > 0 && (!a->k || !a->v)))
     return fail(KDA_ERR_NULL_PTR, "k, v and start must be non-NULL");
   const size_t es = dsize(a->act_dtype);

@@ -129,16 +129,15 @@ __device__ __forceinline__ bf16x8 e4m3_operand(uint32_t w0, uint32_t w1) {
                                           e4m3_bf16<false>(w1), e4m3_bf16<true>(w1)});
 }
 
-// Whether a word of cached values holds an infinity or a NaN.
+// A word of cached values holds an infinity or a NaN if ((w & kMagnitude) + kStep) & kOver: adding
+// a step to a magnitude whose exponent (e4m3, which has no infinities: all bits) is all ones
+// carries into the sign's place and no further.
 template <int CT>
-__device__ __forceinline__ bool not_finite(uint32_t w) {
-  if constexpr (CT == kF32) return (w & 0x7f800000u) == 0x7f800000u;
-  if constexpr (CT == kBF16) return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-  // e4m3 has no infinities; NaN is all ones but the sign
-  if constexpr (CT == kF8)
-    return (w & 0x7fu) == 0x7fu || (w & 0x7f00u) == 0x7f00u || (w & 0x7f0000u) == 0x7f0000u ||
-           (w & 0x7f000000u) == 0x7f000000u;
-}
+struct NotFinite {
+  static constexpr uint32_t kMagnitude = CT == kF32 ? 0x7fffffffu : CT == kBF16 ? 0x7fff7fffu : 0x7f7f7f7fu;
+  static constexpr uint32_t kStep = CT == kF32 ? 0x00800000u : CT == kBF16 ? 0x00800080u : 0x01010101u;
+  static constexpr uint32_t kOver = ~kMagnitude;
+};
 
 // The VEC channels of a lane's words of a value row, as floats.
 template <int CT, int VEC>
@@ -286,38 +285,22 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     n = __builtin_amdgcn_readfirstlane(n);
     pair = __builtin_amdgcn_readfirstlane(pair);
     u_first = __builtin_amdgcn_readfirstlane(u_first);
-    len = __builtin_amdgcn_readfirstlane(len);
-    const int next_len = seq_len(p, min(n + 1, p.N - 1));
-    const int un = seq_units(p, len);
-    const int cnt = __builtin_amdgcn_readfirstlane((int)min((int64_t)(un - u_first), left));
     const int rb = p.row_blocks == 1 ? 0 : pair / p.groups;
     const int h0 = (pair - rb * p.groups) * p.heads, h = h0 + head_at;
     const int row0 = rb * COLS;
     const int rows = min(COLS, p.rows - row0);
+    const int32_t* pages = block_table + n * p.c.table_stride;
 
-    // what the rows see: row of new token j sees [lo(j), hi(j))
-    auto hi_of = [&](int j) { return len - p.m + 1 + j; };
-    auto lo_of = [&](int j) {
-      return p.window ? (int)max((int64_t)0, (int64_t)hi_of(j) - p.window) : 0;
-    };
-    const int j_first = div_group(p, row0), j_last = div_group(p, row0 + rows - 1);
-    const int all_lo = lo_of(j_last), all_hi = hi_of(j_first);  // seen by every row
-    const int any_lo = lo_of(j_first), any_hi = hi_of(j_last);  // seen by one at least
-
-    // ---- the query rows: columns r of NT tiles, as B operands. fp32 rows are scaled here (a
-    // score then overflows only if it is itself out of range), bf16 ones keep their values and
-    // the scores are scaled.
-    const float to_log2 = log2_scale * (p.c.k_scale ? p.c.k_scale[h] : 1.f);
-    const float v_scale = p.c.v_scale ? p.c.v_scale[h] : 1.f;
+    // ---- what does not wait for the length: the query rows (columns r of NT tiles, as B operands),
+    //      and the scales
     uint32_t q[NT][TY::QW];
-    int lo[NT], hi[NT];
+    int j_of[NT];  // new token of this lane's row; -1: no such row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = row0 + nt * 16 + r;
       const bool there = row < p.rows;
       const int j = there ? div_group(p, row) : 0, head = h * p.group + (there ? row - j * p.group : 0);
-      lo[nt] = there ? lo_of(j) : 0;
-      hi[nt] = there ? hi_of(j) : 0;
+      j_of[nt] = there ? j : -1;
       const char* qp = p.q + ((int64_t)n * p.m + j) * p.q_token + head * p.q_head;
       if constexpr (CT == kF32) {
 #pragma unroll
@@ -329,10 +312,34 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
           load_words<4>(qp + 2 * d, &q[nt][4 * s]);
         }
       }
+    }
+    const float to_log2 = log2_scale * (p.c.k_scale ? p.c.k_scale[h] : 1.f);
+    const float v_scale = p.c.v_scale ? p.c.v_scale[h] : 1.f;
+    const int next_len = seq_len(p, min(n + 1, p.N - 1));
+
+    len = __builtin_amdgcn_readfirstlane(len);
+    const int un = seq_units(p, len);
+    const int cnt = __builtin_amdgcn_readfirstlane((int)min((int64_t)(un - u_first), left));
+
+    // what the rows see: row of new token j sees [lo(j), hi(j))
+    auto hi_of = [&](int j) { return len - p.m + 1 + j; };
+    auto lo_of = [&](int j) {
+      return p.window ? (int)max((int64_t)0, (int64_t)hi_of(j) - p.window) : 0;
+    };
+    const int j_first = div_group(p, row0), j_last = div_group(p, row0 + rows - 1);
+    const int all_lo = lo_of(j_last), all_hi = hi_of(j_first);  // seen by every row
+    const int any_lo = lo_of(j_first), any_hi = hi_of(j_last);  // seen by one at least
+    int lo[NT], hi[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      lo[nt] = j_of[nt] >= 0 ? lo_of(j_of[nt]) : 0;
+      hi[nt] = j_of[nt] >= 0 ? hi_of(j_of[nt]) : 0;
+      // fp32 rows are scaled here (a score then overflows only if it is itself out of range), bf16
+      // ones keep their values and the scores are scaled
 #pragma unroll
       for (int s = 0; s < TY::QW; ++s) {
         if (CT == kF32) q[nt][s] = __float_as_uint(__uint_as_float(q[nt][s]) * to_log2);
-        q[nt][s] = there ? q[nt][s] : 0u;
+        q[nt][s] = j_of[nt] >= 0 ? q[nt][s] : 0u;
       }
     }
 
@@ -351,7 +358,6 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     const int i0 = any_lo > base + 31 ? (any_lo - base - 32) / unit + 1 : 0;
     const int i1 = any_hi > base ? min(cnt, (any_hi - base - 1) / unit + 1) : 0;
 
-    const int32_t* pages = block_table + n * p.c.table_stride;
     const char* kh = p.c.k + h * p.c.k_head;
     const char* vh = p.c.v + h * p.c.v_head;
     const int last = any_hi - 1;  // the newest token that some row sees (>= 0 if i0 < i1)
@@ -526,26 +532,32 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       if (!plain) {
         auto token = [&](int i8) { return tb + 4 * g + (i8 & 3) + 16 * (i8 >> 2); };
         auto on_page = [&](int i8) { return is_page(now.id[P16 ? i8 >> 2 : 2 + i8]); };
-        bool odd = false;
 #pragma unroll
         for (int i8 = 0; i8 < 8; ++i8) {
           const int tok = token(i8);
-          const bool in = on_page(i8);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const bool sees = in && tok >= lo[nt] && tok < hi[nt];
+            const bool sees = on_page(i8) && tok >= lo[nt] && tok < hi[nt];
             s[nt][i8 >> 2][i8 & 3] = sees ? s[nt][i8 >> 2][i8 & 3] : -INFINITY;
           }
-          const bool some = tok >= any_lo && tok < any_hi, all = tok >= all_lo && tok < all_hi;
-#pragma unroll
-          for (int e = 0; e < TY::VW; ++e) odd = odd || (in && some && !all && not_finite<CT>(vw[i8][e]));
         }
-        careful = __any(odd);
+        if (max(tb, any_lo) < all_lo || min(tb + 32, any_hi) > all_hi) {  // the tile has private tokens
+          uint32_t over = 0;
+#pragma unroll
+          for (int i8 = 0; i8 < 8; ++i8) {
+            const int tok = token(i8);
+            const bool some = tok >= any_lo && tok < any_hi, all = tok >= all_lo && tok < all_hi;
+            const uint32_t pick = on_page(i8) && some && !all ? NotFinite<CT>::kMagnitude : 0u;
+#pragma unroll
+            for (int e = 0; e < TY::VW; ++e) over |= (vw[i8][e] & pick) + NotFinite<CT>::kStep;
+          }
+          careful = __any((over & NotFinite<CT>::kOver) != 0);
+        }
+        const int from = careful ? all_lo : any_lo, to = careful ? all_hi : any_hi;
 #pragma unroll
         for (int i8 = 0; i8 < 8; ++i8) {
           const int tok = token(i8);
-          const bool some = tok >= any_lo && tok < any_hi, all = tok >= all_lo && tok < all_hi;
-          const uint32_t keep = on_page(i8) && (careful ? all : some) ? ~0u : 0u;
+          const uint32_t keep = on_page(i8) && tok >= from && tok < to ? ~0u : 0u;
           // In place: the compiler would copy the values on the other way round, and wait there.
 #pragma unroll
           for (int e = 0; e < TY::VW; ++e) asm volatile("v_and_b32 %0, %1, %0" : "+v"(vw[i8][e]) : "v"(keep));

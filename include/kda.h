@@ -318,7 +318,7 @@ typedef struct {
  *   flags      0: pair i is channels (i, i + rot / 2). KDA_APPEND_PAIRS: (2i, 2i + 1).
  *   cache      where k and v go. With KDA_F8E4M3 a value is divided by its scale, limited to
  *              [-448, 448] and rounded to nearest even; NaN stays NaN. The k and v arrays
- *              overlap no other argument.
+ *              overlap no other argument, and no two of their rows share elements.
  */
 #define KDA_APPEND_PAIRS 1u
 typedef struct {
@@ -349,7 +349,8 @@ typedef struct {
  *   max_len    no length is larger; 1 <= max_len <= max_pages * page_size. The launch is shaped
  *              by it, so a tight one is faster; the result does not depend on it.
  *   window     0, or the number of latest tokens that a query sees (its own included).
- *   scale      finite; o = softmax(scale * q k^T) v. New token j of sequence n sees positions
+ *   scale      finite; o = softmax(scale * q k^T) v, scores in 32 bits (beyond 3.4e38 they are
+ *              infinite). New token j of sequence n sees positions
  *              t < hi = seq_lens[n] - m + 1 + j, with a window t >= hi - window too. What it does
  *              not see does not reach it, NaN and infinities included. If it sees none, its o
  *              is 0 and its lse -inf.

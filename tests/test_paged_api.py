@@ -71,7 +71,8 @@ def append_args(b, **kw):
     (dict(cache__num_pages=0), BAD_SHAPE), (dict(cache__page_size=0), BAD_SHAPE),
     (dict(cache__max_pages=0), BAD_SHAPE), (dict(cache__k_token_stride=-128), BAD_SHAPE),
     (dict(cache__v_page_stride=4100), BAD_SHAPE), (dict(cache__k=FAKE + 8), BAD_SHAPE),
-    (dict(cache__k_scale=FAKE), UNSUPPORTED), (dict(cache__table_stride=-1), BAD_SHAPE),
+    (dict(cache__k_token_stride=0), BAD_SHAPE), (dict(cache__v_page_stride=64), BAD_SHAPE),
+    (dict(cache__k_head_stride=0), BAD_SHAPE), (dict(cache__k_scale=FAKE), UNSUPPORTED), (dict(cache__table_stride=-1), BAD_SHAPE),
     (dict(k_token_stride=257), BAD_SHAPE), (dict(q_head_stride=-8), BAD_SHAPE),
     (dict(v=FAKE + (2 << 32) + 2), BAD_SHAPE), (dict(cu_seqlens=FAKE + (6 << 32), N=3), BAD_SHAPE),
     (dict(B=1, cu_seqlens=FAKE + (6 << 32), N=0), BAD_SHAPE), (dict(B=1 << 20, T=1 << 20), BAD_SHAPE),
@@ -107,7 +108,8 @@ def decode_args(b, **kw):
     (dict(N=0), BAD_SHAPE), (dict(m=0), BAD_SHAPE), (dict(Hq=7), BAD_SHAPE), (dict(Hkv=0), BAD_SHAPE),
     (dict(d=256), BAD_SHAPE), (dict(act_dtype=0), BAD_DTYPE), (dict(out_dtype=2), BAD_DTYPE),
     (dict(cache__dtype=0), BAD_DTYPE), (dict(flags=1), UNSUPPORTED), (dict(max_len=0), BAD_SHAPE),
-    (dict(max_len=321), BAD_SHAPE), (dict(window=-1), BAD_SHAPE), (dict(m=1 << 22), BAD_SHAPE),
+    (dict(max_len=321), BAD_SHAPE),
+    (dict(cache__max_pages=1 << 27, max_len=1 << 30, m=1 << 12), BAD_SHAPE), (dict(window=-1), BAD_SHAPE), (dict(m=1 << 22), BAD_SHAPE),
     (dict(N=1 << 24), BAD_SHAPE), (dict(q=None), NULL_PTR), (dict(seq_lens=None), NULL_PTR),
     (dict(o=None), NULL_PTR), (dict(scale=float("nan")), BAD_SHAPE), (dict(scale=float("inf")), BAD_SHAPE),
     (dict(cache__v=None), NULL_PTR), (dict(cache__v_scale=FAKE), UNSUPPORTED),
