@@ -16,9 +16,11 @@ int64_t shared_workgroups(const PagedDecodePlan& p) {
   const int tile = 2 * 32 * p.d * (p.cache_type == kF32 ? 4 : p.cache_type == kBF16 ? 2 : 1);
   return 256 * (tile >= 8192 ? 1 : 2);
 }
-// Up to this many 128-token units, a (sequence, row block, head) is done by one workgroup, four
-// waves to a head, with nothing left to join.
-constexpr int64_t kAlone = 4;
+// Contexts of up to this many 128-token units, of this many (sequence, row block, head)s, are done by
+// one workgroup each, four waves to a head, with nothing left to join. Beyond, sharing wins: 8 heads
+// of one context of 512 tokens 10.2 us alone, 11.1 shared; of 1,024 tokens 16.5 and 12.2 (a CU reads
+// only some 55 GB/s); 128 contexts of up to 512 tokens 42 and 41 us, 512 of them 137 and 118.
+constexpr int64_t kAloneUnits = 4, kAlonePairs = 1024;
 
 size_t parts(const PagedDecodePlan& p) { return (size_t)p.split * 2 * p.heads * p.part_rows; }
 
@@ -38,7 +40,7 @@ size_t plan_paged_decode(PagedDecodePlan* p) {
   int64_t span = p->max_len;
   if (p->window) span = std::min<int64_t>(span, (int64_t)p->window + p->m - 1 + 127);
   const int64_t units = (span + 127) / 128, all = (int64_t)p->N * p->row_blocks * p->Hkv;
-  if (units <= kAlone) return 0;
+  if (units <= kAloneUnits && all <= kAlonePairs) return 0;
   // Neighbouring heads together where every workgroup still has four units (of 128 tokens of one
   // head) or more; below that, the four waves of one head finish sooner.
   const int64_t shared = shared_workgroups(*p);
