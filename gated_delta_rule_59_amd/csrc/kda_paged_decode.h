@@ -44,19 +44,20 @@
 namespace kda {
 namespace paged {
 
-// Work is counted in units: a workgroup's four waves carry p.heads (1, 2 or 4) neighbouring
-// key/value heads, 4 / p.heads waves each, and take 32 tokens per wave at a time, so a unit is
-// 2^p.unit_log = 128 / p.heads tokens of p.heads heads. The heads of a token lie side by side in a cache with the
-// token outermost, and reading 1 KiB of each token at a time runs nearer to what HBM delivers than
-// 256 B (4 contexts of 65k tokens, 8 heads: 222 us with one head per workgroup, 188 with four).
-//
-// Workgroups with the same number of waves per head share (sequence, row block, head group)s
-// evenly: each takes equally many units (or one more), in order. Where it begins or ends
-// inside a group it leaves a part in the workspace.
 // row / p.group, for 0 <= row < 2^24
 __device__ __forceinline__ int div_group(const PagedDecodePlan& p, int row) {
   return (int)(((uint64_t)(unsigned)row * p.group_mul) >> p.group_shift);
 }
+// Work is counted in units: a workgroup's four waves carry p.heads (1, 2 or 4) neighbouring
+// key/value heads, 4 / p.heads waves each, and take 32 tokens per wave at a time, so a unit is
+// 2^p.unit_log = 128 / p.heads tokens of p.heads heads. The heads of a token lie side by side in a
+// cache with the token outermost, and reading 1 KiB of each token at a time runs nearer to what HBM
+// delivers than 256 B (4 contexts of 65k tokens, 8 heads, 512 workgroups: 213 us with one head per
+// workgroup, 188 with four).
+//
+// Workgroups share the units of all (sequence, row block, head group)s evenly and in order. One that
+// begins or ends inside a group leaves a part in the workspace, which paged_join_kernel joins.
+
 // The new tokens of sequence n see positions [0, len); with a window, the first of them begins
 // at len - m + 1 - window.
 __device__ __forceinline__ int seq_len(const PagedDecodePlan& p, int n) {

@@ -127,6 +127,81 @@ def test_against_definition(case):
     check(o, h, d ** -0.5, window, out, lse)
 
 
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_loose_bound_on_the_lengths(case):
+    """The same cases with a block table for 40,000 tokens: all workgroups share the work, several
+    neighbouring heads each where the number of heads allows it."""
+    import torch
+    from gated_delta_rule_59_amd import binding
+    lens, m, Hq, Hkv, d, page, window, cache, out, layout = CASES[case]
+    print(f"paged decode, loose bound {CASES[case]}", flush=True)
+    dev, h = make((31, case), lens, m, Hq, Hkv, d, page, cache, layout)
+    table = torch.full((len(lens), -(-40000 // page)), -3, dtype=torch.int32, device="cuda")
+    table[:, :dev["block_table"].shape[1]] = dev["block_table"]
+    dev["block_table"] = table
+    lse = torch.empty((len(lens), m, Hq), dtype=torch.float32, device="cuda")
+    o = binding.paged_decode(**dev, window=window, lse=lse,
+                             out_dtype=torch.float32 if out == "f32" else torch.bfloat16)
+    torch.cuda.synchronize()
+    check(o, h, d ** -0.5, window, out, lse)
+
+
+@pytest.mark.parametrize("Hkv,m,cache", [(4, 1, "bf16"), (8, 4, "bf16"), (4, 3, "e4m3"), (12, 1, "f32"), (6, 9, "bf16")])
+def test_neighbouring_heads_and_parts(Hkv, m, cache):
+    """Long contexts whose heads are carried two or four to a workgroup and cut into parts, several of
+    them in one sequence, beside short and empty ones; whole and in part the same values."""
+    import torch
+    from gated_delta_rule_59_amd import binding
+    lens = [6000, 3, 0, 1500, 33, 4096, 64]
+    dev, h = make((42, Hkv, m), lens, m, 2 * Hkv, Hkv, 64, 16, cache)
+    lse = torch.empty((len(lens), m, 2 * Hkv), dtype=torch.float32, device="cuda")
+    o = binding.paged_decode(**dev, lse=lse)
+    torch.cuda.synchronize()
+    check(o, h, 64 ** -0.5, 0, "f32", lse)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3", "f32"])
+def test_unseen_infinities_with_shared_heads(cache, wide):
+    """As test_unseen_values_do_not_reach_a_row, four heads to a workgroup."""
+    import torch
+    from gated_delta_rule_59_amd import binding
+    m, L, page, H = 3, 90, 16, 4
+    dev, h = make((43, 1), [L, 7], m, 2 * H, H, 64, page, cache)
+    if wide:
+        table = torch.full((2, 2500), -3, dtype=torch.int32, device="cuda")
+        table[:, :dev["block_table"].shape[1]] = dev["block_table"]
+        dev["block_table"] = table
+    for n, tok in ((0, L - 1), (1, 6)):
+        pg = int(dev["block_table"][n, tok // page])
+        x = torch.full((H, 64), float("nan")).to(dev["v_cache"].dtype).cuda()
+        dev["v_cache"].view(torch.uint8)[pg, tok % page] = x.view(torch.uint8)
+    o = binding.paged_decode(**dev)
+    torch.cuda.synchronize()
+    assert torch.isnan(o[:, m - 1]).all() and torch.isfinite(o[:, :m - 1]).all()
+    ref, _ = attend(h["q"], h["k"], h["v"], [np.ones(x, bool) for x in h["lens"]], h["lens"], 64 ** -0.5, 0)
+    tol = attend_bound(h["q"], h["k"], h["v"], h["lens"], 64 ** -0.5, cache, ref, "f32")
+    assert (np.abs(o.cpu().numpy() - ref)[:, :m - 1] <= tol[:, :m - 1]).all()
+
+
+def test_two_calls_at_once():
+    """Two calls on two streams, each with its own workspace, many times over."""
+    import torch
+    from gated_delta_rule_59_amd import binding
+    a, ha = make((44, 1), [3000, 10, 700], 2, 8, 4, 64, 16, "bf16")
+    b, hb = make((44, 2), [50, 2500], 1, 8, 4, 64, 16, "bf16")
+    wa, wb = binding.paged_decode(**a), binding.paged_decode(**b)
+    torch.cuda.synchronize()
+    check(wa, ha, 64 ** -0.5, 0, "f32")
+    check(wb, hb, 64 ** -0.5, 0, "f32")
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(10):
+        got.append((binding.paged_decode(**a, stream=sa), binding.paged_decode(**b, stream=sb)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, wa) and torch.equal(y, wb) for x, y in got)
+
+
 def test_long_context_shared_by_many_workgroups():
     """One sequence of 20,000 tokens among short ones: its parts meet in the workspace."""
     import torch
