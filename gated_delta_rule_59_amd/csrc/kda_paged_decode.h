@@ -215,7 +215,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
   __shared__ __align__(16) float s_o[4][COLS * OS];
   __shared__ float s_m[4][COLS], s_l[4][COLS];
   __shared__ int64_t s_scan[4];
-  __shared__ int s_at[3];
+  __shared__ int s_at[4];
 
   const int t = threadIdx.x, lane = t & 63, r = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -234,10 +234,11 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     len = seq_len(p, n);
     left = seq_units(p, len);
   } else {
-    const int c = (p.N + 255) / 256;
-    int64_t mine = 0;
-    for (int i = 0; i < c; ++i)
-      if (t * c + i < p.N) mine += seq_units(p, seq_len(p, t * c + i));
+    // each thread the units of c sequences, of which it keeps the first's
+    const int c = (p.N + 255) / 256, i0 = t * c;
+    const int len0 = i0 < p.N ? seq_len(p, i0) : 0, un0 = seq_units(p, len0);
+    int64_t mine = i0 < p.N ? un0 : 0;
+    for (int i = i0 + 1; i < min(i0 + c, p.N); ++i) mine += seq_units(p, seq_len(p, i));
     mine *= per_seq;
     int64_t incl = mine;
 #pragma unroll
@@ -261,22 +262,23 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     const int64_t u0 = (int64_t)(each * w) + min(w, more);
     int64_t excl = before + incl - mine;
     if (excl <= u0 && u0 < excl + mine) {
-      int i = t * c;
-      int un = seq_units(p, seq_len(p, i));
+      int i = i0, un = un0, at_len = len0;
       while (u0 - excl >= (int64_t)un * per_seq && i + 1 < p.N) {
         excl += (int64_t)un * per_seq;
-        un = seq_units(p, seq_len(p, ++i));
+        at_len = seq_len(p, ++i);
+        un = seq_units(p, at_len);
       }
       const unsigned at = (unsigned)(u0 - excl);  // below 2^31
       s_at[0] = i;
       s_at[1] = at / (unsigned)un;
-      s_at[2] = at % (unsigned)un;
+      s_at[2] = at - s_at[1] * (unsigned)un;
+      s_at[3] = at_len;
     }
     __syncthreads();
     n = s_at[0];
     pair = s_at[1];
     u_first = s_at[2];
-    len = seq_len(p, n);
+    len = s_at[3];
   }
 
   const float log2_scale = p.scale * kLog2e;
