@@ -123,6 +123,7 @@ struct PagedDecodePlan {
   int split;                     // workgroups that share all work evenly; 0: one per (n, row
                                  // block, head group)
   int part_rows;                 // rows of a part
+  int hold;                      // heads == 4: bytes of LDS in which a wave holds results back
   float *part_o, *part_ml;       // workspace: parts of shared groups, [split][2][heads][part_rows]
                                  // of d values, and of (maximum, sum)
   int* part_of;                  // [n][row block][head group]: first and last workgroup

@@ -37,6 +37,7 @@ size_t plan_paged_decode(PagedDecodePlan* p) {
   p->unit_log = 7;
   divide_by(p->group, &p->group_mul, &p->group_shift);
   p->split = 0;
+  p->hold = 0;
   int64_t span = p->max_len;
   if (p->window) span = std::min<int64_t>(span, (int64_t)p->window + p->m - 1 + 127);
   const int64_t units = (span + 127) / 128, all = (int64_t)p->N * p->row_blocks * p->Hkv;
@@ -51,6 +52,15 @@ size_t plan_paged_decode(PagedDecodePlan* p) {
     p->unit_log = 7 - log;
   }
   p->split = (int)std::min(shared, all * units);
+  if (p->heads == 4) {
+    // room for a workgroup's share of the pairs, one more that it shares at either end, and one that
+    // is uneven; at most what the CU has (160 KiB for its one or two workgroups, less 512 B that they
+    // use otherwise and a scratch of 32 tokens x rows), which is two results or more
+    const int64_t entry = sizeof(paged::Held) + p->part_rows * (p->d * (int64_t)sizeof(float) + paged::kHeldPad);
+    const int64_t room = (160 * 1024 * 256 / shared - 512) / 4 - 32 * 16 * p->tiles * (int64_t)sizeof(float);
+    const int64_t pairs = (int64_t)p->N * p->row_blocks * p->groups;
+    p->hold = (int)std::min(room, entry * ((pairs + p->split - 1) / p->split + 2)) & ~15;
+  }
   return parts(*p) * (p->d + 2) * sizeof(float) + (size_t)(all / p->heads) * 2 * sizeof(int);
 }
 

@@ -226,6 +226,23 @@ def test_many_sequences():
     check(o, h, 32 ** -0.5, 0, "bf16")
 
 
+@pytest.mark.parametrize("d,m,cache,out", [
+    (128, 4, "bf16", "f32"), (128, 4, "e4m3", "bf16"), (128, 8, "bf16", "bf16"),  # 16, 16 and 32 rows
+    (64, 4, "e4m3", "f32"), (32, 7, "bf16", "bf16")])                             # two workgroups per CU
+def test_more_short_sequences_than_a_workgroup_holds_back(d, m, cache, out):
+    """Contexts of a few tokens between two long ones: some workgroups have dozens of finished heads,
+    next to parts of the long contexts."""
+    import torch
+    from gated_delta_rule_59_amd import binding
+    lens = [1 + 7 * i % 33 for i in range(900)]
+    lens[450], lens[899], lens[17] = 6000, 9001, 0
+    dev, h = make((44, d, m), lens, m, 16, 4, d, 16, cache)
+    lse = torch.empty((900, m, 16), dtype=torch.float32, device="cuda")
+    o = binding.paged_decode(**dev, lse=lse, out_dtype=torch.float32 if out == "f32" else torch.bfloat16)
+    torch.cuda.synchronize()
+    check(o, h, d ** -0.5, 0, out, lse)
+
+
 @pytest.mark.parametrize("max_len", [128, 512, 513, 1000, 5000])
 def test_result_does_not_depend_on_max_len(max_len):
     import torch
