@@ -122,6 +122,7 @@ struct PagedDecodePlan {
   int group_shift;
   int split;                     // workgroups that share all work evenly; 0: one per (n, row
                                  // block, head group)
+  int start;                     // units that beginning a group counts for (0 without split)
   int part_rows;                 // rows of a part
   int hold;                      // heads == 4: bytes of LDS in which a wave holds results back
   float *part_o, *part_ml;       // workspace: parts of shared groups, [split][2][heads][part_rows]

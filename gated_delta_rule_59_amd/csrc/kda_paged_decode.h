@@ -55,8 +55,10 @@ __device__ __forceinline__ int div_group(const PagedDecodePlan& p, int row) {
 // delivers than 256 B (4 contexts of 65k tokens, 8 heads, 512 workgroups: 213 us with one head per
 // workgroup, 188 with four).
 //
-// Workgroups share the units of all (sequence, row block, head group)s evenly and in order. One that
-// begins or ends inside a group leaves a part in the workspace, which paged_join_kernel joins.
+// Workgroups share the units of all (sequence, row block, head group)s evenly and in order, each group
+// counted p.start units longer than it is: what its first loads and its results cost comes before
+// its first unit. A workgroup that begins or ends inside a group's units leaves a part in the
+// workspace, which paged_join_kernel joins.
 
 // The new tokens of sequence n see positions [0, len); with a window, the first of them begins
 // at len - m + 1 - window.
@@ -236,9 +238,9 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
   const int head_at = wv / wph, part_at = wv % wph;  // this wave's head of the group, share of a unit
   const int unit = 1 << p.unit_log;
 
-  // ---- this workgroup's units: `left` of them, from unit u_first of (row block, head group)
-  //      `pair` of sequence n on
-  int n, pair, u_first = 0, len;
+  // ---- this workgroup's share: `left` units, from unit `from` of (row block, head group) `pair` of
+  //      sequence n on (the first p.start of a group's are not read)
+  int n, pair, from = 0, len;
   int64_t left;
   if (p.split == 0) {
     n = blockIdx.x / per_seq;
@@ -248,9 +250,9 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
   } else {
     // each thread the units of c sequences, of which it keeps the first's
     const int c = (p.N + 255) / 256, i0 = t * c;
-    const int len0 = i0 < p.N ? seq_len(p, i0) : 0, un0 = seq_units(p, len0);
+    const int len0 = i0 < p.N ? seq_len(p, i0) : 0, un0 = p.start + seq_units(p, len0);
     int64_t mine = i0 < p.N ? un0 : 0;
-    for (int i = i0 + 1; i < min(i0 + c, p.N); ++i) mine += seq_units(p, seq_len(p, i));
+    for (int i = i0 + 1; i < min(i0 + c, p.N); ++i) mine += p.start + seq_units(p, seq_len(p, i));
     mine *= per_seq;
     int64_t incl = mine;
 #pragma unroll
@@ -278,18 +280,19 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       while (u0 - excl >= (int64_t)un * per_seq && i + 1 < p.N) {
         excl += (int64_t)un * per_seq;
         at_len = seq_len(p, ++i);
-        un = seq_units(p, at_len);
+        un = p.start + seq_units(p, at_len);
       }
-      const unsigned at = (unsigned)(u0 - excl);  // below 2^31
+      const int64_t at = u0 - excl;
+      const int in = at >> 32 ? (int)(at / un) : (int)((unsigned)at / (unsigned)un);
       s_at[0] = i;
-      s_at[1] = at / (unsigned)un;
-      s_at[2] = at - s_at[1] * (unsigned)un;
+      s_at[1] = in;
+      s_at[2] = (int)(at - (int64_t)in * un);
       s_at[3] = at_len;
     }
     __syncthreads();
     n = s_at[0];
     pair = s_at[1];
-    u_first = s_at[2];
+    from = s_at[2];
     len = s_at[3];
   }
 
@@ -327,7 +330,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
   while (left > 0) {
     n = __builtin_amdgcn_readfirstlane(n);
     pair = __builtin_amdgcn_readfirstlane(pair);
-    u_first = __builtin_amdgcn_readfirstlane(u_first);
+    from = __builtin_amdgcn_readfirstlane(from);
     const int rb = p.row_blocks == 1 ? 0 : pair / p.groups;
     const int h0 = (pair - rb * p.groups) * p.heads, h = h0 + head_at;
     const int row0 = rb * COLS;
@@ -362,7 +365,9 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
 
     len = __builtin_amdgcn_readfirstlane(len);
     const int un = seq_units(p, len);
-    const int cnt = __builtin_amdgcn_readfirstlane((int)min((int64_t)(un - u_first), left));
+    const int take = __builtin_amdgcn_readfirstlane((int)min((int64_t)(p.start + un - from), left));
+    const int u_first = max(from - p.start, 0), cnt = from + take - p.start - u_first;
+    if (cnt <= 0) break;  // the share ends before the group's first unit
 
     // what the rows see: row of new token j sees [lo(j), hi(j))
     auto hi_of = [&](int j) { return len - p.m + 1 + j; };
@@ -831,8 +836,8 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       if (u_first + cnt == un) of[1] = blockIdx.x;
     }
 
-    left -= cnt;
-    u_first = 0;
+    left -= take;
+    from = 0;
     if (++pair == per_seq) {
       pair = 0;
       ++n;
