@@ -37,10 +37,10 @@ template <typename T>
 __device__ __forceinline__ int standing(const VerifyPlan& v, int n, int count) {
   const T* p = static_cast<const T*>(v.p) + n * v.p_seq;
   const T* q = v.q ? static_cast<const T*>(v.q) + n * v.q_seq : nullptr;
-  for (int j0 = 0; j0 < count; j0 += 64) {
+  for (int j0 = 0; j0 < v.m; j0 += 64) {
     const int j = j0 + (threadIdx.x & 63);
     bool falls = false;
-    if (j < count) {
+    if (j < v.m) {  // also those that are none: their number then arrives meanwhile
       const int x = v.drafts[(int64_t)n * v.m + j];
       const float u = uniform_of(v.uniform[(int64_t)n * (v.m + 1) + j]);
       falls = x < 0 || x >= v.V;
@@ -49,8 +49,9 @@ __device__ __forceinline__ int standing(const VerifyPlan& v, int n, int count) {
         falls = !(fabsf(px) < INFINITY && fabsf(qx) < INFINITY && (double)u * (double)qx < (double)px);
       }
     }
-    const uint64_t fallen = __ballot(falls);
+    const uint64_t fallen = __ballot(falls && j < count);
     if (fallen) return j0 + __builtin_ctzll(fallen);
+    if (j0 + 64 >= count) break;
   }
   return count;
 }
@@ -184,16 +185,29 @@ __device__ __forceinline__ int find_lane(double x, double base, double threshold
 template <typename T>
 __global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyPlan v, int blocks) {
   constexpr int K = kBlock / 64;
+  constexpr int kKept = 2;  // blocks of a lane up to 131,072 tokens
   const int n = blockIdx.x, lane = threadIdx.x;
   const double* sums = static_cast<const double*>(v.workspace) + (int64_t)n * blocks * 2;
   const int count = draft_count(v, n), a = v.accept[n];
   const float u = uniform_of(v.uniform[(int64_t)n * (v.m + 1) + v.m]);
   const Weights<T> row = weights<T>(v, n, a, count);
 
-  // each lane a run of blocks
+  // each lane a run of blocks, the first kKept of which it keeps
   const int per = (blocks + 63) / 64, b0 = min(lane * per, blocks), b1 = min(b0 + per, blocks);
-  double w = 0.0, all = 0.0;
-  for (int b = b0; b < b1; ++b) {
+  double kept_w[kKept], kept_all[kKept], w = 0.0, all = 0.0;
+#pragma unroll
+  for (int k = 0; k < kKept; ++k) {
+    const bool mine = b0 + k < b1;
+    const double2 s = reinterpret_cast<const double2*>(sums)[mine ? b0 + k : 0];
+    kept_w[k] = mine ? s.x : 0.0;
+    kept_all[k] = mine ? s.y : 0.0;
+  }
+#pragma unroll
+  for (int k = 0; k < kKept; ++k) {
+    w += kept_w[k];
+    all += kept_all[k];
+  }
+  for (int b = b0 + kKept; b < b1; ++b) {
     w += sums[2 * (int64_t)b];
     all += sums[2 * (int64_t)b + 1];
   }
@@ -208,15 +222,19 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyPlan v, int
     // the block among that lane's
     int block = -1;
     double block_base = base;
-    for (int b = owner * per; b < min((owner + 1) * per, blocks); ++b) {
-      const double s = sums[2 * (int64_t)b + which];
-      if (s > 0.0) {
+    bool passed_block = false;
+    auto look = [&](int b, double s) {
+      if (!passed_block && s > 0.0) {
         block = b;
         block_base = base;
-        if (base + s > threshold) break;
+        passed_block = base + s > threshold;
       }
       base += s;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) look(owner * per + k, __shfl(which ? kept_all[k] : kept_w[k], owner, 64));
+    for (int b = owner * per + kKept; b < min((owner + 1) * per, blocks) && !passed_block; ++b)
+      look(b, sums[2 * (int64_t)b + which]);
     // the token within it: each lane K neighbouring ones
     double wk[K], pk[K], sum = 0.0;
     row.template at<K>(block * kBlock + lane * K, wk, pk);
@@ -248,8 +266,9 @@ int64_t row_blocks(int V) { return ((int64_t)V + kBlock - 1) / kBlock; }
 template <typename T>
 hipError_t launch_t(const VerifyPlan& p, hipStream_t stream) {
   const int blocks = (int)row_blocks(p.V);
-  // as many waves as the 256 CUs hold (32 each), and never more than there are blocks
-  const int waves = (int)std::min<int64_t>(blocks, std::max<int64_t>(1, 8192 / p.N));
+  // A wave per block, up to 65,536 of them, eight times what the CUs hold: waves that begin while others
+  // wait for their row keep HBM busy (512 x 4 drafts over 131,072 tokens 79 us, 87 with 8,192 waves).
+  const int waves = (int)std::min<int64_t>(blocks, std::max<int64_t>(1, 65536 / p.N));
   hipLaunchKernelGGL(verify_sums_kernel<T>, dim3((unsigned)(((int64_t)waves * p.N + 3) / 4)), dim3(256), 0,
                      stream, p, blocks, waves);
   hipError_t e = hipGetLastError();
