@@ -785,39 +785,41 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       }
     } else {
       // the waves' parts of a head meet in LDS
-      if (g == 0) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s_m[wv][nt * 16 + r] = top[nt];
-          s_l[wv][nt * 16 + r] = sum[nt];
-        }
-      }
-      __syncthreads();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int c = nt * 16 + r;
-        float now = top[nt];
-        for (int w = wv - part_at; w < wv - part_at + wph; ++w) now = fmaxf(now, s_m[w][c]);
-        const float fade = kUnlift * __builtin_amdgcn_exp2f(top[nt] - (now == -INFINITY ? 0.f : now));
+        if (g == 0) {
+          s_m[wv][c] = top[nt];
+          s_l[wv][c] = sum[nt];
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x[VEC];
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) x[j] = acc[nt][j][e] * fade;
+          for (int j = 0; j < VEC; ++j) x[j] = acc[nt][j][e];
           store_channels<VEC, float>(&s_o[wv][c * OS + g * (D / 4) + VEC * e], x);
         }
       }
       __syncthreads();
-#pragma unroll 2
       for (int x = t; x < p.heads * rows * (D / 4); x += 256) {
-        const int y = x / (D / 4), d = x % (D / 4) * 4, hh = p.heads == 1 ? 0 : y / rows, c = y - hh * rows;
-        const float scale = p.heads == 1 ? v_scale : p.c.v_scale ? p.c.v_scale[h0 + hh] : 1.f;
-        float now = -INFINITY, l = 0.f;
+        const int y = x / (D / 4), d = x % (D / 4) * 4, hh = y >= rows ? 1 : 0, c = y - hh * rows;  // at most two heads
+        const float scale = hh == head_at ? v_scale : p.c.v_scale ? p.c.v_scale[h0 + hh] : 1.f;
+        // all four waves at once, those of the other head with weight zero
+        float m[4], l = 0.f, now = -INFINITY;
         floatx4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int w = hh * wph; w < (hh + 1) * wph; ++w) now = fmaxf(now, s_m[w][c]);
-        for (int w = hh * wph; w < (hh + 1) * wph; ++w) {
-          l += s_l[w][c] * __builtin_amdgcn_exp2f(s_m[w][c] - (now == -INFINITY ? 0.f : now));
-          o += *reinterpret_cast<const floatx4*>(&s_o[w][c * OS + d]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          m[w] = w / wph == hh ? s_m[w][c] : -INFINITY;
+          now = fmaxf(now, m[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = __builtin_amdgcn_exp2f(m[w] - (now == -INFINITY ? 0.f : now));
+          const floatx4 ow = *reinterpret_cast<const floatx4*>(&s_o[w][c * OS + d]);
+          if (w / wph != hh) continue;
+          l = fmaf(s_l[w][c], f, l);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = fmaf(ow[e], kUnlift * f, o[e]);
         }
         if (whole) {
           write_row<D>(p, out_row(p, n, h0 + hh, row0 + c), d, scale, now, l, o);
@@ -827,7 +829,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
           if (d == 0) *reinterpret_cast<floatx2*>(p.part_ml + part * 2) = floatx2{now, l};
         }
       }
-      __syncthreads();  // s_o, s_m and s_l are free again
+      if (left > take) __syncthreads();  // s_o, s_m and s_l are free again
     }
     // which workgroups have the group's first and last units
     if (p.split && t == 0) {
