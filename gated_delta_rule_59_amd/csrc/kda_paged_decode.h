@@ -120,6 +120,17 @@ __device__ __forceinline__ uint32_t halves_hi(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 typedef float floatx2 __attribute__((ext_vector_type(2)));
+// op over the lanes r, 16 + r, 32 + r, 48 + r, in all of them. Row exchanges, not shuffles: those go
+// through LDS, whose counter the page ids' scalar loads share, so the maximum of each tile would wait
+// for the page ids of the tile two ahead (one short context 8.84 -> 8.76 us).
+template <typename Op>
+__device__ __forceinline__ float over_groups(float x, Op op) {
+  const unsigned a = __float_as_uint(x);
+  const auto y = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const unsigned b = __float_as_uint(op(__uint_as_float(y[0]), __uint_as_float(y[1])));
+  const auto z = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return op(__uint_as_float(z[0]), __uint_as_float(z[1]));
+}
 // Elements 2h and 2h + 1 of four e4m3 values.
 template <bool H>
 __device__ __forceinline__ floatx2 e4m3_pair(uint32_t w) {
@@ -617,8 +628,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
       for (int nt = 0; nt < NT; ++nt) {
         float mx = fmaxf(fmaxf(fmaxf(s[nt][0][0], s[nt][0][1]), fmaxf(s[nt][0][2], s[nt][0][3])),
                          fmaxf(fmaxf(s[nt][1][0], s[nt][1][1]), fmaxf(s[nt][1][2], s[nt][1][3])));
-        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        mx = over_groups(mx, [](float a, float b) { return fmaxf(a, b); });
         const float most = fmaxf(top[nt], mx);
         const float peak = most == -INFINITY ? 0.f : most, ref = peak - kLift;
         const float fade = __builtin_amdgcn_exp2f(top[nt] - peak);
@@ -745,8 +755,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     const int64_t slot = (2 * (int64_t)blockIdx.x + (u_first == 0 ? 1 : 0)) * p.heads * p.part_rows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      sum[nt] += __shfl_xor(sum[nt], 16, 64);
-      sum[nt] += __shfl_xor(sum[nt], 32, 64);
+      sum[nt] = over_groups(sum[nt], [](float a, float b) { return a + b; });
       sum[nt] *= kUnlift;
     }
     if (wph == 1) {
