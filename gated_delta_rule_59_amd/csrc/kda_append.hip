@@ -60,7 +60,7 @@ struct Chunk<float> {
 // E values as type CACHE (a kda_dtype), rounded to nearest even; streamed (65,536 prompt tokens,
 // 1.6 GB read and written: 269 us, 282 with ordinary stores).
 template <int CACHE, int E>
-__device__ __forceinline__ void store_chunk(char* p, const float* x, float inv_scale) {
+__device__ __forceinline__ void store_chunk(char* p, const float* x, float scale) {
   if constexpr (CACHE == kF32) {
     __builtin_nontemporal_store(floatx4{x[0], x[1], x[2], x[3]}, reinterpret_cast<floatx4*>(p));
   } else if constexpr (CACHE == kBF16) {
@@ -72,7 +72,7 @@ __device__ __forceinline__ void store_chunk(char* p, const float* x, float inv_s
     float y[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      y[i] = x[i] * inv_scale;
+      y[i] = x[i] / scale;  // not times 1 / scale: 175 / 7 is a tie, 175 * (1 / 7) lies above it
       y[i] = y[i] > 448.f ? 448.f : y[i];  // NaN passes both comparisons
       y[i] = y[i] < -448.f ? -448.f : y[i];
     }
@@ -163,11 +163,11 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const KvAppendPlan p) {
       store_chunk<SA == 4 ? kF32 : kBF16, E>(dst + b * SA, x + E, 1.f);
     } else {
       const float* sc = is_v ? p.c.v_scale : p.c.k_scale;
-      const float inv = CACHE == kF8 && sc ? 1.f / sc[h] : 1.f;
+      const float scale = CACHE == kF8 && sc ? sc[h] : 1.f;
       char* dst = is_v ? p.c.v + page * p.c.v_page + slot * p.c.v_token + h * p.c.v_head
                        : p.c.k + page * p.c.k_page + slot * p.c.k_token + h * p.c.k_head;
-      store_chunk<CACHE, E>(dst + a * SC, x, inv);
-      store_chunk<CACHE, E>(dst + b * SC, x + E, inv);
+      store_chunk<CACHE, E>(dst + a * SC, x, scale);
+      store_chunk<CACHE, E>(dst + b * SC, x + E, scale);
     }
   }
 }

@@ -204,6 +204,27 @@ def test_e4m3_limits_and_nan():
     assert torch.equal(got, want)
 
 
+def test_e4m3_quotients_that_are_ties():
+    """Odd multiples of 7 over a scale of 7 lie halfway between two e4m3 values and go to the even
+    one; times the rounded 1 / 7 they come out above the middle."""
+    import torch
+    from gated_delta_rule_59_amd import binding
+    dev, h = make((55, 2), [0], [1], 1, 1, 32, 0, 16, "bf16", "e4m3")
+    dev["k_scale"].fill_(7.0)
+    dev["v_scale"].fill_(7.0)
+    x = torch.zeros(32)
+    x[:10] = torch.tensor([161.0, 175.0, 189.0, 203.0, 217.0, -161.0, -175.0, -189.0, -203.0, -217.0])
+    for name in ("k", "v"):
+        dev[name][0, 0, 0] = x.to(torch.bfloat16).cuda()
+    binding.kv_append(**dev)
+    torch.cuda.synchronize()
+    pg = int(dev["block_table"][0, 0])
+    want = torch.zeros(32)
+    want[:10] = torch.tensor([24.0, 24.0, 28.0, 28.0, 32.0, -24.0, -24.0, -28.0, -28.0, -32.0])
+    for c in ("k_cache", "v_cache"):
+        assert torch.equal(dev[c][pg, 0, 0].float().cpu(), want)
+
+
 def test_no_tokens():
     import torch
     from gated_delta_rule_59_amd import binding
