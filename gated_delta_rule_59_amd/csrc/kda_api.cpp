@@ -370,6 +370,7 @@ kda_status validate_verify_shapes(const kda_verify_args* a) {
   if (a->N < 1 || a->m < 1 || a->V < 1)
     return fail(KDA_ERR_BAD_SHAPE, "need N, m, V >= 1 (got N=%d m=%d V=%d)", a->N, a->m, a->V);
   if (!dtype_ok(a->dtype)) return fail(KDA_ERR_BAD_DTYPE, "unknown dtype");
+  if (a->m > (1 << 24)) return fail(KDA_ERR_BAD_SHAPE, "m too large (got %d)", a->m);
   if (a->V > (1 << 30) || kda::verify_blocks(a->N, a->V) > kMaxDecodePairs)
     return fail(KDA_ERR_BAD_SHAPE, "N * V too large for one launch");
   return KDA_OK;

@@ -347,7 +347,7 @@ typedef struct {
  *   seq_lens   device int32 [N]: tokens of each sequence in the cache, the new ones included.
  *              Values outside [0, max_len] are taken as the nearer bound.
  *   max_len    no length is larger; 1 <= max_len <= max_pages * page_size. The launch is shaped
- *              by it, so a tight one is faster; the result does not depend on it.
+ *              by it, so a tight one is faster; the result depends on it by rounding only.
  *   window     0, or the number of latest tokens that a query sees (its own included).
  *   scale      finite; o = softmax(scale * q k^T) v, scores in 32 bits (beyond 3.4e38 they are
  *              infinite). New token j of sequence n sees positions
@@ -381,7 +381,8 @@ typedef struct {
 /* Arguments of kda_verify_drafts: how many of m drafted tokens of each of N sequences stand
  * against the target model's probabilities, and the token that follows them, so that the
  * tokens are distributed as if drawn from the target alone.
- *   m, V       drafts per sequence and vocabulary size, >= 1.   dtype  of p and q: KDA_F32 or KDA_BF16.
+ *   m, V       drafts per sequence (1 .. 2^24) and vocabulary size (1 .. 2^30).
+ *   dtype      of p and q: KDA_F32 or KDA_BF16.
  *   p          target probabilities [N, m + 1, V]: row j of sequence n, for the token after j
  *              drafts, begins at n * p_seq_stride + j * p_row_stride (elements).
  *   q          probabilities the drafts were drawn from, [N, m, V] by its strides; or NULL if the

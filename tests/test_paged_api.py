@@ -166,6 +166,14 @@ def test_verify_refusals(b, change, status):
     assert rc == status and msg, (rc, msg)
 
 
+@pytest.mark.parametrize("m", [(1 << 24) + 1, 2 ** 31 - 1])
+def test_verify_refuses_too_many_drafts(b, m):
+    """m + 1 rows per sequence would pass 32 bits."""
+    rc, msg = call(b, "verify_drafts", verify_args(b, m=m))
+    assert rc == BAD_SHAPE and "m too large" in msg
+    assert b.lib().kda_verify_drafts_workspace_bytes(ctypes.byref(verify_args(b, m=m))) == b.SIZE_MAX
+
+
 def test_verify_workspace(b):
     q = lambda a: b.lib().kda_verify_drafts_workspace_bytes(ctypes.byref(a))  # noqa: E731
     assert 0 < q(verify_args(b)) < 1 << 20
