@@ -312,8 +312,8 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
   // One wave per head: finished rows and parts wait in LDS until there is no room for more or the
   // wave's work is done. A few lines written now and then among the reads of everyone else cost HBM
   // a change of direction each: 512 contexts of up to 4096 e4m3 tokens with 16 rows per head, whose
-  // results are 33 MB next to 2.1 GB read, 399 us with every result written at once, 357
-  // with results held back.
+  // results are 33 MB next to 2.1 GB read, 399 us with every result written at once, 357 with results
+  // held back.
   char* const scratch = lds + wv * (32 * COLS * (int)sizeof(float) + p.hold);
   char* const hold = scratch + 32 * COLS * (int)sizeof(float);
   int held = 0;  // bytes
@@ -323,9 +323,9 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     for (int at = 0; at < held;) {
       const Held x = *reinterpret_cast<const Held*>(hold + at);
       const char* from = hold + at + sizeof(Held);
-      const int es = x.part < 0 && p.out_bf16 ? 2 : 4, row = D * es, pieces = row / 16;
+      const int es = x.part < 0 && p.out_bf16 ? 2 : 4, row = D * es, pieces = row / 16;  // a power of two
       for (int i = lane; i < x.rows * pieces; i += 64) {
-        const int c = i / pieces, b = (i - c * pieces) * 16;
+        const int c = i >> __builtin_ctz(pieces), b = (i & (pieces - 1)) * 16;
         char* to = x.part < 0 ? static_cast<char*>(p.o) + out_row(p, x.n, x.h, x.row0 + c) * row
                               : reinterpret_cast<char*>(p.part_o) + (x.part + c) * row;
         *reinterpret_cast<u32x4*>(to + b) = *reinterpret_cast<const u32x4*>(from + c * (row + kHeldPad) + b);
@@ -959,7 +959,7 @@ hipError_t launch_d(const PagedDecodePlan& p, hipStream_t stream) {
   const int lds = 4 * (int)sizeof(float) * (p.heads == 4 ? 32 * cols : cols * (D + 4) + 2 * cols) +
                   (p.heads == 4 ? 4 * p.hold : 0);
   hipError_t e = hipSuccess;
-  if (lds > 64 * 1024)
+  if (lds > 60 * 1024)  // with the static part, past the 64 KiB that need no asking
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, grid, dim3(256), lds, stream, p, p.c.table);
