@@ -10,10 +10,11 @@
 // batch, latency for one sequence. Two launches: in the first, every wave finds out which drafts
 // stand (a few gathered values) and sums the weights of its blocks of 1024 tokens; in the second,
 // one wave per sequence finds the block in the blocks' prefix sums and the token within the block.
-// No wave waits for another, so there are no barriers and no LDS.
+// No wave waits for another there, so there are no barriers and no LDS.
 //
 // Sums are 64 bit in a fixed order: a token's share can be 10^-8 of the sum, less than 32 bits
-// resolve next to it, and the result is the same on every run.
+// resolve next to it, and the result is the same on every run. Small vocabularies take one launch
+// (verify_alone_kernel).
 #include <algorithm>
 
 #include "kda_device.h"
@@ -128,13 +129,32 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
+// A wave's sums over block b: of w and of p, in every lane.
+template <typename T>
+__device__ __forceinline__ void block_sums(const Weights<T>& row, int b, double* w_sum, double* p_sum) {
+  // Tokens per lane and step: 16 bytes, so a load instruction covers 1 KiB in one piece. (Eight fp32
+  // values per lane, two instructions that each skip every other 16 bytes: 53 us where this takes 46.)
+  constexpr int N = 16 / sizeof(T);
+  const int lane = threadIdx.x & 63;
+  double w = 0.0, all = 0.0;
+#pragma unroll
+  for (int c = 0; c < kBlock; c += 64 * N) {
+    double wk[N], pk[N];
+    row.template at<N>(b * kBlock + c + lane * N, wk, pk);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      w += wk[k];
+      all += pk[k];
+    }
+  }
+  *w_sum = wave_sum(w);
+  *p_sum = wave_sum(all);
+}
+
 // Four waves per workgroup, `waves` per sequence; wave i of a sequence sums blocks i, i + waves, ...
 // into sums[n][block] = {sum of w, sum of p}.
 template <typename T>
 __global__ __launch_bounds__(256) void verify_sums_kernel(const VerifyPlan v, int blocks, int waves) {
-  // Tokens per lane and step: 16 bytes, so a load instruction covers 1 KiB in one piece. (Eight fp32
-  // values per lane, two instructions that each skip every other 16 bytes: 53 us where this takes 46.)
-  constexpr int N = 16 / sizeof(T);
   const int lane = threadIdx.x & 63;
   const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = (int)(wave / waves), first = (int)(wave - (int64_t)n * waves);
@@ -145,19 +165,8 @@ __global__ __launch_bounds__(256) void verify_sums_kernel(const VerifyPlan v, in
   const Weights<T> row = weights<T>(v, n, a, count);
   double* out = static_cast<double*>(v.workspace) + (int64_t)n * blocks * 2;
   for (int b = first; b < blocks; b += waves) {
-    double w = 0.0, all = 0.0;
-#pragma unroll
-    for (int c = 0; c < kBlock; c += 64 * N) {
-      double wk[N], pk[N];
-      row.template at<N>(b * kBlock + c + lane * N, wk, pk);
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        w += wk[k];
-        all += pk[k];
-      }
-    }
-    w = wave_sum(w);
-    all = wave_sum(all);
+    double w, all;
+    block_sums(row, b, &w, &all);
     if (lane < 2) out[2 * (int64_t)b + lane] = lane ? all : w;
   }
 }
@@ -181,16 +190,14 @@ __device__ __forceinline__ int find_lane(double x, double base, double threshold
   return found;
 }
 
-// One wave per sequence.
+// The tokens of sequence n, by one wave, from the blocks' sums.
 template <typename T>
-__global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyPlan v, int blocks) {
+__device__ __forceinline__ void pick(const VerifyPlan& v, int n, int a, const Weights<T>& row,
+                                     const double* sums, int blocks) {
   constexpr int K = kBlock / 64;
   constexpr int kKept = 2;  // blocks of a lane up to 131,072 tokens
-  const int n = blockIdx.x, lane = threadIdx.x;
-  const double* sums = static_cast<const double*>(v.workspace) + (int64_t)n * blocks * 2;
-  const int count = draft_count(v, n), a = v.accept[n];
+  const int lane = threadIdx.x & 63;
   const float u = uniform_of(v.uniform[(int64_t)n * (v.m + 1) + v.m]);
-  const Weights<T> row = weights<T>(v, n, a, count);
 
   // each lane a run of blocks, the first kKept of which it keeps
   const int per = (blocks + 63) / 64, b0 = min(lane * per, blocks), b1 = min(b0 + per, blocks);
@@ -198,9 +205,9 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyPlan v, int
 #pragma unroll
   for (int k = 0; k < kKept; ++k) {
     const bool mine = b0 + k < b1;
-    const double2 s = reinterpret_cast<const double2*>(sums)[mine ? b0 + k : 0];
-    kept_w[k] = mine ? s.x : 0.0;
-    kept_all[k] = mine ? s.y : 0.0;
+    const int b = mine ? b0 + k : 0;
+    kept_w[k] = mine ? sums[2 * (int64_t)b] : 0.0;
+    kept_all[k] = mine ? sums[2 * (int64_t)b + 1] : 0.0;
   }
 #pragma unroll
   for (int k = 0; k < kKept; ++k) {
@@ -261,11 +268,45 @@ __global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyPlan v, int
         j < a ? v.drafts[(int64_t)n * v.m + j] : j == a ? next : -1;
 }
 
+// One wave per sequence.
+template <typename T>
+__global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyPlan v, int blocks) {
+  const int n = blockIdx.x, a = v.accept[n];
+  const Weights<T> row = weights<T>(v, n, a, draft_count(v, n));
+  pick(v, n, a, row, static_cast<const double*>(v.workspace) + (int64_t)n * blocks * 2, blocks);
+}
+
+// All of it in one launch: a workgroup per sequence with a wave per block, whose sums meet in LDS.
+constexpr int kAloneBlocks = 16;
+template <typename T>
+__global__ __launch_bounds__(64 * kAloneBlocks) void verify_alone_kernel(const VerifyPlan v, int blocks) {
+  __shared__ double sums[2 * kAloneBlocks];
+  const int n = blockIdx.x, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int count = draft_count(v, n);
+  const int a = __builtin_amdgcn_readfirstlane(standing<T>(v, n, count));
+  const Weights<T> row = weights<T>(v, n, a, count);
+  double w, all;
+  block_sums(row, wave, &w, &all);
+  if (lane < 2) sums[2 * wave + lane] = lane ? all : w;
+  __syncthreads();
+  if (wave) return;
+  if (lane == 0) v.accept[n] = a;
+  pick(v, n, a, row, sums, blocks);
+}
+
 int64_t row_blocks(int V) { return ((int64_t)V + kBlock - 1) / kBlock; }
 
 template <typename T>
 hipError_t launch_t(const VerifyPlan& p, hipStream_t stream) {
   const int blocks = (int)row_blocks(p.V);
+  // One launch for small vocabularies and no more sequences than CUs: 4 drafts over 8,000 tokens 7.1 us
+  // (two launches 8.3), 256 sequences 9.7 (11.8), 512 sequences 17.2 (14.9); with two blocks to a wave
+  // it loses, one sequence over 32,000 tokens 10.8 us (8.2).
+  if (blocks <= kAloneBlocks && p.N <= 256) {
+    hipLaunchKernelGGL(verify_alone_kernel<T>, dim3((unsigned)p.N), dim3(64 * blocks), 0, stream, p, blocks);
+    return hipGetLastError();
+  }
   // A wave per block, up to 65,536 of them, eight times what the CUs hold: waves that begin while others
   // wait for their row keep HBM busy (512 x 4 drafts over 131,072 tokens 79 us, 87 with 8,192 waves).
   const int waves = (int)std::min<int64_t>(blocks, std::max<int64_t>(1, 65536 / p.N));

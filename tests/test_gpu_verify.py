@@ -62,6 +62,16 @@ def test_against_definition(N, m, V, drawn, dtype):
         assert a.min() == 0 and a.max() == m   # both ways of choosing the following token
 
 
+@pytest.mark.parametrize("N,m,V,drawn,dtype", [
+    (3, 2, 16384, True, "f32"), (3, 2, 16385, True, "f32"), (2, 3, 16383, True, "bf16"), (2, 3, 16400, False, "bf16"),
+    (256, 2, 1025, True, "f32"), (257, 2, 1025, True, "f32"), (300, 1, 3, False, "f32")])
+def test_one_launch_or_two(N, m, V, drawn, dtype):
+    """Around the vocabulary and the number of sequences up to which one workgroup does a sequence."""
+    print(f"verify N={N} m={m} V={V} drawn={drawn} {dtype}", flush=True)
+    p, q, x, r = make((66, N, m, V), N, m, V, drawn)
+    check(p, q, x, r, dtype=dtype)
+
+
 def test_ragged_counts():
     p, q, x, r = make((62, 1), 24, 4, 500)
     check(p, q, x, r, counts=[0, 1, 2, 3, 4, -3, 9, 4] * 3)
