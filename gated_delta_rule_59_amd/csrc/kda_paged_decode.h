@@ -21,8 +21,9 @@
 // parts (16 significant bits, an error of 2^-17 of each weight), which costs a second V product
 // that hides under the loads; one part alone (2^-9) would add as much error to a bf16 result as
 // its own rounding. An e4m3 value is exact in bf16 (K) and in fp16 (V), so over an e4m3 cache P is
-// fp16: one part for a bf16 result (2^-12 of each weight, an eighth of the result's own rounding),
-// two for an fp32 one (2^-23). fp32 caches take the fp32 matrix instruction throughout.
+// two fp16 parts (2^-23). One part (2^-12) put 8 % of the bf16 results a step off and saved nothing at
+// up to 16 rows (512 contexts with 4 drafts 347 us either way), 5 % at 32 rows (64 contexts of up to
+// 4000 tokens with 8 drafts 85 us, 89 with two). fp32 caches take the fp32 matrix instruction throughout.
 //
 // Who sees what. Rows of a block differ in what they see only near the newest token and the
 // window's far edge ("private" tokens, at most m - 1 at each end). A row that does not see a token
@@ -221,12 +222,10 @@ __device__ __forceinline__ void write_row(const PagedDecodePlan& p, int64_t dst,
 }
 
 // P16: page_size is a multiple of 16, so 16 aligned tokens have one page.
-// ONE: the weights in one fp16 part (e4m3 caches only).
-template <int CT, int D, int NT, bool P16, bool ONE>
+template <int CT, int D, int NT, bool P16>
 __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
     const PagedDecodePlan p, const int32_t* __restrict__ block_table) {
   using TY = Types<CT, D>;
-  static_assert(!ONE || CT == kF8, "V must be exact in fp16");
   constexpr int VEC = TY::VEC;
   // Weights that become fp16 are held 2^14 times as large (at most 16384): the smallest fp16 step
   // is then 2^-38 of the largest weight, and a long tail of small weights is not lost.
@@ -689,7 +688,7 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
               acc[nt][j] = mfma_bf16(a, p_lo[nt], acc[nt][j]);
             } else {
               acc[nt][j] = mfma_f16(a, p_hi[nt], acc[nt][j]);
-              if constexpr (!ONE) acc[nt][j] = mfma_f16(a, p_lo[nt], acc[nt][j]);
+              acc[nt][j] = mfma_f16(a, p_lo[nt], acc[nt][j]);
             }
           }
         };
@@ -947,14 +946,8 @@ hipError_t launch_d(const PagedDecodePlan& p, hipStream_t stream) {
   // one page per 16 aligned tokens, whose rows lie within 32 bits of each other
   const bool p16 = p.c.page_size % 16 == 0 && p.c.k_token < (1 << 26) && p.c.v_token < (1 << 26) &&
                    p.c.k_page < (int64_t(1) << 36) && p.c.v_page < (int64_t(1) << 36);
-  auto pick = [&](auto one) {
-    constexpr bool ONE = decltype(one)::value;
-    return p.tiles == 1 ? (p16 ? paged_decode_kernel<CT, D, 1, true, ONE> : paged_decode_kernel<CT, D, 1, false, ONE>)
-                        : (p16 ? paged_decode_kernel<CT, D, 2, true, ONE> : paged_decode_kernel<CT, D, 2, false, ONE>);
-  };
-  auto kern = pick(std::false_type{});
-  if constexpr (CT == kF8)
-    if (p.out_bf16) kern = pick(std::true_type{});
+  const auto kern = p.tiles == 1 ? (p16 ? paged_decode_kernel<CT, D, 1, true> : paged_decode_kernel<CT, D, 1, false>)
+                                 : (p16 ? paged_decode_kernel<CT, D, 2, true> : paged_decode_kernel<CT, D, 2, false>);
   const int cols = 16 * p.tiles;
   const int lds = 4 * (int)sizeof(float) * (p.heads == 4 ? 32 * cols : cols * (D + 4) + 2 * cols) +
                   (p.heads == 4 ? 4 * p.hold : 0);

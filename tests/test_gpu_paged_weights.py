@@ -1,0 +1,38 @@
+"""kda_paged_decode holds its softmax weights in 24 bits or more, whatever the types of the cache and
+the result: rows of two tokens, to within the roundings of 32-bit arithmetic."""
+import numpy as np
+import pytest
+
+from tests.paged_weights import make, outside, reference
+
+pytestmark = pytest.mark.gpu
+
+# cache, result, N, Hq, Hkv, d: one wave per head and several, one row tile and two
+CASES = [
+    ("e4m3", "bf16", 300, 8, 8, 128), ("e4m3", "bf16", 40, 40, 2, 64), ("e4m3", "bf16", 64, 4, 1, 32),
+    ("e4m3", "f32", 300, 32, 8, 128), ("e4m3", "f32", 33, 5, 5, 64), ("e4m3", "f32", 9, 17, 1, 128),
+]
+
+
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_rows_of_two_tokens(case, page):
+    import torch
+    from gated_delta_rule_59_amd import binding
+    cache, out, N, Hq, Hkv, d = CASES[case]
+    print(f"weights {CASES[case]} pages of {page}", flush=True)
+    q, k, v, scales, scale = make((82, case), cache, N, Hq, Hkv, d)
+    act = torch.float32 if cache == "f32" else torch.bfloat16
+    ct = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[cache]
+    dev = lambda x, t: torch.from_numpy(np.ascontiguousarray(x)).to(t).cuda()  # noqa: E731
+    pages = np.zeros((2, N, page, Hkv, d))
+    pages[0][:, :2], pages[1][:, :2] = k, v
+    ks, vs = (dev(x, torch.float32) if cache == "e4m3" else None for x in scales)
+    o = binding.paged_decode(dev(q, act), dev(pages[0], ct), dev(pages[1], ct),
+                             torch.arange(N, dtype=torch.int32, device="cuda")[:, None].contiguous(),
+                             torch.full((N,), 2, dtype=torch.int32, device="cuda"), scale=scale,
+                             k_scale=ks, v_scale=vs,
+                             out_dtype=torch.bfloat16 if out == "bf16" else torch.float32)
+    torch.cuda.synchronize()
+    ref, s = reference(q, k, v, scales, scale)
+    assert outside(o[:, 0].double().cpu().numpy(), ref, s, cache, out) == 0
