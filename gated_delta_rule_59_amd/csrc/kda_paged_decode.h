@@ -17,13 +17,15 @@
 //   within the lane. Tile j then holds channels {VEC r + j}, so lane (r, g) ends with the D / 4
 //   consecutive channels from g D / 4 on of row r.
 //
-// Rounding: products and sums are held in 32 bits. Over a bf16 cache P is split into two bf16
-// parts (16 significant bits, an error of 2^-17 of each weight), which costs a second V product
-// that hides under the loads; one part alone (2^-9) would add as much error to a bf16 result as
-// its own rounding. An e4m3 value is exact in bf16 (K) and in fp16 (V), so over an e4m3 cache P is
-// two fp16 parts (2^-23). One part (2^-12) put 8 % of the bf16 results a step off and saved nothing at
-// up to 16 rows (512 contexts with 4 drafts 347 us either way), 5 % at 32 rows (64 contexts of up to
-// 4000 tokens with 8 drafts 85 us, 89 with two). fp32 caches take the fp32 matrix instruction throughout.
+// Rounding: products, sums and the softmax weights P are held in 32 bits. Over a bf16 cache P goes into
+// the V product as three bf16 parts, which hold all 24 bits. (With two, 2^-17 of each weight, fp32
+// results were off by 2e-6 where they are off by 4e-7, and 0.25 % of the bf16 results a step, for
+// 0.15 us of 8.85 on one short context, 2 % at 32 rows per head: 64 contexts of up to 4000 tokens 129 us,
+// 131 with three; nothing that shows elsewhere, since the products hide under the loads.) An e4m3 value
+// is exact in bf16 (K) and in fp16 (V), so over an e4m3 cache P is two fp16 parts (2^-23). One part
+// (2^-12) put 8 % of the bf16 results a step off and saved nothing at up to 16 rows (512 contexts with 4
+// drafts 347 us either way), 5 % at 32 rows (64 contexts of up to 4000 tokens with 8 drafts 85 us, 89
+// with two). fp32 caches take the fp32 matrix instruction throughout.
 //
 // Who sees what. Rows of a block differ in what they see only near the newest token and the
 // window's far edge ("private" tokens, at most m - 1 at each end). A row that does not see a token
@@ -661,36 +663,32 @@ __global__ __launch_bounds__(256, 2) void paged_decode_kernel(
                   __uint_as_float(vw[i8][j]), s[nt][i8 >> 2][i8 & 3], acc[nt][j], 0, 0, 0);
       } else {
         typedef std::conditional_t<CT == kF8, half8, bf16x8> operand;
-        operand p_hi[NT], p_lo[NT];
+        typedef std::conditional_t<CT == kF8, _Float16, __bf16> element;
+        constexpr int PARTS = CT == kF8 ? 2 : 3;
+        operand parts[NT][PARTS];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i8 = 0; i8 < 8; ++i8) {
-            const float w = s[nt][i8 >> 2][i8 & 3];
-            if constexpr (CT == kBF16) {
-              __bf16 a, b;
-              split_bf16(w, a, b);
-              p_hi[nt][i8] = a;
-              p_lo[nt][i8] = b;
-            } else {
-              _Float16 a, b;
-              split_f16(w, a, b);
-              p_hi[nt][i8] = a;
-              p_lo[nt][i8] = b;
+            float rest = s[nt][i8 >> 2][i8 & 3];
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x) {
+              const element y = static_cast<element>(rest);
+              parts[nt][x][i8] = y;
+              rest -= static_cast<float>(y);
             }
           }
         auto product = [&](int j, const u32x4& frag) {
           const operand a = __builtin_bit_cast(operand, frag);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (CT == kBF16) {
-              acc[nt][j] = mfma_bf16(a, p_hi[nt], acc[nt][j]);
-              acc[nt][j] = mfma_bf16(a, p_lo[nt], acc[nt][j]);
-            } else {
-              acc[nt][j] = mfma_f16(a, p_hi[nt], acc[nt][j]);
-              acc[nt][j] = mfma_f16(a, p_lo[nt], acc[nt][j]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x) {
+              if constexpr (CT == kBF16)
+                acc[nt][j] = mfma_bf16(a, parts[nt][x], acc[nt][j]);
+              else
+                acc[nt][j] = mfma_f16(a, parts[nt][x], acc[nt][j]);
             }
-          }
         };
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {

@@ -11,6 +11,9 @@ pytestmark = pytest.mark.gpu
 CASES = [
     ("e4m3", "bf16", 300, 8, 8, 128), ("e4m3", "bf16", 40, 40, 2, 64), ("e4m3", "bf16", 64, 4, 1, 32),
     ("e4m3", "f32", 300, 32, 8, 128), ("e4m3", "f32", 33, 5, 5, 64), ("e4m3", "f32", 9, 17, 1, 128),
+    ("bf16", "bf16", 300, 32, 8, 128), ("bf16", "bf16", 40, 40, 2, 64), ("bf16", "bf16", 64, 4, 1, 32),
+    ("bf16", "f32", 300, 8, 8, 128), ("bf16", "f32", 33, 5, 5, 64), ("bf16", "f32", 9, 17, 1, 128),
+    ("f32", "f32", 300, 8, 4, 64), ("f32", "f32", 9, 5, 5, 128), ("f32", "bf16", 33, 17, 1, 32),
 ]
 
 

@@ -16,6 +16,16 @@ def fp16_parts(n):
     return rounded
 
 
+def bf16_parts(n):
+    def rounded(w):
+        rest, total = w, 0.0
+        for _ in range(n):
+            part = to_bf16(rest)
+            rest, total = rest - part, total + part
+        return total
+    return rounded
+
+
 def results(cache, out, weight):
     x = make((81, 1), cache, 40, 8, 2, 32)
     o, s = reference(*x)
@@ -28,3 +38,16 @@ def test_one_fp16_part_is_seen_and_two_pass(out):
     bad, n = results("e4m3", out, fp16_parts(1))
     assert bad > n / 100
     assert results("e4m3", out, fp16_parts(2))[0] == 0
+
+
+@pytest.mark.parametrize("n", [1, 2])
+def test_too_few_bf16_parts_are_seen_and_three_pass(n):
+    bad, size = results("bf16", "f32", bf16_parts(n))
+    assert bad > size / 100
+    assert results("bf16", "f32", bf16_parts(3))[0] == 0
+
+
+def test_one_bf16_part_is_seen_in_bf16_results():
+    """(Two are not: 2^-17 moves too few results past the edge of a bf16 step by more than the bound.)"""
+    assert results("bf16", "bf16", bf16_parts(1))[0] > 0
+    assert results("bf16", "bf16", bf16_parts(3))[0] == 0
