@@ -370,7 +370,9 @@ def check_gates(g, beta, stream=None, counts=None) -> int:
 
 
 # ---- the layers beside KDA: a paged key/value cache, and the verification of drafts. The tensors
-#      are marshalled in csrc/torch/marshal.cpp (built as _marshal.so).
+#      are marshalled in csrc/torch/marshal.cpp (built as _marshal.so). With a stream given, a call runs there
+#      (the caller orders it after what wrote its tensors), what it allocates is that stream's memory,
+#      and results may be used on the current stream once that has waited for it.
 
 _ops = None
 

@@ -10,6 +10,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -19,6 +20,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <optional>
 
 #include "kda.h"
 
@@ -155,39 +157,41 @@ void page_cache(const On& on, const at::Tensor& k, const at::Tensor& v, const at
   c->v_scale = v_scale ? static_cast<const float*>(v_scale->data_ptr()) : nullptr;
 }
 
-// The stream of a call: the one given (a torch.cuda.Stream), or the device's current one. A tensor
-// allocated here for another stream than the current one is recorded on it, so that its memory is
-// not handed out again before that stream is done with it.
+// The stream of a call: the one given (a torch.cuda.Stream), or the device's current one. What is
+// allocated here for a given stream comes from that stream's memory: memory of the current stream may
+// have been freed while work queued there still uses it, and only that stream waits for that work.
+// The other way round, a result's memory is not handed out again before the current stream, where
+// the caller is, is done with it.
 struct Stream {
-  PyObject* given;
+  std::optional<c10::Stream> given, current;
   void* raw;
-  Stream(PyObject* o, const On& on) : given(o == Py_None ? nullptr : o) {
-    if (!given) {
-      raw = c10::hip::getCurrentHIPStream(on.device.index()).stream();
-      return;
-    }
-    const int64_t index = attribute("device_index");
-    if (index != on.device.index())
+  Stream(PyObject* o, const On& on) {
+    const c10::hip::HIPStream now = c10::hip::getCurrentHIPStream(on.device.index());
+    raw = now.stream();
+    if (o == Py_None) return;
+    if (attribute(o, "device_index") != on.device.index())
       value_error("the stream must be of %s", on.device.str().c_str());
-    raw = reinterpret_cast<void*>(attribute("cuda_stream"));
+    void* const own = reinterpret_cast<void*>(attribute(o, "cuda_stream"));
+    if (own == raw) return;
+    raw = own;
+    given = c10::Stream(c10::Stream::UNSAFE, on.device, attribute(o, "stream_id"));
+    current = c10::Stream(c10::Stream::UNSAFE, on.device, now.id());
   }
-  int64_t attribute(const char* name) const {
-    PyObject* a = PyObject_GetAttrString(given, name);
+  static int64_t attribute(PyObject* o, const char* name) {
+    PyObject* a = PyObject_GetAttrString(o, name);
     if (!a) throw python_error();
     const int64_t x = PyLong_AsLongLong(a);
     Py_DECREF(a);
     if (x == -1 && PyErr_Occurred()) throw python_error();
     return x;
   }
+  at::Tensor scratch(at::IntArrayRef shape, at::ScalarType type, const On& on) const {
+    const c10::OptionalStreamGuard guard(given);
+    return at::empty(shape, at::TensorOptions().dtype(type).device(on.device));
+  }
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const On& on) const {
-    at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(on.device));
-    if (given) {
-      PyObject* w = THPVariable_Wrap(t);
-      PyObject* r = w ? PyObject_CallMethod(w, "record_stream", "O", given) : nullptr;
-      Py_XDECREF(w);
-      if (!r) throw python_error();
-      Py_DECREF(r);
-    }
+    at::Tensor t = scratch(shape, type, on);
+    if (given && t.numel()) t.record_stream(*current);
     return t;
   }
 };
@@ -205,7 +209,7 @@ void workspace(Args* a, Opt given, size_t (*bytes)(const Args*), const Stream& s
   }
   const size_t n = bytes(a);
   if (n == 0 || n == SIZE_MAX) return;  // if invalid, the call itself says what is wrong
-  *own = s.empty({(int64_t)n}, at::kByte, on);
+  *own = s.scratch({(int64_t)n}, at::kByte, on);
   a->workspace = own->data_ptr();
   a->workspace_bytes = n;
 }
