@@ -185,6 +185,23 @@ def _stream(stream) -> _P:
     return _P(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream=None, result=True) -> torch.Tensor:
+    """A device tensor for a call on `stream`. It is that stream's memory: a block of the current
+    stream's may still be in use by work queued there, which `stream` does not wait for. A result is
+    recorded on the current stream, where the caller is, so that it is not handed out again before
+    that stream is done with it."""
+    now = None if stream is None else torch.cuda.current_stream(device)
+    if now is None or stream.cuda_stream == now.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(now)
+    return t
+
+
 def chunk_args(q, k, v, g, beta, S0=None, cu_seqlens=None, *, chunk=64, o=None, S_T=None,
                workspace=None, generic=False, ckpt=None, ckpt_every=0,
                pairwise_diag=False, segments=0, walk64=False, walk128=False) -> ChunkArgs:
@@ -226,11 +243,12 @@ def chunk_fwd_workspace_bytes(q, k, v, g, beta, S0=None, cu_seqlens=None, *, chu
     return int(n)
 
 
-def alloc_workspace(nbytes: int, device) -> Optional[torch.Tensor]:
-    """Device scratch for kda_chunk_fwd (torch's allocator returns 256-byte aligned blocks)."""
+def alloc_workspace(nbytes: int, device, stream=None) -> Optional[torch.Tensor]:
+    """Device scratch for kda_chunk_fwd (torch's allocator returns 256-byte aligned blocks), for
+    calls on `stream` (by default the current one)."""
     if nbytes == 0:
         return None
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _empty(nbytes, torch.uint8, device, stream, result=False)
 
 
 def chunk_fwd(q, k, v, g, beta, S0=None, cu_seqlens=None, *, chunk=64,
@@ -259,16 +277,16 @@ def chunk_fwd(q, k, v, g, beta, S0=None, cu_seqlens=None, *, chunk=64,
     dv = v.shape[-1]
     n_seq = B if cu_seqlens is None else cu_seqlens.numel() - 1
     if o is None:
-        o = torch.empty((B, T, H, dv), dtype=out_dtype, device=q.device)
+        o = _empty((B, T, H, dv), out_dtype, q.device, stream)
     else:
         _dev(o, "o")
     if S_T is None and want_state:
-        S_T = torch.empty((n_seq, H, dk, dv), dtype=torch.float32, device=q.device)
+        S_T = _empty((n_seq, H, dk, dv), torch.float32, q.device, stream)
     if workspace is None:
         nbytes = chunk_fwd_workspace_bytes(q, k, v, g, beta, S0, cu_seqlens, chunk=chunk,
                                            generic=generic, segments=segments, walk64=walk64,
                                            walk128=walk128, ckpt_every=ckpt_every)
-        workspace = alloc_workspace(nbytes, q.device)
+        workspace = alloc_workspace(nbytes, q.device, stream)
     if ckpt_every:
         if ckpt is None:
             raise ValueError("ckpt_every needs a ckpt buffer (size it with checkpoint_slots)")
@@ -318,7 +336,7 @@ def decode_step(q, k, v, g, beta, S, *, o=None, out_dtype=torch.float32, stream=
     for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("S", S)):
         _dev(t, name)
     if o is None:
-        o = torch.empty((q.shape[0], q.shape[1], v.shape[-1]), dtype=out_dtype, device=q.device)
+        o = _empty((q.shape[0], q.shape[1], v.shape[-1]), out_dtype, q.device, stream)
     a = decode_args(q, k, v, g, beta, S, o)
     _check(lib().kda_decode_step(ctypes.byref(a), _stream(stream)))
     return o
@@ -338,7 +356,7 @@ def decode_multi(q, k, v, g, beta, S, *, accept=None, o=None, want_output=True,
         if accept.dtype != torch.int32 or accept.numel() != N:
             raise ValueError("accept must be int32 [N]")
     if o is None and want_output:
-        o = torch.empty((N, m, H, v.shape[-1]), dtype=out_dtype, device=q.device)
+        o = _empty((N, m, H, v.shape[-1]), out_dtype, q.device, stream)
     elif o is not None:
         _dev(o, "o")
     a = DecodeMultiArgs()
@@ -358,7 +376,7 @@ def check_gates(g, beta, stream=None, counts=None) -> int:
     _dev(g, "g")
     _dev(beta, "beta")
     if counts is None:
-        counts = torch.empty(CHECK_COUNTERS, dtype=torch.int64, device=g.device)
+        counts = _empty(CHECK_COUNTERS, torch.int64, g.device, stream, result=False)
     _dev(counts, "counts")
     if counts.dtype != torch.int64:
         raise TypeError("counts must be int64")

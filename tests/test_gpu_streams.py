@@ -118,3 +118,45 @@ def test_a_freed_result_waits_for_the_current_stream():
         assert all(t.data_ptr() != address for t in taken)
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+@pytest.mark.parametrize("call,count", [("chunk_fwd", 3), ("decode_step", 1), ("decode_multi", 1), ("check_gates", 1)])
+def test_kda_calls(call, count):
+    import torch
+    from gated_delta_rule_59_amd import binding, inputs
+    if call in ("chunk_fwd", "check_gates"):
+        x = inputs.make_prefill(1, T=130, H=2)
+        dev = [torch.from_numpy(a).cuda().bfloat16() for a in (x.q, x.k, x.v, x.g, x.beta)]
+        S0 = torch.from_numpy(x.S0).cuda()
+        if call == "chunk_fwd":
+            run = lambda **kw: binding.chunk_fwd(*dev, S0, **kw)  # noqa: E731
+        else:
+            run = lambda **kw: (torch.tensor(binding.check_gates(dev[3], dev[4], **kw)),)  # noqa: E731
+    else:
+        dev = [torch.from_numpy(a).cuda().bfloat16() for a in inputs.make_decode_step(0, N=4, H=2)]
+        S = torch.from_numpy(inputs.make_decode_state(4, 2)).cuda()
+        if call == "decode_step":
+            run = lambda **kw: (binding.decode_step(*dev, S0.copy_(S), **kw),)  # noqa: E731
+            S0 = S.clone()
+        else:
+            run = lambda **kw: (binding.decode_multi(*[a[:, None] for a in dev], S, **kw),)  # noqa: E731
+    want = run()
+    torch.cuda.synchronize()
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for current in (torch.cuda.current_stream(), other):
+        with torch.cuda.stream(current):
+            if call == "decode_step":  # the copy into S0 comes before the call on s
+                S0.copy_(S)
+                torch.cuda.synchronize()
+                with Allocations() as at:
+                    got = (binding.decode_step(*dev, S0, stream=s),)
+            else:
+                with Allocations() as at:
+                    got = run(stream=s)
+            assert at.streams == [s.cuda_stream] * count
+            assert torch.cuda.current_stream() == current
+            with Allocations() as at:
+                run()
+            assert at.streams == [current.cuda_stream] * count
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
