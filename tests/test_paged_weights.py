@@ -51,3 +51,16 @@ def test_one_bf16_part_is_seen_in_bf16_results():
     """(Two are not: 2^-17 moves too few results past the edge of a bf16 step by more than the bound.)"""
     assert results("bf16", "bf16", bf16_parts(1))[0] > 0
     assert results("bf16", "bf16", bf16_parts(3))[0] == 0
+
+
+@pytest.mark.parametrize("cache,rounded", [("bf16", bf16_parts(1)), ("f32", bf16_parts(1)), ("e4m3", fp16_parts(1))])
+def test_a_bound_for_each_row_sees_lost_bits(cache, rounded):
+    from tests import paged_rows
+    rng = np.random.default_rng(83)
+    lens = [2, 3, 40]
+    q = to_bf16(rng.standard_normal((3, 1, 4, 64)))
+    k, v = ([to_bf16(rng.standard_normal((n, 2, 64))) for n in lens] for _ in "kv")
+    o, off, _, _ = paged_rows.attend_rows(q, k, v, lens, 0.01, 0, cache)
+    assert not paged_rows.outside(o.astype(np.float32), o, off, "f32").any()
+    got, _, _, _ = paged_rows.attend_rows(q, k, v, lens, 0.01, 0, cache, weight=rounded)
+    assert paged_rows.outside(got, o, off, "f32").mean() > 0.1
