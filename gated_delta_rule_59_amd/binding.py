@@ -428,7 +428,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, start, *, q=None, q_out=None,
 
 def paged_decode_workspace_bytes(q, k_cache, v_cache, block_table, seq_lens, *, window=0,
                                  max_len=None, k_scale=None, v_scale=None) -> int:
-    """Bytes of workspace that paged_decode needs for these arguments."""
+    """Bytes of workspace that paged_decode needs for these arguments (the most with window 0 and the
+    longest max_len)."""
     return _marshal().paged_decode(q, k_cache, v_cache, block_table, seq_lens, None, window, max_len,
                                    k_scale, v_scale, None, None, torch.float32, False, None)
 

@@ -75,6 +75,9 @@ size_t plan_paged_decode(PagedDecodePlan* p) {
     const int64_t pairs = (int64_t)p->N * p->row_blocks * p->groups;
     p->hold = (int)std::min(room, entry * ((pairs + p->split - 1) / p->split + 2)) & ~15;
   }
+  // Grows with the units, so a window or a smaller max_len never needs more: split does; and where heads
+  // grows instead, at all * units = 4 * shared, the further heads' parts (1 KiB and more for each
+  // workgroup) are more than the shorter table of parts saves (32 B for each at most).
   return parts(*p) * (p->d + 2) * sizeof(float) + (size_t)(all / p->heads) * 2 * sizeof(int);
 }
 

@@ -423,7 +423,9 @@ typedef struct {
 kda_status kda_kv_append(const kda_kv_append_args* args, void* hip_stream);
 
 /* Attention of new tokens over a paged cache (see kda_paged_decode_args). The workspace query
- * looks at shapes, dtypes and max_len, not at pointers; SIZE_MAX when they are invalid. */
+ * looks at shapes, dtypes, max_len and window, not at pointers; SIZE_MAX when they are invalid. A
+ * window or a smaller max_len never needs more: the size for window = 0 and the longest max_len
+ * serves every call of otherwise the same shapes. */
 size_t kda_paged_decode_workspace_bytes(const kda_paged_decode_args* args);
 kda_status kda_paged_decode(const kda_paged_decode_args* args, void* hip_stream);
 
