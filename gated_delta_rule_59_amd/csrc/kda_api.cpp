@@ -38,6 +38,9 @@ kda_status ok() {
 // 256-work-item workgroup per (sequence, head).
 constexpr int64_t kMaxGridItems = 0xffffffffLL;
 constexpr int64_t kMaxDecodePairs = kMaxGridItems / 256;
+// kda_verify_drafts: a 64-work-item workgroup per sequence; its other launch has a wave per sequence too,
+// or 65,536 waves.
+constexpr int64_t kMaxVerifySequences = kMaxGridItems / 64;
 
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
@@ -371,8 +374,8 @@ kda_status validate_verify_shapes(const kda_verify_args* a) {
     return fail(KDA_ERR_BAD_SHAPE, "need N, m, V >= 1 (got N=%d m=%d V=%d)", a->N, a->m, a->V);
   if (!dtype_ok(a->dtype)) return fail(KDA_ERR_BAD_DTYPE, "unknown dtype");
   if (a->m > (1 << 24)) return fail(KDA_ERR_BAD_SHAPE, "m too large (got %d)", a->m);
-  if (a->V > (1 << 30) || kda::verify_blocks(a->N, a->V) > kMaxDecodePairs)
-    return fail(KDA_ERR_BAD_SHAPE, "N * V too large for one launch");
+  if (a->V > (1 << 30)) return fail(KDA_ERR_BAD_SHAPE, "V too large (got %d)", a->V);
+  if (a->N > kMaxVerifySequences) return fail(KDA_ERR_BAD_SHAPE, "N too large for one launch (got %d)", a->N);
   return KDA_OK;
 }
 

@@ -146,7 +146,6 @@ struct VerifyPlan {
   void* workspace;
 };
 size_t verify_workspace_bytes(int N, int V);
-int64_t verify_blocks(int N, int V);  // workgroups of its larger launch
 hipError_t launch_verify(const VerifyPlan& p, hipStream_t stream);
 
 // Device check of g in [-5, 0] and beta in [0, 1] over n_blocks workgroups (1 .. check_blocks());

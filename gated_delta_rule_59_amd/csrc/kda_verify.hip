@@ -320,10 +320,7 @@ hipError_t launch_t(const VerifyPlan& p, hipStream_t stream) {
 
 }  // namespace
 
-int64_t verify_blocks(int N, int V) { return row_blocks(V) * N; }
-size_t verify_workspace_bytes(int N, int V) {
-  return (size_t)verify_blocks(N, V) * 2 * sizeof(double);
-}
+size_t verify_workspace_bytes(int N, int V) { return (size_t)(row_blocks(V) * N) * 2 * sizeof(double); }
 hipError_t launch_verify(const VerifyPlan& p, hipStream_t stream) {
   return p.bf16 ? launch_t<uint16_t>(p, stream) : launch_t<float>(p, stream);
 }
