@@ -2,12 +2,14 @@
 
     python -m gated_delta_rule_59_amd.build
 
-hipcc compiles every source under csrc/ and links one shared library, libkda.so. The host
-compiler builds csrc/torch/marshal.cpp, which marshals torch tensors into it, as _marshal.so.
+hipcc compiles every source under csrc/ and links one shared library, libkda.so. Where torch is
+installed, the host compiler builds csrc/torch/marshal.cpp, which marshals torch tensors into it, as
+_marshal.so; the library needs neither.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -29,11 +31,14 @@ MARSHAL = os.path.join(HERE, "_marshal.so")
 CXX = os.environ.get("CXX", "g++")
 
 
-def marshal_command(out: str) -> list:
+def marshal_command(out: str):
+    """The compiler's command line for the marshalling module; None without torch."""
     import sysconfig
 
-    import torch
-    root = os.path.dirname(torch.__file__)
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        return None
+    root = os.path.dirname(torch.origin)
     dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
             sysconfig.get_paths()["include"], "/opt/rocm/include"]
     lib = os.path.join(root, "lib")
@@ -52,15 +57,12 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(objdir, exist_ok=True)
     procs, objs = [], []
     marshal = MARSHAL + ".tmp%d" % os.getpid()
-    procs.append(("marshal.cpp", subprocess.Popen(marshal_command(marshal), stdout=subprocess.PIPE,
-                                                  stderr=subprocess.STDOUT)))
+    marshal_cmd = marshal_command(marshal)
+    marshal_proc = marshal_cmd and _start(marshal_cmd, verbose)
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         objs.append(obj)
-        cmd = [HIPCC, *FLAGS, "-x", "hip", "-c", src, "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        procs.append((src, _start([HIPCC, *FLAGS, "-x", "hip", "-c", src, "-o", obj], verbose)))
         if len(procs) >= jobs:
             _wait(procs.pop(0))
     for p in procs:
@@ -68,8 +70,19 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
-    os.replace(marshal, MARSHAL)
+    # after the library, which does not wait for it
+    if marshal_proc:
+        _wait(("csrc/torch/marshal.cpp", marshal_proc))
+        os.replace(marshal, MARSHAL)
+    else:
+        sys.stderr.write("torch is not installed: _marshal.so is not built\n")
     return LIB
+
+
+def _start(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 
 def _wait(item):
