@@ -359,7 +359,6 @@ kda_status validate_decode_shapes(const kda_paged_decode_args* a, kda::PagedDeco
     return fail(KDA_ERR_BAD_SHAPE, "N * m * Hq or max_len * m * Hq too large for one launch");
   *p = kda::PagedDecodePlan{};
   p->N = a->N, p->m = a->m, p->Hq = a->Hq, p->Hkv = a->Hkv, p->d = a->d;
-  p->act_bf16 = a->act_dtype == KDA_BF16;
   p->out_bf16 = a->out_dtype == KDA_BF16;
   p->cache_type = a->cache.dtype;
   p->max_len = a->max_len;

@@ -5,7 +5,7 @@
 // written once, so HBM bounds the call; the angles are formed once per token and shared by all
 // heads of q and k through LDS.
 //
-// Angles: p f_i is exact in 64 bits (31 + 24 bits, rounded at 53), and is reduced there to a
+// Angles: p f_i is formed in 64 bits (31 + 24 bits, rounded at 53) and is reduced there to a
 // quarter turn, so the 32-bit sine and cosine see |angle| <= pi/4 whatever the position. (In 32
 // bits a position of 10^5 would leave an angle off by 10^-2.)
 //

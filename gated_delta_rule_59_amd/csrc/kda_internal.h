@@ -105,7 +105,7 @@ struct PagedDecodePlan {
   int group, rows;               // Hq / Hkv; m * group query rows per key/value head
   int row_blocks;                // blocks of 16 * tiles rows
   int tiles;                     // 16-row tiles a workgroup carries
-  bool act_bf16, out_bf16;
+  bool out_bf16;
   int cache_type;
   const char* q;                 // strides in bytes
   int64_t q_token, q_head;

@@ -5,7 +5,8 @@
 // as the columns of one 16 x 16 tile. One pass over the cache keeps the running maximum and sum
 // of each row's softmax:
 //     M' = max(M, max s),  l' = l 2^{M - M'} + sum 2^{s - M'},  O' = O 2^{M - M'} + sum 2^{s - M'} v
-// (s in units of log2). The cache is read once and nothing else is large: HBM bounds it.
+// (s in units of log2). Up to 32 rows the cache is read once (every 32 rows, a row block, read it again)
+// and nothing else is large: HBM bounds it.
 //
 // Layout (no LDS and no cross-lane move between load and product). A wave takes 32 tokens at a
 // time. v_mfma 16x16x32: lane l = (r = l & 15, g = l >> 4).
@@ -98,7 +99,7 @@ struct Types {
   static constexpr int QW = CT == kF32 ? D / 4 : D / 8;  // words of a query row per lane
 };
 
-// Streamed: each cached value is read once (4 contexts of 65k tokens: 222 -> 213 us; a plain read
+// Streamed: each cached value is read once per row block (4 contexts of 65k tokens: 222 -> 213 us; a plain read
 // of 4 GiB runs at 7.1 TB/s with such loads, at 6.2 without).
 template <int W>
 __device__ __forceinline__ void load_words(const char* p, uint32_t* w) {
@@ -873,7 +874,7 @@ __global__ __launch_bounds__(256, 6) void paged_join_kernel(const PagedDecodePla
   const int w0 = of[0], count = of[1] - w0 + 1;
   if (count == 1) return;
 
-  int lanes = SETS;  // sets per row, a power of two: four parts or more each
+  int lanes = SETS;  // sets per row, a power of two: two parts or more each
   while (lanes > 1 && lanes * 2 >= count) lanes /= 2;
   const int lane = set % lanes, at_once = SETS / lanes;
   const int row0 = rb * cols, c1 = min(min(cols, p.rows - row0), ((int)blockIdx.y + 1) * rows);

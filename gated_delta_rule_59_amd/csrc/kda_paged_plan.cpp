@@ -69,7 +69,8 @@ size_t plan_paged_decode(PagedDecodePlan* p) {
   if (p->heads == 4) {
     // room for a workgroup's share of the pairs, one more that it shares at either end, and one that
     // is uneven; at most what the CU has (160 KiB for its one or two workgroups, less 512 B that they
-    // use otherwise and a scratch of 32 tokens x rows), which is two results or more
+    // use otherwise and a scratch of 32 tokens x rows), which is one result at least: e4m3 heads of 64
+    // channels with 32 rows have room for one fp32 result (8,736 of 16,256 B), others for two or more
     const int64_t entry = sizeof(paged::Held) + p->part_rows * (p->d * (int64_t)sizeof(float) + paged::kHeldPad);
     const int64_t room = (160 * 1024 * 256 / shared - 512) / 4 - 32 * 16 * p->tiles * (int64_t)sizeof(float);
     const int64_t pairs = (int64_t)p->N * p->row_blocks * p->groups;

@@ -307,12 +307,12 @@ typedef struct {
  *              if q is contiguous; otherwise it overlaps no input.
  *   start      device int32 [n_seq]: tokens of each sequence in the cache so far. New token j
  *              has position start[n] + j, and goes to slot position % page_size of page
- *              position / page_size. Tokens whose position is negative or at or past
- *              max_pages * page_size are not stored; their q_out is written all the same. Two
- *              new tokens must not go to the same slot of the same page.
+ *              position / page_size. Tokens whose position is negative, or at or past
+ *              max_pages * page_size or 2^31, are not stored; their q_out is written all the
+ *              same. Two new tokens must not go to the same slot of the same page.
  *   inv_freq   device fp32 [rot / 2], or NULL with rot = 0 (no rotation: k is stored and q
  *              copied as they are). Channel pair i < rot / 2 of a token at position p is turned
- *              by the angle p * inv_freq[i] (exact product, reduced in 64 bits):
+ *              by the angle p * inv_freq[i] (formed and reduced in 64 bits):
  *                  x' = x cos - y sin,   y' = y cos + x sin.
  *   rot        channels that turn, a multiple of 16, 0 <= rot <= d. Channels rot .. d - 1 stay.
  *   flags      0: pair i is channels (i, i + rot / 2). KDA_APPEND_PAIRS: (2i, 2i + 1).
@@ -352,8 +352,9 @@ typedef struct {
  *   scale      finite; o = softmax(scale * q k^T) v, scores in 32 bits (beyond 3.4e38 they are
  *              infinite). New token j of sequence n sees positions
  *              t < hi = seq_lens[n] - m + 1 + j, with a window t >= hi - window too. What it does
- *              not see does not reach it, NaN and infinities included. If it sees none, its o
- *              is 0 and its lse -inf.
+ *              not see does not reach it, NaN and infinities included; a value that it does
+ *              see and that is not finite makes its channel of o infinite or NaN. If it sees
+ *              none, its o is 0 and its lse -inf.
  *   o          [N, m, Hq, d] contiguous, out_dtype, 16-byte aligned.
  *   lse        fp32 [N, m, Hq], or NULL: natural logarithm of sum_t e^{scale q k_t} (for joining
  *              results over parts of a context).
