@@ -38,9 +38,9 @@ kda_status ok() {
 // 256-work-item workgroup per (sequence, head).
 constexpr int64_t kMaxGridItems = 0xffffffffLL;
 constexpr int64_t kMaxDecodePairs = kMaxGridItems / 256;
-// kda_verify_drafts: a 64-work-item workgroup per sequence; its other launch has a wave per sequence too,
-// or 65,536 waves.
-constexpr int64_t kMaxVerifySequences = kMaxGridItems / 64;
+// kda_verify_drafts: a wave per sequence, in workgroups of four in one launch and alone in the other;
+// where the first has more waves than sequences, they are at most 65,536.
+constexpr int64_t kMaxVerifySequences = 4 * kMaxDecodePairs;
 
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 bool dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }

@@ -42,8 +42,8 @@ def test_a_window_or_a_shorter_bound_needs_no_more(b):
 
 
 def test_verification_is_limited_by_its_launches(b):
-    """Sequences times blocks of 1024 tokens are no limit of the launches, which have a workgroup of 64
-    per sequence and at most 65,536 waves or a wave per sequence."""
+    """Sequences times blocks of 1024 tokens are no limit of the launches, which have a wave per sequence,
+    or at most 65,536 waves, in whole workgroups of 256."""
     def need(N, V):
         a = b.VerifyArgs()
         a.N, a.m, a.V, a.dtype = N, 4, V, 1
@@ -51,6 +51,6 @@ def test_verification_is_limited_by_its_launches(b):
 
     assert need(1 << 15, 1 << 20) == 1 << 29       # 32,768 sequences over 2^20 tokens
     assert need(1, 1 << 30) == 1 << 24
-    most = (2 ** 32 - 1) // 64
+    most = 4 * ((2 ** 32 - 1) // 256)               # four sequences to a workgroup of 256
     assert need(most, 1) == 16 * most and need(most + 1, 1) == b.SIZE_MAX
     assert need(1, (1 << 30) + 1) == b.SIZE_MAX
