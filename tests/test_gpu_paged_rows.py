@@ -104,3 +104,30 @@ def test_values_that_are_not_finite_with_two_row_tiles(cache, N, page, window):
             assert np.isnan(got[:, j]).all(), j
         else:
             assert np.isposinf(got[:, j]).all(), j
+
+
+@pytest.mark.parametrize("cache,m", [("bf16", 1), ("e4m3", 2), ("bf16", 5)])
+def test_four_heads_to_a_workgroup_captured_and_replayed(cache, m):
+    """The launch that asks for more LDS than is given unasked, captured; lengths change between
+    replays, with eager calls in between."""
+    import torch
+    from gated_delta_rule_59_amd import binding
+    N, scale = 270, 0.05
+    lens = [[300 - i for i in range(N)], [(7 * i) % 301 for i in range(N)], [0] * (N - 1) + [300]]
+    dev, _ = make((75, m), [300] * N, m, 32, 8, 64, 16, cache, poison=False)
+    want = []
+    for x in lens:
+        dev["seq_lens"].copy_(torch.tensor(x))
+        want.append(binding.paged_decode(**dev, scale=scale))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = binding.paged_decode(**dev, scale=scale)
+    for i in (0, 1, 2, 1, 0):
+        dev["seq_lens"].copy_(torch.tensor(lens[i]))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[i])
+        assert torch.equal(binding.paged_decode(**dev, scale=scale), want[i])
+        torch.cuda.synchronize()
+    assert (want[2][:-1] == 0).all() and (want[2][-1] != 0).any()
