@@ -19,6 +19,8 @@ KDA_FLAG_PAIRWISE_DIAG = 2
 KDA_FLAG_WALK64 = 4
 KDA_FLAG_WALK128 = 8
 KDA_APPEND_PAIRS = 1
+KDA_LIN_FIXED_DECAY = 1
+KDA_LOGITS_PROBS = 1
 ABI_VERSION = 4  # KDA_ABI_VERSION of include/kda.h this binding marshals for
 STATUS = {0: "KDA_OK", 1: "KDA_ERR_NULL_PTR", 2: "KDA_ERR_BAD_SHAPE", 3: "KDA_ERR_BAD_DTYPE",
           4: "KDA_ERR_UNSUPPORTED", 5: "KDA_ERR_DECAY_RANGE", 6: "KDA_ERR_WORKSPACE",
@@ -103,6 +105,46 @@ class VerifyArgs(ctypes.Structure):
                 ("tokens", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
 
 
+_LIN = ([("act_dtype", ctypes.c_int), ("gate_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+         ("q", _P), ("k", _P), ("v", _P)]
+        + [(f"{x}_{y}_stride", ctypes.c_int64) for x in "qkv" for y in ("token", "head")]
+        + [("g", _P), ("scale", ctypes.c_float)])
+
+
+class LinChunkArgs(ctypes.Structure):
+    _fields_ = ([(x, ctypes.c_int) for x in ("B", "T", "Hk", "H", "dk", "dv")]
+                + [("cu_seqlens", _P), ("N", ctypes.c_int)] + _LIN
+                + [("S0", _P), ("o", _P), ("S_T", _P), ("workspace", _P),
+                   ("workspace_bytes", ctypes.c_size_t), ("flags", ctypes.c_uint)])
+
+
+class LinDecodeArgs(ctypes.Structure):
+    _fields_ = ([(x, ctypes.c_int) for x in ("N", "m", "Hk", "H", "dk", "dv")] + _LIN
+                + [("S", _P), ("o", _P), ("accept", _P), ("flags", ctypes.c_uint)])
+
+
+class PagePlanArgs(ctypes.Structure):
+    _fields_ = ([(x, ctypes.c_int) for x in ("N", "page_size", "max_pages", "max_tokens",
+                                             "free_capacity")]
+                + [("block_table", _P), ("table_stride", ctypes.c_int64)]
+                + [(x, _P) for x in ("held", "lens", "new_lens", "free_pages", "ring", "held_out",
+                                     "ring_out", "seq_lens", "cu_seqlens", "slots", "positions")])
+
+
+class LogitsArgs(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("R", ctypes.c_int), ("V", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("logits", _P),
+                ("seq_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("out", _P),
+                ("out_seq_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+                ("history", _P), ("history_stride", ctypes.c_int64), ("max_history", ctypes.c_int),
+                ("history_lens", _P), ("prompt_lens", _P), ("drafts", _P), ("repetition", _P),
+                ("frequency", _P), ("presence", _P), ("bias_ids", _P), ("bias", _P),
+                ("bias_counts", _P), ("max_bias", ctypes.c_int), ("mask", _P),
+                ("mask_seq_stride", ctypes.c_int64), ("mask_row_stride", ctypes.c_int64),
+                ("temperature", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
+                ("flags", ctypes.c_uint)]
+
+
 class KDAError(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__(f"{STATUS.get(status, status)}: {detail}")
@@ -134,10 +176,13 @@ def lib() -> ctypes.CDLL:
                                       ctypes.c_int, _P, ctypes.POINTER(ctypes.c_int64)]
         L.kda_check_gates.restype = ctypes.c_int
         for name, args in (("kv_append", KvAppendArgs), ("paged_decode", PagedDecodeArgs),
-                           ("verify_drafts", VerifyArgs)):
+                           ("verify_drafts", VerifyArgs), ("lin_chunk_fwd", LinChunkArgs),
+                           ("lin_decode_step", LinDecodeArgs), ("lin_decode_multi", LinDecodeArgs),
+                           ("page_plan", PagePlanArgs), ("adjust_logits", LogitsArgs)):
             f = getattr(L, "kda_" + name)
             f.argtypes, f.restype = [ctypes.POINTER(args), _P], ctypes.c_int
-        for name, args in (("paged_decode", PagedDecodeArgs), ("verify_drafts", VerifyArgs)):
+        for name, args in (("paged_decode", PagedDecodeArgs), ("verify_drafts", VerifyArgs),
+                           ("lin_chunk_fwd", LinChunkArgs), ("adjust_logits", LogitsArgs)):
             f = getattr(L, f"kda_{name}_workspace_bytes")
             f.argtypes, f.restype = [ctypes.POINTER(args)], ctypes.c_size_t
         L.kda_status_string.argtypes = [ctypes.c_int]
@@ -387,8 +432,8 @@ def check_gates(g, beta, stream=None, counts=None) -> int:
     return int(n.value)
 
 
-# ---- the layers beside KDA: a paged key/value cache, and the verification of drafts. The tensors
-#      are marshalled in csrc/torch/marshal.cpp (built as _marshal.so). With a stream given, a call runs there
+# ---- the layers beside KDA: a paged key/value cache, the verification of drafts, linear attention with a
+#      decay for each head, the plan of a step's pages, and logits to probabilities. The tensors are marshalled in csrc/torch/marshal.cpp (built as _marshal.so). With a stream given, a call runs there
 #      (the caller orders it after what wrote its tensors), what it allocates is that stream's memory,
 #      and results may be used on the current stream once that has waited for it.
 
@@ -407,7 +452,10 @@ def _marshal():
                                "python -m gated_delta_rule_59_amd.build") from e
         ops.bind(*[ctypes.cast(f, _P).value for f in (
             L.kda_kv_append, L.kda_paged_decode, L.kda_paged_decode_workspace_bytes,
-            L.kda_verify_drafts, L.kda_verify_drafts_workspace_bytes, L.kda_last_error)], KDAError)
+            L.kda_verify_drafts, L.kda_verify_drafts_workspace_bytes, L.kda_lin_chunk_fwd,
+            L.kda_lin_chunk_fwd_workspace_bytes, L.kda_lin_decode_step, L.kda_lin_decode_multi,
+            L.kda_page_plan, L.kda_adjust_logits, L.kda_adjust_logits_workspace_bytes,
+            L.kda_last_error)], KDAError)
         _ops = ops
     return _ops
 
@@ -457,3 +505,72 @@ def verify_drafts(p, q, drafts, uniform, *, n_drafts=None, accept=None, tokens=N
     Returns (accept int32 [N], tokens int32 [N, m + 1]): the drafts that stand, and those drafts,
     the following token, then -1. accept is the `accept` of a decode_multi over the drafts."""
     return (_ops or _marshal()).verify_drafts(p, q, drafts, uniform, n_drafts, accept, tokens, workspace, stream)
+
+
+# ---- linear attention with a decay for each head: S <- e^g S + k v^T, o = scale S^T q
+
+def lin_chunk_fwd_workspace_bytes(q, k, v, g, S0=None, cu_seqlens=None) -> int:
+    """Bytes of workspace that lin_chunk_fwd needs for these arguments."""
+    return _marshal().lin_chunk_fwd(q, k, v, g, S0, cu_seqlens, 1.0, None, None, False, torch.float32,
+                                    False, None)
+
+
+def lin_chunk_fwd(q, k, v, g, S0=None, cu_seqlens=None, *, scale=1.0, out_dtype=torch.float32, o=None,
+                  S_T=None, want_state=True, workspace=None, stream=None):
+    """Prompts through linear attention with a decay for each head. q, k [B, T, Hk, dk]; v [B, T, H, dv]
+    (bf16 or fp32; strided views with contiguous channels will do; head h reads query and key head
+    h / (H / Hk)); g the logarithms of the decays, [B, T, H], or [H] for the same at every token (bf16 or
+    fp32); S0 [n_seq, H, dk, dv] fp32 or None; cu_seqlens int32 [N + 1] of packed sequences (B = 1).
+    Returns (o [B, T, H, dv] out_dtype, S_T [n_seq, H, dk, dv] fp32 or None). S_T may be passed as S0
+    itself to continue in place."""
+    return (_ops or _marshal()).lin_chunk_fwd(q, k, v, g, S0, cu_seqlens, scale, o, S_T, want_state, out_dtype,
+                                              workspace, stream)
+
+
+def lin_decode_step(q, k, v, g, S, *, scale=1.0, o=None, out_dtype=torch.float32, stream=None):
+    """One token per sequence: q, k [N, Hk, dk]; v [N, H, dv]; g [N, H] or [H]; S [N, H, dk, dv] fp32
+    updated in place. Returns o [N, H, dv]."""
+    return (_ops or _marshal()).lin_decode(q, k, v, g, S, None, scale, o, True, out_dtype, True, stream)
+
+
+def lin_decode_multi(q, k, v, g, S, *, accept=None, scale=1.0, o=None, want_output=True,
+                     out_dtype=torch.float32, stream=None):
+    """m tokens per sequence from one read of S: q, k [N, m, Hk, dk]; v [N, m, H, dv]; g [N, m, H] or
+    [H]. accept None: S unchanged (verification); accept int32 [N]: S[n] <- state after its first
+    accept[n] tokens (commit). Returns o [N, m, H, dv] (None when want_output is False and o is not
+    given)."""
+    return (_ops or _marshal()).lin_decode(q, k, v, g, S, accept, scale, o, want_output, out_dtype, False, stream)
+
+
+# ---- around the layers of a step
+
+def page_plan(block_table, held, lens, new_lens, free_pages, ring, *, page_size, max_tokens, held_out=None,
+              ring_out=None, seq_lens=None, cu_seqlens=None, slots=None, positions=None, stream=None):
+    """Pages for a step's new tokens and everything that its layers take, on the GPU (all int32, slots
+    int64). block_table [N, max_pages] and the ring of free pages free_pages [capacity] are updated in
+    place; held [N]: pages of each sequence; lens [N]: its tokens that stand (`start` of kv_append);
+    new_lens [N]: its tokens of this step, below 0 where it has ended and gives its pages back; ring [2]:
+    head and number of the free pages. Returns (held, ring, both after the call; seq_lens [N];
+    cu_seqlens [N + 1]; slots [max_tokens]; positions [max_tokens]), in new tensors where none are
+    given. A sequence that the pages or max_tokens do not suffice for gets no tokens in this step (see
+    kda_page_plan_args)."""
+    return (_ops or _marshal()).page_plan(block_table, held, lens, new_lens, free_pages, ring, page_size,
+                                          max_tokens, held_out, ring_out, seq_lens, cu_seqlens, slots,
+                                          positions, stream)
+
+
+def adjust_logits(logits, *, history=None, history_lens=None, prompt_lens=None, drafts=None, repetition=None,
+                  frequency=None, presence=None, bias_ids=None, bias=None, bias_counts=None, mask=None,
+                  temperature=None, probs=False, out=None, out_dtype=torch.float32, workspace=None,
+                  stream=None):
+    """Penalties, biases, a grammar's mask and a temperature on logits [N, R, V] (fp32 or bf16, rows
+    contiguous; row j for the token after j drafts); with probs also the softmax, the p or q of
+    verify_drafts. history int32 [N, ids] with history_lens and prompt_lens int32 [N], drafts int32
+    [N, R - 1]: what repetition (history and drafts) and frequency and presence (all but the prompt), fp32
+    [N] each, go by. bias_ids int32, bias fp32 [N, entries], bias_counts int32 [N]. mask int32
+    [N, R, ceil(V / 32)] (a view expanded over rows or sequences will do): bit i % 32 of word i / 32 is 1
+    where token i is allowed. temperature fp32 [N]; 0 stands for the likeliest token. Returns out
+    [N, R, V] (may be logits itself). See kda_logits_args for the order and what NaN and infinities do."""
+    return (_ops or _marshal()).adjust_logits(logits, history, history_lens, prompt_lens, drafts, repetition,
+                                              frequency, presence, bias_ids, bias, bias_counts, mask,
+                                              temperature, probs, out, out_dtype, workspace, stream)

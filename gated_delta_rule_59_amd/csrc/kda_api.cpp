@@ -1,64 +1,23 @@
 // libkda C ABI: argument validation, path selection, workspace sizing and launches.
 // Every check happens on the host before anything is enqueued; see include/kda.h.
-#include "../../include/kda.h"
+#include "kda_api.h"
 
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <string>
-
 #include "kda_internal.h"
 
 namespace {
 
-thread_local std::string g_last_error;
+using namespace kda::api;
 
-kda_status fail(kda_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  std::vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return s;
-}
-
-kda_status ok() {
-  g_last_error.clear();
-  return KDA_OK;
-}
-
-// A launch's grid holds at most 2^32 - 1 work-items. The decode kernels run one
-// 256-work-item workgroup per (sequence, head).
-constexpr int64_t kMaxGridItems = 0xffffffffLL;
-constexpr int64_t kMaxDecodePairs = kMaxGridItems / 256;
 // kda_verify_drafts: a wave per sequence, in workgroups of four in one launch and alone in the other;
 // where the first has more waves than sequences, they are at most 65,536.
 constexpr int64_t kMaxVerifySequences = 4 * kMaxDecodePairs;
-
-bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
-bool dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16; }
-size_t dsize(kda_dtype t) { return t == KDA_F32 ? 4 : 2; }
-
-struct Range {
-  const char* name;
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range(const char* name, const void* p, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{name, a, a + bytes};
-}
-
-bool overlap(const Range& a, const Range& b) {
-  return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
-}
 
 bool env_check() {
   const char* s = std::getenv("KDA_CHECK");
@@ -254,14 +213,6 @@ kda_status chunk_fwd(const kda_chunk_args* a, void* hip_stream, bool noalloc) {
 
 bool cache_dtype_ok(kda_dtype t) { return t == KDA_F32 || t == KDA_BF16 || t == KDA_F8E4M3; }
 size_t cache_dsize(kda_dtype t) { return t == KDA_F32 ? 4 : t == KDA_BF16 ? 2 : 1; }
-constexpr int64_t kMaxStride = int64_t(1) << 40;  // bytes; keeps every address below 2^63
-
-// A stride (elements of `es` bytes) of an array read and written 16 bytes at a time.
-bool stride_ok(int64_t s, size_t es) {
-  return s >= 0 && s <= kMaxStride / (int64_t)es && s * (int64_t)es % 16 == 0;
-}
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 // Shapes, dtypes and strides of a paged cache beside activations of type `act`.
 kda_status validate_cache_shapes(const kda_page_cache& c, kda_dtype act) {
   if (!cache_dtype_ok(c.dtype)) return fail(KDA_ERR_BAD_DTYPE, "unknown cache dtype");
@@ -325,14 +276,6 @@ kda::PageCache page_cache(const kda_page_cache& c) {
 Range table_range(const kda_page_cache& c, int n_seq) {
   return range("block_table", c.block_table,
                sizeof(int32_t) * ((size_t)(n_seq - 1) * c.table_stride + c.max_pages));
-}
-
-// Rows of [tokens, heads, d] by strides (elements): what they span.
-size_t span_bytes(int64_t tokens, int64_t token_stride, int heads, int64_t head_stride, int d, size_t es) {
-  return tokens ? (size_t)((tokens - 1) * token_stride + (heads - 1) * head_stride + d) * es : 0;
-}
-bool span_ok(int64_t tokens, int64_t token_stride, int heads, int64_t head_stride) {
-  return (double)tokens * (double)token_stride + (double)heads * (double)head_stride < 0x1p58;
 }
 
 // Shapes of kda_paged_decode, and its launch.
@@ -713,7 +656,7 @@ const char* kda_status_string(kda_status s) {
   return "KDA_ERR_UNKNOWN";
 }
 
-const char* kda_last_error(void) { return g_last_error.c_str(); }
+const char* kda_last_error(void) { return kda::api::g_last_error.c_str(); }
 
 int kda_abi_version(void) { return KDA_ABI_VERSION; }
 

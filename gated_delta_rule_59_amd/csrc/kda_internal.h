@@ -148,6 +148,66 @@ struct VerifyPlan {
 size_t verify_workspace_bytes(int N, int V);
 hipError_t launch_verify(const VerifyPlan& p, hipStream_t stream);
 
+// Linear attention with a decay for each head: prompts and decode (validated; strides in bytes).
+struct LinPlan {
+  int n_seq, T;                  // dense: T tokens of each sequence; packed: of all
+  int Hk, H, dk, dv;
+  const int32_t* cu_seqlens;     // device, or nullptr for a dense batch
+  bool act_bf16, gate_bf16, out_bf16, fixed;  // fixed: g is [H]
+  const char *q, *k, *v;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  const void* g;
+  float scale;
+  const float* S0;               // nullptr: zeros
+  void* o;                       // nullptr: results not written (decode)
+  float* S_T;                    // may be S0; nullptr: states not written
+  const int32_t* accept;         // decode: S_T is the state after accept[n] tokens; nullptr: after all
+  int seg;                       // prompts: tokens of a segment
+  int jobs;                      // segments there may be at most, of all sequences
+  void* workspace;
+};
+hipError_t launch_lin_recurrent(const LinPlan& p, hipStream_t stream);
+// Chooses seg and jobs, and returns the workspace bytes.
+size_t plan_lin_chunk(LinPlan* p);
+hipError_t launch_lin_chunk(const LinPlan& p, hipStream_t stream);
+
+struct PagePlan {
+  int N, page_size, max_pages, max_tokens, cap;
+  int32_t* table;
+  int64_t table_stride;
+  const int32_t *held, *lens, *new_lens;
+  int32_t* free_pages;
+  const int32_t* ring;
+  int32_t *held_out, *ring_out, *seq_lens, *cu_seqlens;
+  int64_t* slots;
+  int32_t* positions;
+};
+hipError_t launch_page_plan(const PagePlan& p, hipStream_t stream);
+
+struct LogitsPlan {
+  int N, R, V;
+  bool bf16, out_bf16, probs;
+  const void* logits;
+  int64_t seq, row;              // elements
+  void* out;
+  int64_t out_seq, out_row;
+  const int32_t* history;
+  int64_t history_stride;
+  int max_history;
+  const int32_t *history_lens, *prompt_lens, *drafts;
+  const float *repetition, *frequency, *presence;
+  const int32_t* bias_ids;
+  const float* bias;
+  const int32_t* bias_counts;
+  int max_bias;
+  const uint32_t* mask;
+  int64_t mask_seq, mask_row;    // words
+  const float* temperature;
+  void* workspace;
+};
+size_t logits_workspace_bytes(int N, int R, int V);
+hipError_t launch_logits(const LogitsPlan& p, hipStream_t stream);
+
 // Device check of g in [-5, 0] and beta in [0, 1] over n_blocks workgroups (1 .. check_blocks());
 // writes each workgroup's count of violations into counts[0 .. n_blocks).
 int check_blocks();

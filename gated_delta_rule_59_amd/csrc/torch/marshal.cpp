@@ -1,5 +1,5 @@
-// Tensor marshalling of kda_kv_append, kda_paged_decode and kda_verify_drafts for binding.py: checks
-// the tensors, fills the argument structs of include/kda.h, allocates what the caller left out, and
+// Tensor marshalling of the calls beside KDA (kda_kv_append and those declared after it) for binding.py:
+// checks the tensors, fills the argument structs of include/kda.h, allocates what the caller left out, and
 // calls the library on the tensors' device. No computation. It is C++ because these calls can be
 // shorter than their own marshalling: a decode step's append runs 5 us on the GPU, and the same
 // checks written in Python took 17 us of the host.
@@ -21,6 +21,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <optional>
+#include <type_traits>
 
 #include "kda.h"
 
@@ -32,6 +33,13 @@ struct Library {
   decltype(&kda_paged_decode_workspace_bytes) decode_bytes;
   decltype(&kda_verify_drafts) verify;
   decltype(&kda_verify_drafts_workspace_bytes) verify_bytes;
+  decltype(&kda_lin_chunk_fwd) lin_chunk;
+  decltype(&kda_lin_chunk_fwd_workspace_bytes) lin_chunk_bytes;
+  decltype(&kda_lin_decode_step) lin_step;
+  decltype(&kda_lin_decode_multi) lin_multi;
+  decltype(&kda_page_plan) plan;
+  decltype(&kda_adjust_logits) logits;
+  decltype(&kda_adjust_logits_workspace_bytes) logits_bytes;
   decltype(&kda_last_error) last_error;
   PyObject* error;  // binding.KDAError
 } lib{};
@@ -101,6 +109,13 @@ kda_dtype act_type(const at::Tensor& t, const char* name) {
   if (t.scalar_type() == at::kFloat) return KDA_F32;
   if (t.scalar_type() == at::kBFloat16) return KDA_BF16;
   type_error("%s must be float32 or bfloat16", name);
+}
+
+at::ScalarType out_type(Opt given, PyObject* dtype) {
+  if (!given && !THPDtype_Check(dtype)) type_error("out_dtype must be a torch.dtype");
+  const at::ScalarType t = given ? given->scalar_type() : reinterpret_cast<THPDtype*>(dtype)->scalar_type;
+  if (t != at::kFloat && t != at::kBFloat16) type_error("the output must be float32 or bfloat16");
+  return t;
 }
 
 // Token and head strides of a [lead0, lead1, heads, d] view whose tokens lie evenly apart.
@@ -244,18 +259,21 @@ int number(PyObject* o, const char* name) {
 // bind(addresses of the library's functions ..., KDAError)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 7);
-  void* p[6];
-  for (int i = 0; i < 6; ++i) {
+  constexpr int F = 13;  // functions of Library
+  arguments(n, F + 1);
+  void* p[F];
+  for (int i = 0; i < F; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (!p[i] && PyErr_Occurred()) throw python_error();
   }
-  Py_INCREF(args[6]);
+  Py_INCREF(args[F]);
   Py_XDECREF(lib.error);
-  lib = Library{reinterpret_cast<decltype(lib.append)>(p[0]), reinterpret_cast<decltype(lib.decode)>(p[1]),
-                reinterpret_cast<decltype(lib.decode_bytes)>(p[2]), reinterpret_cast<decltype(lib.verify)>(p[3]),
-                reinterpret_cast<decltype(lib.verify_bytes)>(p[4]),
-                reinterpret_cast<decltype(lib.last_error)>(p[5]), args[6]};
+  int i = 0;
+  const auto next = [&](auto& f) { f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(p[i++]); };
+  next(lib.append), next(lib.decode), next(lib.decode_bytes), next(lib.verify), next(lib.verify_bytes);
+  next(lib.lin_chunk), next(lib.lin_chunk_bytes), next(lib.lin_step), next(lib.lin_multi);
+  next(lib.plan), next(lib.logits), next(lib.logits_bytes), next(lib.last_error);
+  lib.error = args[F];
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -333,10 +351,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     value_error("q must be of shape [N, m, Hq, d], k_cache and v_cache of shape "
                             "[pages, page_size, Hkv, d]");
   const int64_t N = q.size(0), m = q.size(1), Hq = q.size(2), d = q.size(3), Hkv = k_cache.size(2);
-  if (!o && !THPDtype_Check(args[12])) type_error("out_dtype must be a torch.dtype");
-  const at::ScalarType out = o ? o->scalar_type() : reinterpret_cast<THPDtype*>(args[12])->scalar_type;
-  if (out != at::kFloat && out != at::kBFloat16)
-    type_error("the output must be float32 or bfloat16");
+  const at::ScalarType out = out_type(o, args[12]);
   kda_paged_decode_args a{};
   a.N = to_int("N", N), a.m = to_int("m", m), a.Hq = to_int("Hq", Hq), a.Hkv = to_int("Hkv", Hkv);
   a.d = to_int("d", d);
@@ -369,6 +384,172 @@ PyObject* paged_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   const c10::DeviceGuard guard(on.device);
   check(lib.decode(&a, stream.raw));
   return o ? Py_NewRef(args[10]) : THPVariable_Wrap(own);
+  END_HANDLE_TH_ERRORS
+}
+
+// Heads, dims, types, strides and decays of linear attention: q, k [lead0, lead1, Hk, dk], v [lead0, lead1,
+// H, dv], g [lead0, lead1, H] or [H].
+template <typename Args>
+void linear(const On& on, const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, const at::Tensor& g,
+            PyObject* scale, Args* a) {
+  const int64_t lead0 = q.size(0), lead1 = q.size(1), dk = q.size(3), H = v.size(2), dv = v.size(3);
+  a->act_dtype = act_type(q, "q");
+  heads(on, "q", q, q.scalar_type(), lead0, lead1, dk, &a->q_token_stride, &a->q_head_stride);
+  heads(on, "k", k, q.scalar_type(), lead0, lead1, dk, &a->k_token_stride, &a->k_head_stride);
+  heads(on, "v", v, q.scalar_type(), lead0, lead1, dv, &a->v_token_stride, &a->v_head_stride);
+  if (k.size(2) != q.size(2)) value_error("q and k must have the same heads");
+  a->gate_dtype = act_type(g, "g");
+  const bool fixed = g.dim() == 1;
+  const int64_t shape[] = {lead0, lead1, H};
+  plain(on, "g", &g, g.scalar_type(), at::IntArrayRef(shape + (fixed ? 2 : 0), shape + 3));
+  a->Hk = to_int("Hk", q.size(2)), a->H = to_int("H", H);
+  a->dk = to_int("dk", dk), a->dv = to_int("dv", dv);
+  a->q = q.data_ptr(), a->k = k.data_ptr(), a->v = v.data_ptr(), a->g = g.data_ptr();
+  a->scale = (float)PyFloat_AsDouble(scale);
+  if (PyErr_Occurred()) throw python_error();
+  a->flags = fixed ? KDA_LIN_FIXED_DECAY : 0;
+}
+
+// lin_chunk_fwd(q, k, v, g, S0, cu_seqlens, scale, o, S_T, want_state, out_dtype, workspace, stream)
+//   -> (o, S_T or None); with workspace False: the workspace's bytes
+PyObject* lin_chunk_fwd(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  arguments(nargs, 13);
+  const at::Tensor &q = tensor(args[0], "q"), &k = tensor(args[1], "k"), &v = tensor(args[2], "v"),
+                   &g = tensor(args[3], "g");
+  Opt S0 = optional(args[4], "S0"), cu = optional(args[5], "cu_seqlens"), o = optional(args[7], "o"),
+      S_T = optional(args[8], "S_T");
+  const bool query = args[11] == Py_False, want = S_T || truth(args[9]);
+  Opt given = query ? nullptr : optional(args[11], "workspace");
+  const On on(q);
+  if (q.dim() != 4 || v.dim() != 4)
+    value_error("q and k must be of shape [B, T, Hk, dk], v of shape [B, T, H, dv]");
+  const at::ScalarType out = out_type(o, args[10]);
+  kda_lin_chunk_args a{};
+  linear(on, q, k, v, g, args[6], &a);
+  const int64_t n_seq = cu ? cu->numel() - 1 : q.size(0);
+  const int64_t state[] = {n_seq, v.size(2), q.size(3), v.size(3)};
+  plain(on, "cu_seqlens", cu, at::kInt, {n_seq + 1});
+  plain(on, "S0", S0, at::kFloat, state);
+  plain(on, "S_T", S_T, at::kFloat, state);
+  plain(on, "o", o, out, v.sizes());
+  a.B = to_int("B", q.size(0)), a.T = to_int("T", q.size(1));
+  a.cu_seqlens = ints(cu);
+  a.N = cu ? to_int("N", n_seq) : 0;
+  a.out_dtype = out == at::kFloat ? KDA_F32 : KDA_BF16;
+  if (query) {
+    const size_t bytes = lib.lin_chunk_bytes(&a);
+    if (bytes == SIZE_MAX) check(KDA_ERR_BAD_SHAPE);
+    return PyLong_FromSize_t(bytes);
+  }
+  const Stream stream(args[12], on);
+  at::Tensor own_o, own_state, scratch;
+  if (!o) own_o = stream.empty(v.sizes(), out, on);
+  if (!S_T && want) own_state = stream.empty(state, at::kFloat, on);
+  a.S0 = S0 ? static_cast<const float*>(S0->data_ptr()) : nullptr;
+  a.o = o ? o->data_ptr() : own_o.data_ptr();
+  a.S_T = S_T ? static_cast<float*>(S_T->data_ptr()) : want ? static_cast<float*>(own_state.data_ptr()) : nullptr;
+  workspace(&a, given, lib.lin_chunk_bytes, stream, on, &scratch);
+  const c10::DeviceGuard guard(on.device);
+  check(lib.lin_chunk(&a, stream.raw));
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, o ? Py_NewRef(args[7]) : THPVariable_Wrap(own_o));
+  PyTuple_SET_ITEM(r, 1, S_T ? Py_NewRef(args[8]) : want ? THPVariable_Wrap(own_state) : Py_NewRef(Py_None));
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// lin_decode(q, k, v, g, S, accept, scale, o, want_output, out_dtype, step, stream) -> o or None
+PyObject* lin_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  arguments(nargs, 12);
+  const at::Tensor &q = tensor(args[0], "q"), &k = tensor(args[1], "k"), &v = tensor(args[2], "v"),
+                   &g = tensor(args[3], "g"), &S = tensor(args[4], "S");
+  Opt accept = optional(args[5], "accept"), o = optional(args[7], "o");
+  const bool want = o || truth(args[8]), step = truth(args[10]);
+  const On on(q);
+  const int64_t dim = step ? 3 : 4;
+  if (q.dim() != dim || k.dim() != dim || v.dim() != dim || (g.dim() != 1 && g.dim() != dim - 1)) {
+    if (step)
+      value_error("q and k must be of shape [N, Hk, dk], v of shape [N, H, dv], g of shape [N, H] or [H]");
+    value_error("q and k must be of shape [N, m, Hk, dk], v of shape [N, m, H, dv], g of shape [N, m, H] or [H]");
+  }
+  const at::ScalarType out = out_type(o, args[9]);
+  kda_lin_decode_args a{};
+  if (step)
+    linear(on, q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.dim() == 1 ? g : g.unsqueeze(1), args[6], &a);
+  else
+    linear(on, q, k, v, g, args[6], &a);
+  const int64_t N = q.size(0);
+  plain(on, "S", &S, at::kFloat, {N, a.H, a.dk, a.dv});
+  plain(on, "accept", accept, at::kInt, {N});
+  plain(on, "o", o, out, v.sizes());
+  a.N = to_int("N", N), a.m = step ? 1 : to_int("m", q.size(1));
+  a.out_dtype = out == at::kFloat ? KDA_F32 : KDA_BF16;
+  const Stream stream(args[11], on);
+  at::Tensor own;
+  if (!o && want) own = stream.empty(v.sizes(), out, on);
+  a.S = static_cast<float*>(S.data_ptr());
+  a.o = o ? o->data_ptr() : want ? own.data_ptr() : nullptr;
+  a.accept = ints(accept);
+  const c10::DeviceGuard guard(on.device);
+  check((step ? lib.lin_step : lib.lin_multi)(&a, stream.raw));
+  return o ? Py_NewRef(args[7]) : want ? THPVariable_Wrap(own) : Py_NewRef(Py_None);
+  END_HANDLE_TH_ERRORS
+}
+
+// page_plan(block_table, held, lens, new_lens, free_pages, ring, page_size, max_tokens, held_out, ring_out,
+//           seq_lens, cu_seqlens, slots, positions, stream)
+//   -> (held, ring, seq_lens, cu_seqlens, slots, positions)
+PyObject* page_plan(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  arguments(nargs, 15);
+  const at::Tensor &table = tensor(args[0], "block_table"), &held = tensor(args[1], "held"),
+                   &lens = tensor(args[2], "lens"), &fresh = tensor(args[3], "new_lens"),
+                   &pages = tensor(args[4], "free_pages"), &ring = tensor(args[5], "ring");
+  const On on(table);
+  of_type("block_table", table, at::kInt);
+  if (table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1))
+    value_error("block_table must be of shape [N, max_pages], pages side by side");
+  const int64_t N = table.size(0);
+  plain(on, "held", &held, at::kInt, {N});
+  plain(on, "lens", &lens, at::kInt, {N});
+  plain(on, "new_lens", &fresh, at::kInt, {N});
+  plain(on, "free_pages", &pages, at::kInt, {pages.numel()});
+  plain(on, "ring", &ring, at::kInt, {2});
+  kda_page_plan_args a{};
+  a.N = to_int("N", N);
+  a.page_size = number(args[6], "page_size");
+  a.max_tokens = number(args[7], "max_tokens");
+  a.max_pages = to_int("block_table", table.size(1));
+  a.free_capacity = to_int("free_pages", pages.numel());
+  const Stream stream(args[14], on);
+  static const char* const names[] = {"held_out", "ring_out", "seq_lens", "cu_seqlens", "slots", "positions"};
+  const int64_t sizes[] = {N, 2, N, N + 1, a.max_tokens, a.max_tokens};
+  at::Tensor own[6];
+  void* to[6];
+  for (int i = 0; i < 6; ++i) {
+    Opt x = optional(args[8 + i], names[i]);
+    const at::ScalarType type = i == 4 ? at::kLong : at::kInt;
+    plain(on, names[i], x, type, {sizes[i]});
+    if (!x) own[i] = stream.empty({std::max<int64_t>(sizes[i], 0)}, type, on);
+    to[i] = x ? x->data_ptr() : own[i].data_ptr();
+  }
+  a.block_table = out_ints(table);
+  a.table_stride = N > 1 ? table.stride(0) : std::max<int64_t>(table.size(1), 1);
+  a.held = ints(&held), a.lens = ints(&lens), a.new_lens = ints(&fresh);
+  a.free_pages = out_ints(pages), a.ring = ints(&ring);
+  a.held_out = static_cast<int32_t*>(to[0]), a.ring_out = static_cast<int32_t*>(to[1]);
+  a.seq_lens = static_cast<int32_t*>(to[2]), a.cu_seqlens = static_cast<int32_t*>(to[3]);
+  a.slots = static_cast<int64_t*>(to[4]), a.positions = static_cast<int32_t*>(to[5]);
+  const c10::DeviceGuard guard(on.device);
+  check(lib.plan(&a, stream.raw));
+  PyObject* r = PyTuple_New(6);
+  if (!r) return nullptr;
+  for (int i = 0; i < 6; ++i)
+    PyTuple_SET_ITEM(r, i, own[i].defined() ? THPVariable_Wrap(own[i]) : Py_NewRef(args[8 + i]));
+  return r;
   END_HANDLE_TH_ERRORS
 }
 
@@ -430,11 +611,91 @@ PyObject* verify_drafts(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// adjust_logits(logits, history, history_lens, prompt_lens, drafts, repetition, frequency, presence, bias_ids,
+//               bias, bias_counts, mask, temperature, probs, out, out_dtype, workspace, stream) -> out
+PyObject* adjust_logits(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  arguments(nargs, 18);
+  const at::Tensor& logits = tensor(args[0], "logits");
+  Opt history = optional(args[1], "history"), history_lens = optional(args[2], "history_lens"),
+      prompt_lens = optional(args[3], "prompt_lens"), drafts = optional(args[4], "drafts"),
+      repetition = optional(args[5], "repetition"), frequency = optional(args[6], "frequency"),
+      presence = optional(args[7], "presence"), bias_ids = optional(args[8], "bias_ids"),
+      bias = optional(args[9], "bias"), bias_counts = optional(args[10], "bias_counts"),
+      mask = optional(args[11], "mask"), temperature = optional(args[12], "temperature"),
+      o = optional(args[14], "out"), given = optional(args[16], "workspace");
+  const On on(logits);
+  if (logits.dim() != 3) value_error("logits must be of shape [N, R, V]");
+  const int64_t N = logits.size(0), R = logits.size(1), V = logits.size(2);
+  kda_logits_args a{};
+  a.N = to_int("N", N), a.R = to_int("R", R), a.V = to_int("V", V);
+  a.dtype = act_type(logits, "logits");
+  rows(on, "logits", logits, logits.scalar_type(), N, R, V, &a.seq_stride, &a.row_stride);
+  const at::ScalarType out = out_type(o, args[15]);
+  a.out_dtype = out == at::kFloat ? KDA_F32 : KDA_BF16;
+  if ((history != nullptr) != (history_lens != nullptr)) value_error("history and history_lens go together");
+  if (prompt_lens && !history) value_error("prompt_lens needs history");
+  if (history) {
+    on.also("history", history);
+    of_type("history", *history, at::kInt);
+    if (history->dim() != 2 || history->size(0) != N || (history->size(1) > 1 && history->stride(1) != 1))
+      value_error("history must be of shape [%lld, ids], ids side by side", (long long)N);
+    a.max_history = to_int("history", history->size(1));
+    a.history_stride = N > 1 ? history->stride(0) : a.max_history;
+    if (a.max_history > 0) {  // a history of no columns is none
+      a.history = ints(history);
+      a.history_lens = ints(history_lens);
+      a.prompt_lens = ints(prompt_lens);
+    }
+  }
+  plain(on, "history_lens", history_lens, at::kInt, {N});
+  plain(on, "prompt_lens", prompt_lens, at::kInt, {N});
+  plain(on, "drafts", drafts, at::kInt, {N, R - 1});
+  plain(on, "repetition", repetition, at::kFloat, {N});
+  plain(on, "frequency", frequency, at::kFloat, {N});
+  plain(on, "presence", presence, at::kFloat, {N});
+  plain(on, "temperature", temperature, at::kFloat, {N});
+  if ((bias != nullptr) != (bias_ids != nullptr)) value_error("bias and bias_ids go together");
+  if (bias_counts && !bias) value_error("bias_counts needs bias and bias_ids");
+  if (bias) {
+    if (bias->dim() != 2) value_error("bias must be of shape [%lld, entries]", (long long)N);
+    plain(on, "bias", bias, at::kFloat, {N, bias->size(1)});
+    plain(on, "bias_ids", bias_ids, at::kInt, {N, bias->size(1)});
+    plain(on, "bias_counts", bias_counts, at::kInt, {N});
+    a.max_bias = to_int("bias", bias->size(1));
+    if (a.max_bias > 0) {
+      a.bias_ids = ints(bias_ids);
+      a.bias = static_cast<const float*>(bias->data_ptr());
+      a.bias_counts = ints(bias_counts);
+    }
+  }
+  if (mask) {
+    rows(on, "mask", *mask, at::kInt, N, R, (V + 31) / 32, &a.mask_seq_stride, &a.mask_row_stride);
+    a.mask = reinterpret_cast<const uint32_t*>(ints(mask));
+  }
+  const auto floats = [](Opt x) { return x ? static_cast<const float*>(x->data_ptr()) : nullptr; };
+  a.drafts = drafts && R > 1 ? ints(drafts) : nullptr;
+  a.repetition = floats(repetition), a.frequency = floats(frequency), a.presence = floats(presence);
+  a.temperature = floats(temperature);
+  a.flags = truth(args[13]) ? KDA_LOGITS_PROBS : 0;
+  const Stream stream(args[17], on);
+  at::Tensor own, scratch;
+  if (!o) own = stream.empty(logits.sizes(), out, on);
+  const at::Tensor& to = o ? *o : own;
+  rows(on, "out", to, out, N, R, V, &a.out_seq_stride, &a.out_row_stride);
+  a.logits = logits.data_ptr();
+  a.out = to.data_ptr();
+  workspace(&a, given, lib.logits_bytes, stream, on, &scratch);
+  const c10::DeviceGuard guard(on.device);
+  check(lib.logits(&a, stream.raw));
+  return o ? Py_NewRef(args[14]) : THPVariable_Wrap(own);
+  END_HANDLE_TH_ERRORS
+}
+
+#define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
-    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
-    {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(kv_append)), METH_FASTCALL, nullptr},
-    {"paged_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_decode)), METH_FASTCALL, nullptr},
-    {"verify_drafts", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(verify_drafts)), METH_FASTCALL, nullptr},
+    METHOD(bind), METHOD(kv_append), METHOD(paged_decode), METHOD(verify_drafts), METHOD(lin_chunk_fwd),
+    METHOD(lin_decode), METHOD(page_plan), METHOD(adjust_logits),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -435,6 +435,224 @@ kda_status kda_paged_decode(const kda_paged_decode_args* args, void* hip_stream)
 size_t kda_verify_drafts_workspace_bytes(const kda_verify_args* args);
 kda_status kda_verify_drafts(const kda_verify_args* args, void* hip_stream);
 
+/* ---- Around the layers of a step -------------------------------------------------------
+ *
+ * What the step of a hybrid stack needs beside the calls above: its layers whose state decays by
+ * one number per head (kda_lin_*), the block tables and slots that its paged cache works by
+ * (kda_page_plan), and the way from logits to the probabilities that kda_verify_drafts takes
+ * (kda_adjust_logits). As above, values on the device cannot be checked on the host: nothing is
+ * read or written out of bounds whatever lengths, counts, page ids and token ids hold.
+ */
+
+/* Linear attention with a decay for each head. Per (sequence, head) the state S is a dk x dv fp32
+ * matrix, rows indexed by key channel, and each token t does
+ *
+ *     S <- exp(g_t) S + k_t v_t^T;   o_t = scale * S^T q_t
+ *
+ *   Hk, H      heads of q and k, and of v, g, S and o: H is a multiple of Hk, and head h reads
+ *              query and key head h / (H / Hk).
+ *   dk, dv     each in {32, 64, 128}.
+ *   act_dtype  of q, k, v: KDA_F32 or KDA_BF16. gate_dtype of g, out_dtype of o: either. With
+ *              KDA_BF16 activations products that need more than bf16 holds (states, weights, and
+ *              values times decays) go in several bf16 parts, so o is off by its own rounding and
+ *              2^-16 of its largest terms, S by 2^-22.
+ *   q, k, v    [B, T, heads, d] (decode: [N, m, heads, d]): token t = b * T + j of head h begins at
+ *              t * token_stride + h * head_stride (elements), so views of a fused projection can be
+ *              passed. Pointers and strides are multiples of 16 bytes.
+ *   g          natural logarithm of each token's decay, contiguous [B, T, H] (decode [N, m, H]); with
+ *              KDA_LIN_FIXED_DECAY [H], the same for every token. -infinity is a decay of 0, which
+ *              ends the memory of all earlier tokens. Values above 0 (growth) are taken as they are.
+ *   scale      finite.
+ *   flags      0 or KDA_LIN_FIXED_DECAY.
+ *
+ * A value of q, k, v or g that is not finite reaches results of its own sequence and the heads that
+ * read it only; in kda_lin_chunk_fwd, tokens up to 63 places before it too, in the decode calls
+ * only its own token and later ones.
+ */
+#define KDA_LIN_FIXED_DECAY 1u
+
+/* Arguments of kda_lin_chunk_fwd: whole prompts, chunkwise parallel.
+ *   B, T, cu_seqlens, N
+ *              dense batch or packed sequences, as in kda_chunk_args (T = 0 is allowed: S_T receives
+ *              S0, zeros if NULL). Rows of o at or past cu_seqlens[N] are left as they were. Offsets
+ *              outside [0, T] are taken as the nearer bound, and a sequence that ends before it begins
+ *              has no tokens; results of tokens that offsets give to two sequences are unspecified.
+ *   S0         [n_seq, H, dk, dv] fp32 initial states, or NULL for zeros.
+ *   o          [B, T, H, dv] contiguous, out_dtype, 16-byte aligned. Overlaps no input.
+ *   S_T        [n_seq, H, dk, dv] fp32 final states, or NULL. May be S0 itself (continue in place);
+ *              does not overlap it in part. S0 and S_T are 16-byte aligned.
+ *   workspace  device scratch of at least kda_lin_chunk_fwd_workspace_bytes() bytes, 256-byte
+ *              aligned; contents on entry are ignored. (NULL when that is 0.) Calls that overlap in
+ *              time need one each.
+ */
+typedef struct {
+    int B, T, Hk, H, dk, dv;
+    const int32_t* cu_seqlens;
+    int N;
+    kda_dtype act_dtype, gate_dtype, out_dtype;
+    const void *q, *k, *v;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    const void* g;
+    float scale;
+    const float* S0;
+    void* o;
+    float* S_T;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned flags;
+} kda_lin_chunk_args;
+
+/* Arguments of kda_lin_decode_step (m = 1, accept NULL: S is updated in place) and of
+ * kda_lin_decode_multi (m >= 1 tokens of each of N sequences, S as in kda_decode_multi: unchanged
+ * with accept NULL, else the state after the first clamp(accept[n], 0, m) tokens).
+ *   S          [N, H, dk, dv] fp32, 16-byte aligned.
+ *   o          [N, m, H, dv] contiguous, out_dtype, 16-byte aligned; kda_lin_decode_multi: or NULL.
+ *              o of a call with accept and of one without agree bitwise.
+ *   q, k, v, g and accept overlap neither S nor o, nor do these two each other.
+ */
+typedef struct {
+    int N, m, Hk, H, dk, dv;
+    kda_dtype act_dtype, gate_dtype, out_dtype;
+    const void *q, *k, *v;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    const void* g;
+    float scale;
+    float* S;
+    void* o;
+    const int32_t* accept;
+    unsigned flags;
+} kda_lin_decode_args;
+
+/* Arguments of kda_page_plan: pages for the new tokens of N sequences out of a ring of free ones, the
+ * pages of ended sequences back into it, and everything that the layers of a step take: offsets,
+ * lengths, positions and slots. Sequences are served in order. With pages_n = ceil((lens[n] +
+ * new_lens[n]) / page_size):
+ *   - a sequence with new_lens[n] < 0 has ended: its held[n] pages go back, and it holds none.
+ *   - otherwise it asks for need_n = max(0, pages_n - held[n]) pages, unless pages_n > max_pages: then
+ *     it is refused. It is refused too if it asks for pages and they and those that sequences before
+ *     it asked for (refused for lack of pages or tokens or not) are more than the ring holds, or if it
+ *     has new tokens and they and those before are more than max_tokens. A refused sequence keeps its
+ *     pages and length, and has no new tokens in this step.
+ * Pages that come back are free for the next call, not for this one.
+ *
+ *   N, page_size, max_pages, max_tokens    >= 1
+ *   block_table  int32, page p of sequence n at n * table_stride + p; updated in place: the new pages
+ *                of a served sequence are entries held[n] .. held[n] + need_n - 1. Other entries
+ *                stay. table_stride >= max_pages.
+ *   held         int32 [N]: entries of block_table that are the sequence's (also those that no token
+ *                is in yet, or no more, as after drafts that fell). Taken as within [0, max_pages].
+ *   lens         int32 [N]: tokens in the cache that stand (below 0: as 0): `start` of kda_kv_append.
+ *   new_lens     int32 [N]: tokens of this step.
+ *   free_pages   int32 [free_capacity], a ring: its free pages are entries (head + i) mod
+ *                free_capacity, i < count. Pages are taken from its head; pages that come back are
+ *                written behind its end, in place, by sequence and entry (those that find no
+ *                room are lost: free_capacity >= all pages there are).
+ *   ring         int32 [2]: head (taken mod free_capacity, below 0: as 0), count (taken as within
+ *                [0, free_capacity]).
+ *   held_out, ring_out
+ *                held and ring after the call. Not held and ring themselves: every workgroup reads
+ *                those.
+ *   seq_lens     int32 [N]: tokens in the cache with this step's: `seq_lens` of kda_paged_decode. 0 if
+ *                the sequence has ended.
+ *   cu_seqlens   int32 [N + 1]: offsets of the sequences' new tokens, `cu_seqlens` of the calls above.
+ *   slots        int64 [max_tokens], or NULL: where new token t goes, page * page_size + position %
+ *                page_size; -1 at and past cu_seqlens[N], and where the table has a page below 0.
+ *   positions    int32 [max_tokens], or NULL: its position; -1 at and past cu_seqlens[N].
+ */
+typedef struct {
+    int N, page_size, max_pages, max_tokens, free_capacity;
+    int32_t* block_table;
+    int64_t table_stride;
+    const int32_t *held, *lens, *new_lens;
+    int32_t* free_pages;
+    const int32_t* ring;
+    int32_t *held_out, *ring_out, *seq_lens, *cu_seqlens;
+    int64_t* slots;
+    int32_t* positions;
+} kda_page_plan_args;
+
+/* Arguments of kda_adjust_logits: R rows of logits of each of N sequences, row j for the token after
+ * j drafts (R = 1: plain decode; R = m + 1 beside kda_verify_drafts). For each row, in 32 bits and in
+ * this order, x being the logit of token i:
+ *   - if i is in the sequence's history or among its first j drafts: x = x / repetition[n] where x > 0,
+ *     x * repetition[n] elsewhere.
+ *   - if it is c > 0 times in the history past the prompt and among the first j drafts: x = x -
+ *     (frequency[n] * c + presence[n]).
+ *   - x = x + bias; of a token that is listed twice the last entry counts.
+ *   - where the mask's bit i is 0, x = -infinity (whatever x was, NaN too).
+ *   - x = x / temperature[n]. Temperatures that are not above 0 stand for the limit: x stays, and with
+ *     KDA_LOGITS_PROBS the row is 1 at its largest x (the first of equal ones; NaN is never it) and
+ *     0 elsewhere.
+ *   - with KDA_LOGITS_PROBS softmax over the row: 0 everywhere if every x is -infinity; infinite ones
+ *     share the row evenly; a NaN makes the row NaN.
+ *
+ *   N, R, V    >= 1, V at most 2^30.
+ *   dtype      of logits, out_dtype of out: KDA_F32 or KDA_BF16.
+ *   logits     row (n, j) begins at n * seq_stride + j * row_stride (elements), as the row of out does
+ *              by its strides. out may be logits itself where types and strides are the same; otherwise
+ *              they do not overlap. Rows of out do not overlap each other.
+ *   history    int32: id t of sequence n at n * history_stride + t, t < history_lens[n] (device int32
+ *              [N], taken as within [0, max_history]); the first prompt_lens[n] (device int32 [N] or
+ *              NULL: 0) are its prompt. NULL: none. Ids outside [0, V) are no token's.
+ *   drafts     int32 [N, R - 1], or NULL: none count.
+ *   repetition, frequency, presence
+ *              fp32 [N] each, or NULL for 1, 0, 0.
+ *   bias_ids, bias
+ *              int32 and fp32 [N, max_bias], of which the first bias_counts[n] (device int32 [N] or
+ *              NULL: all; taken as within [0, max_bias]) count. NULL: none.
+ *   mask       32-bit words: bit i % 32 of word i / 32 is token i's, the words of row (n, j) begin at
+ *              n * mask_seq_stride + j * mask_row_stride (words; 0 to share them). NULL: all allowed.
+ *   temperature  fp32 [N], or NULL for 1.
+ *   workspace  device scratch of at least kda_adjust_logits_workspace_bytes() bytes (0 without
+ *              KDA_LOGITS_PROBS), 256-byte aligned; contents on entry are ignored. Calls that overlap
+ *              in time need one each.
+ *   flags      0 or KDA_LOGITS_PROBS.
+ */
+#define KDA_LOGITS_PROBS 1u
+typedef struct {
+    int N, R, V;
+    kda_dtype dtype, out_dtype;
+    const void* logits;
+    int64_t seq_stride, row_stride;
+    void* out;
+    int64_t out_seq_stride, out_row_stride;
+    const int32_t* history;
+    int64_t history_stride;
+    int max_history;
+    const int32_t *history_lens, *prompt_lens;
+    const int32_t* drafts;
+    const float *repetition, *frequency, *presence;
+    const int32_t* bias_ids;
+    const float* bias;
+    const int32_t* bias_counts;
+    int max_bias;
+    const uint32_t* mask;
+    int64_t mask_seq_stride, mask_row_stride;
+    const float* temperature;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned flags;
+} kda_logits_args;
+
+/* Linear attention with a decay for each head: prompts (the workspace query looks at shapes and
+ * dtypes, not at pointers, but for whether cu_seqlens is NULL; SIZE_MAX when they are invalid), one
+ * token, and m tokens with the commit of an accepted prefix. */
+size_t kda_lin_chunk_fwd_workspace_bytes(const kda_lin_chunk_args* args);
+kda_status kda_lin_chunk_fwd(const kda_lin_chunk_args* args, void* hip_stream);
+kda_status kda_lin_decode_step(const kda_lin_decode_args* args, void* hip_stream);
+kda_status kda_lin_decode_multi(const kda_lin_decode_args* args, void* hip_stream);
+
+/* Block tables, lengths, positions and slots of a step (see kda_page_plan_args). */
+kda_status kda_page_plan(const kda_page_plan_args* args, void* hip_stream);
+
+/* Penalties, biases, grammar masks and temperatures on logits, and their softmax (see
+ * kda_logits_args). The workspace query looks at N, R, V, dtypes and flags only; SIZE_MAX when they
+ * are invalid. */
+size_t kda_adjust_logits_workspace_bytes(const kda_logits_args* args);
+kda_status kda_adjust_logits(const kda_logits_args* args, void* hip_stream);
+
 const char* kda_status_string(kda_status s);
 const char* kda_last_error(void);   /* detail of the last failure on this thread */
 int kda_abi_version(void);           /* KDA_ABI_VERSION of the built library */

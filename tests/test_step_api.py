@@ -1,0 +1,239 @@
+"""Host-side behaviour of the calls around a step's layers (linear attention with a decay per head, page
+plans, adjusted logits), without a GPU: every call here is refused before any launch, and no pointer
+is dereferenced. Then the plain 64-bit forms against worked examples."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+from tests import step_ref
+
+FAKE = 1 << 40
+NULL_PTR, BAD_SHAPE, BAD_DTYPE, UNSUPPORTED, WORKSPACE, ALIAS = 1, 2, 3, 4, 6, 8
+
+
+@pytest.fixture(scope="module")
+def b():
+    from gated_delta_rule_59_amd import binding
+    if not os.path.exists(binding.LIB_PATH):
+        pytest.skip("libkda not built")
+    binding.lib()
+    return binding
+
+
+def at(i):
+    return FAKE + (i << 36)
+
+
+def call(b, name, a):
+    rc = getattr(b.lib(), "kda_" + name)(ctypes.byref(a), None)
+    return rc, b.lib().kda_last_error().decode()
+
+
+def put(a, **kw):
+    for k, v in kw.items():
+        assert hasattr(a, k), k
+        setattr(a, k, v)
+    return a
+
+
+def strides(a):
+    a.q_token_stride = a.k_token_stride = a.Hk * a.dk
+    a.v_token_stride = a.H * a.dv
+    a.q_head_stride = a.k_head_stride = a.dk
+    a.v_head_stride = a.dv
+    return a
+
+
+def chunk_args(b, **kw):
+    a = b.LinChunkArgs()
+    a.B, a.T, a.Hk, a.H, a.dk, a.dv = 2, 300, 2, 4, 128, 64
+    a.act_dtype, a.gate_dtype, a.out_dtype, a.scale = 1, 0, 1, 0.1
+    a.q, a.k, a.v, a.g, a.S0, a.o, a.S_T, a.workspace = (at(i) for i in range(8))
+    a.workspace_bytes = 1 << 34
+    return put(strides(a), **kw)
+
+
+LIN = [
+    (dict(Hk=0), BAD_SHAPE), (dict(H=5), BAD_SHAPE), (dict(H=0), BAD_SHAPE), (dict(dk=96), BAD_SHAPE),
+    (dict(dv=256), BAD_SHAPE), (dict(act_dtype=2), BAD_DTYPE), (dict(gate_dtype=3), BAD_DTYPE),
+    (dict(out_dtype=2), BAD_DTYPE), (dict(flags=2), UNSUPPORTED), (dict(q=None), NULL_PTR),
+    (dict(k=None), NULL_PTR), (dict(v=None), NULL_PTR), (dict(g=None), NULL_PTR),
+    (dict(q_token_stride=-128), BAD_SHAPE), (dict(k_head_stride=12), BAD_SHAPE),
+    (dict(v_token_stride=1 << 41), BAD_SHAPE), (dict(q=at(0) + 8), BAD_SHAPE), (dict(o=at(5) + 4), BAD_SHAPE),
+    (dict(scale=float("nan")), BAD_SHAPE), (dict(scale=float("-inf")), BAD_SHAPE), (dict(o=at(0)), ALIAS),
+    (dict(o=at(2) + 128), ALIAS), (dict(o=at(3)), ALIAS),
+]
+
+
+@pytest.mark.parametrize("change,status", LIN + [
+    (dict(B=0), BAD_SHAPE), (dict(T=-1), BAD_SHAPE), (dict(o=None), NULL_PTR),
+    (dict(cu_seqlens=at(9), N=3), BAD_SHAPE), (dict(B=1, cu_seqlens=at(9), N=0), BAD_SHAPE),
+    (dict(B=1 << 15, T=1 << 20), BAD_SHAPE), (dict(S0=at(4) + 4), BAD_SHAPE), (dict(S_T=at(6) + 8), BAD_SHAPE),
+    (dict(o=at(4)), ALIAS), (dict(S_T=at(4) + 64), ALIAS), (dict(S_T=at(1)), ALIAS), (dict(S_T=at(5)), ALIAS),
+    (dict(B=1, cu_seqlens=at(5), N=1), ALIAS)])
+def test_chunk_refusals(b, change, status):
+    rc, msg = call(b, "lin_chunk_fwd", chunk_args(b, **change))
+    assert rc == status and msg, (rc, msg)
+
+
+def test_chunk_workspace(b):
+    L = b.lib()
+    big = chunk_args(b, B=1, T=65536, Hk=4, H=4)
+    need = L.kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(big))
+    assert need != b.SIZE_MAX
+    if need:
+        assert call(b, "lin_chunk_fwd", put(big, workspace_bytes=need - 1))[0] == WORKSPACE
+        assert call(b, "lin_chunk_fwd", put(big, workspace=None, workspace_bytes=need))[0] == WORKSPACE
+        assert call(b, "lin_chunk_fwd", put(big, workspace=at(5)))[0] == ALIAS
+        assert call(b, "lin_chunk_fwd", put(big, workspace=at(4)))[0] == ALIAS
+        assert call(b, "lin_chunk_fwd", put(big, workspace=at(7) + 16))[0] == WORKSPACE
+    # the query looks at no pointer but cu_seqlens
+    for x in ("q", "k", "v", "g", "S0", "o", "S_T", "workspace"):
+        put(big, **{x: None})
+    assert L.kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(big)) == need
+    assert L.kda_lin_chunk_fwd_workspace_bytes(ctypes.byref(put(big, dk=48))) == b.SIZE_MAX
+    assert L.kda_lin_chunk_fwd_workspace_bytes(None) == b.SIZE_MAX
+    assert L.kda_lin_chunk_fwd(None, None) == NULL_PTR
+
+
+def decode_args(b, **kw):
+    a = b.LinDecodeArgs()
+    a.N, a.m, a.Hk, a.H, a.dk, a.dv = 3, 1, 2, 4, 128, 64
+    a.act_dtype, a.gate_dtype, a.out_dtype, a.scale = 1, 0, 1, 0.1
+    a.q, a.k, a.v, a.g, a.S, a.o = (at(i) for i in range(6))
+    return put(strides(a), **kw)
+
+
+@pytest.mark.parametrize("change,status", LIN + [
+    (dict(N=0), BAD_SHAPE), (dict(m=0), BAD_SHAPE), (dict(S=None), NULL_PTR), (dict(S=at(4) + 4), BAD_SHAPE),
+    (dict(N=1 << 23), BAD_SHAPE), (dict(o=at(4)), ALIAS), (dict(S=at(2)), ALIAS)])
+@pytest.mark.parametrize("name", ["lin_decode_step", "lin_decode_multi"])
+def test_decode_refusals(b, name, change, status):
+    rc, msg = call(b, name, decode_args(b, **change))
+    assert rc == status and msg, (rc, msg)
+
+
+def test_decode_forms(b):
+    assert call(b, "lin_decode_step", decode_args(b, m=2))[0] == UNSUPPORTED
+    assert call(b, "lin_decode_step", decode_args(b, accept=at(6)))[0] == UNSUPPORTED
+    assert call(b, "lin_decode_step", decode_args(b, o=None))[0] == NULL_PTR
+    assert call(b, "lin_decode_multi", decode_args(b, m=4, o=None))[0] == 0  # nothing to do
+    assert call(b, "lin_decode_multi", decode_args(b, m=4, accept=at(4)))[0] == ALIAS
+    assert call(b, "lin_decode_multi", decode_args(b, m=4, accept=at(5) + 8))[0] == ALIAS
+    assert b.lib().kda_lin_decode_step(None, None) == NULL_PTR
+    assert b.lib().kda_lin_decode_multi(None, None) == NULL_PTR
+
+
+PLAN_ARRAYS = ("block_table", "held", "lens", "new_lens", "free_pages", "ring", "held_out", "ring_out", "seq_lens",
+               "cu_seqlens", "slots", "positions")
+
+
+def plan_args(b, **kw):
+    a = b.PagePlanArgs()
+    a.N, a.page_size, a.max_pages, a.max_tokens, a.free_capacity, a.table_stride = 5, 16, 30, 100, 200, 32
+    for i, x in enumerate(PLAN_ARRAYS):
+        setattr(a, x, at(i))
+    return put(a, **kw)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(N=0), BAD_SHAPE), (dict(page_size=0), BAD_SHAPE), (dict(max_pages=0), BAD_SHAPE),
+    (dict(max_tokens=0), BAD_SHAPE), (dict(free_capacity=0), BAD_SHAPE), (dict(table_stride=29), BAD_SHAPE),
+    (dict(table_stride=1 << 60), BAD_SHAPE), (dict(N=(1 << 30) + 1), BAD_SHAPE)]
+    + [(dict([(x, None)]), NULL_PTR) for x in PLAN_ARRAYS[:10]]
+    + [(dict(held_out=at(1)), ALIAS), (dict(ring_out=at(5)), ALIAS), (dict(seq_lens=at(2) + 16), ALIAS),
+       (dict(cu_seqlens=at(3)), ALIAS), (dict(slots=at(0) + 400), ALIAS), (dict(positions=at(4)), ALIAS),
+       (dict(positions=at(10) + 792), ALIAS), (dict(cu_seqlens=at(8) - 20), ALIAS)])
+def test_plan_refusals(b, change, status):
+    rc, msg = call(b, "page_plan", plan_args(b, **change))
+    assert rc == status and msg, (rc, msg)
+    assert b.lib().kda_page_plan(None, None) == NULL_PTR
+
+
+def logits_args(b, **kw):
+    a = b.LogitsArgs()
+    a.N, a.R, a.V, a.dtype, a.out_dtype = 3, 2, 1000, 1, 0
+    a.logits, a.out, a.history, a.history_lens, a.prompt_lens, a.drafts = (at(i) for i in range(6))
+    a.seq_stride, a.row_stride, a.out_seq_stride, a.out_row_stride = 2000, 1000, 2000, 1000
+    a.history_stride, a.max_history, a.max_bias = 64, 60, 10
+    a.repetition, a.frequency, a.presence, a.bias_ids, a.bias, a.bias_counts = (at(i) for i in range(6, 12))
+    a.mask, a.mask_seq_stride, a.mask_row_stride, a.temperature = at(12), 64, 32, at(13)
+    a.workspace, a.workspace_bytes, a.flags = at(14), 1 << 20, 1
+    return put(a, **kw)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(N=0), BAD_SHAPE), (dict(R=0), BAD_SHAPE), (dict(V=0), BAD_SHAPE), (dict(V=(1 << 30) + 1), BAD_SHAPE),
+    (dict(N=1 << 20, R=64), BAD_SHAPE), (dict(dtype=2), BAD_DTYPE), (dict(out_dtype=4), BAD_DTYPE),
+    (dict(flags=2), UNSUPPORTED), (dict(logits=None), NULL_PTR), (dict(out=None), NULL_PTR),
+    (dict(history=None), NULL_PTR), (dict(history_lens=None), NULL_PTR), (dict(max_history=0), NULL_PTR),
+    (dict(bias=None), NULL_PTR), (dict(bias_ids=None), NULL_PTR), (dict(max_bias=0), NULL_PTR),
+    (dict(bias=None, bias_ids=None), NULL_PTR), (dict(history_stride=59), BAD_SHAPE),
+    (dict(max_history=(1 << 30) + 1, history_stride=1 << 31), BAD_SHAPE), (dict(R=1), BAD_SHAPE),
+    (dict(seq_stride=-1), BAD_SHAPE), (dict(mask_row_stride=-1), BAD_SHAPE), (dict(out_row_stride=999), BAD_SHAPE),
+    (dict(out_seq_stride=1999), BAD_SHAPE), (dict(out_seq_stride=0), BAD_SHAPE),
+    (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=8), WORKSPACE), (dict(workspace=at(14) + 64), WORKSPACE),
+    (dict(out=at(0)), ALIAS), (dict(out=at(0), out_dtype=1, out_row_stride=1008, out_seq_stride=2016), ALIAS),
+    (dict(out=at(0) + 2, out_dtype=1), ALIAS), (dict(out=at(12)), ALIAS), (dict(out=at(6)), ALIAS),
+    (dict(workspace=at(1)), ALIAS), (dict(workspace=at(2)), ALIAS)])
+def test_logits_refusals(b, change, status):
+    rc, msg = call(b, "adjust_logits", logits_args(b, **change))
+    assert rc == status and msg, (rc, msg)
+
+
+def test_logits_workspace(b):
+    L = b.lib()
+    assert L.kda_adjust_logits(None, None) == NULL_PTR
+    assert L.kda_adjust_logits_workspace_bytes(None) == b.SIZE_MAX
+    assert L.kda_adjust_logits_workspace_bytes(ctypes.byref(logits_args(b, V=0))) == b.SIZE_MAX
+    assert L.kda_adjust_logits_workspace_bytes(ctypes.byref(logits_args(b, flags=0))) == 0
+    need = L.kda_adjust_logits_workspace_bytes(ctypes.byref(logits_args(b, logits=None, out=None)))
+    assert 0 < need < 1 << 20
+
+
+# ---------------------------------------------------------------------- the plain forms themselves
+
+def test_lin_by_hand():
+    half = np.log(0.5)
+    o, S, _, _ = step_ref.lin(np.array([[[2.0]], [[1.0]]]), np.array([[[3.0]], [[1.0]]]),
+                              np.array([[[5.0]], [[7.0]]]), np.array([[half], [half]]), np.array([[[[4.0]]]]), 0.5)
+    assert np.allclose(o.ravel(), [0.5 * 2 * (2 + 15), 0.5 * (8.5 + 7)]) and np.allclose(S.ravel(), [15.5])
+
+
+def test_lin_is_decayed_attention():
+    rng = np.random.default_rng(0)
+    q, k, v = rng.standard_normal((3, 9, 2, 4))
+    g = -rng.random((9, 2))
+    o, _, _, _ = step_ref.lin(q, k, v, g, None, 1.0)
+    G = g.cumsum(0)
+    for h in range(2):
+        w = np.tril((q[:, h] @ k[:, h].T) * np.exp(G[:, None, h] - G[None, :, h]))
+        assert np.allclose(o[:, h], w @ v[:, h])
+
+
+def test_plan_by_hand():
+    table = np.array([[7, 8, -1], [9, -1, -1], [5, 6, -1]])
+    r = step_ref.plan(table, [2, 1, 2], [7, 4, 5], [2, -1, 3], np.array([3, 1, 2, 4, -1]), [3, 3], 4, 6)
+    # the ring holds 4, -1, 3 from place 3 on; sequence 0 needs a third page, 1 ends, 2 has room
+    assert r["table"].tolist() == [[7, 8, 4], [9, -1, -1], [5, 6, -1]]
+    assert r["free"].tolist() == [3, 9, 2, 4, -1] and r["ring"].tolist() == [4, 3]
+    assert r["held"].tolist() == [3, 0, 2] and r["seq_lens"].tolist() == [9, 0, 8] and r["cu"].tolist() == [0, 2, 2, 5]
+    assert r["slots"].tolist() == [35, 16, 25, 26, 27, -1] and r["positions"].tolist() == [7, 8, 5, 6, 7, -1]
+
+
+def test_plan_refuses_in_order():
+    table = -np.ones((4, 2), int)
+    r = step_ref.plan(table, [0] * 4, [0] * 4, [1, 5, 1, 0], np.arange(4), [0, 2], 4, 100)
+    assert r["cu"].tolist() == [0, 1, 1, 1, 1] and r["held"].tolist() == [1, 0, 0, 0] and r["ring"].tolist() == [1, 1]
+
+
+def test_logits_by_hand():
+    x = np.array([[[2.0, -2.0, 1.0, 0.5], [2.0, -2.0, 1.0, 0.5]]])
+    y = step_ref.logits(x, np.array([[0, 1, 1]]), [3], [1], np.array([[2]]), [2.0], [0.5], [0.25],
+                        np.array([[3, 3]]), np.array([[9.0, 1.0]]), None, np.array([[[14], [15]]]), [0.5])
+    assert np.allclose(y[0, 0, 1:], [2 * (-4 - 1.25), 2.0, 3.0]) and y[0, 0, 0] == -np.inf
+    assert np.allclose(y[0, 1], [2.0, 2 * (-4 - 1.25), 2 * (0.5 - 0.75), 3.0])
+    p = step_ref.logits(x, temperature=[0.0], probs=True)
+    assert p[0].tolist() == [[1, 0, 0, 0]] * 2
