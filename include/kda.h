@@ -476,7 +476,8 @@ kda_status kda_verify_drafts(const kda_verify_args* args, void* hip_stream);
  *              dense batch or packed sequences, as in kda_chunk_args (T = 0 is allowed: S_T receives
  *              S0, zeros if NULL). Rows of o at or past cu_seqlens[N] are left as they were. Offsets
  *              outside [0, T] are taken as the nearer bound, and a sequence that ends before it begins
- *              has no tokens; results of tokens that offsets give to two sequences are unspecified.
+ *              has no tokens; where offsets give tokens to two sequences, results from the first of
+ *              them on are unspecified.
  *   S0         [n_seq, H, dk, dv] fp32 initial states, or NULL for zeros.
  *   o          [B, T, H, dv] contiguous, out_dtype, 16-byte aligned. Overlaps no input.
  *   S_T        [n_seq, H, dk, dv] fp32 final states, or NULL. May be S0 itself (continue in place);
