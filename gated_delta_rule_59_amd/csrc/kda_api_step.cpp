@@ -166,6 +166,9 @@ kda_status kda_lin_chunk_fwd(const kda_lin_chunk_args* a, void* hip_stream) {
     return fail(KDA_ERR_NULL_PTR, "q, k, v, g and o must be non-NULL");
   s = validate_lin_rows(a, tok);
   if (s != KDA_OK) return s;
+  // a chunk's 64 rows lie within 2^32 bytes
+  if (std::max({a->q_token_stride, a->k_token_stride, a->v_token_stride}) * (int64_t)dsize(a->act_dtype) >= (1 << 26))
+    return fail(KDA_ERR_BAD_SHAPE, "token strides of q, k and v must be below 2^26 bytes");
   if (!aligned16(a->S0) || !aligned16(a->S_T))
     return fail(KDA_ERR_BAD_SHAPE, "S0 and S_T must be 16-byte aligned");
   if (need && (!a->workspace || a->workspace_bytes < need))

@@ -8,9 +8,9 @@
 //
 // which are matrix products but for the factors. A workgroup walks chunk after chunk through one
 // segment of one (sequence, head), the state in its accumulators. Segments of a sequence run in
-// parallel: lin_walk_kernel<..., true> sums up each segment but the last from a state of zeros, and
+// parallel: lin_walk_kernel<..., 0> sums up each segment but the last from a state of zeros, and
 // lin_entries_kernel turns that into the states that enter the segments (S <- e^{G} S + Z from one to
-// the next); then lin_walk_kernel<..., false> does the walk proper. Without segments only the last is
+// the next); then the others do the walk proper. Without segments only the last is
 // launched.
 //
 // Layout. Every product is a v_mfma_f32_16x16x32_bf16. Each wave owns 16 or 32 value channels, for
@@ -25,10 +25,9 @@
 // exchanged between the waves through LDS.
 //
 // Precision. bf16 inputs go into products as they are. What is no bf16 number goes in parts, each the
-// rounded rest of the one before: the state and the weights (q_i . k_j) e^{G_i - G_j} in two (2^-17
-// each, what o has beside its own rounding), decayed values in three (exact to 2^-25: the state adds
-// up thousands of them, and is a 32-bit result). Two of them for the state would leave it off by
-// 1.6e-6. G is summed in 64 bits and kept in two 32-bit parts, so that a strong decay costs the
+// rounded rest of the one before. Decayed values go in three (2^-25: the state is a 32-bit result); two
+// would leave it off by 1.6e-6. So do the state and the weights (q_i . k_j) e^{G_i - G_j} where o is
+// fp32; where it is bf16, two (2^-17) are as good. G is summed in 64 bits and kept in two 32-bit parts, so that a strong decay costs the
 // differences after it nothing.
 #include <algorithm>
 
@@ -42,7 +41,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kC = 64;      // tokens of a chunk
-constexpr int kPad = 8;     // of an LDS row: 16 neighbouring rows begin in different banks
 
 // Which segment of which sequence job `job` is: false if there is none.
 struct Job {
@@ -89,6 +87,24 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, int job, Job* j) {
   return false;
 }
 
+// A barrier that orders the LDS only: rows of the next chunk stay on their way across it, and so do
+// results. (__syncthreads waits for both: 14 us per chunk where this takes @@.)
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Where channel c of row r lies in an LDS tile of rows of D. 16-byte pieces of a row change places with
+// the row, so that 16 lanes that read one piece of 16 rows, and 16 lanes that read a quarter of a
+// 32-channel block of each of four rows, meet all 64 banks. (Padded rows do the first only: 46 % of the
+// LDS's time went to conflicts of the second.)
+template <int D>
+__device__ __forceinline__ int tile_at(int r, int c) {
+  constexpr int kLog = D == 128 ? 0 : D == 64 ? 1 : 2;  // rows of 64 banks
+  return r * D + ((((c >> 3) ^ ((r >> 2 & 3) | ((r & 3) >> kLog) << 2)) << 3) | (c & 7));
+}
+
 // Four 4 x 16 blocks of 16-bit values, one per 16 lanes, transposed on the way out of the LDS.
 __device__ __forceinline__ s16x4 read_tr(const uint16_t* p) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -99,19 +115,34 @@ __device__ __forceinline__ bf16x8 pair(s16x4 a, s16x4 b) {
   return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 }
 
-// The two or three bf16 parts of eight values.
+// The bf16 parts of eight values.
 template <int PARTS>
 __device__ __forceinline__ void parts_of(const float* x, bf16x8* y) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float r = x[i];
+  for (int i = 0; i < 8; i += 2) {
+    f32x2 r{x[i], x[i + 1]};
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
-      const __bf16 b = static_cast<__bf16>(r);
-      y[k][i] = b;
-      if (k + 1 < PARTS) r -= static_cast<float>(b);
+      const bf16x2 b = __builtin_convertvector(r, bf16x2);
+      y[k][i] = b[0];
+      y[k][i + 1] = b[1];
+      const uint32_t u = __builtin_bit_cast(uint32_t, b);
+      if (k + 1 < PARTS) {
+        r[0] -= __uint_as_float(u << 16);
+        r[1] -= __uint_as_float(u & 0xffff0000u);
+      }
     }
   }
+}
+
+__device__ __forceinline__ void store4(float* p, const floatx4& x) { *reinterpret_cast<floatx4*>(p) = x; }
+__device__ __forceinline__ void store4(uint16_t* p, const floatx4& x) {
+  s16x4 y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = (short)lin_bf16(x[i]);
+  *reinterpret_cast<s16x4*>(p) = y;
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -136,16 +167,18 @@ __device__ __forceinline__ float* decays_of(const LinPlan& p) {
   return static_cast<float*>(p.workspace) + (int64_t)p.jobs * p.H * p.dk * p.dv;
 }
 
-template <int DK, int DV, bool SUM>
+// PARTS: bf16 parts of states and weights in what becomes o; 0: sums of segments only.
+template <int DK, int DV, int PARTS, typename O>
 __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(const LinPlan p) {
   using Sh = Shape<DK, DV>;
+  constexpr bool SUM = PARTS == 0;
+  constexpr int NP = SUM ? 1 : PARTS;
   constexpr int NT = Sh::kThreads, NW = Sh::kWaves, CT = Sh::kTiles, KT = DK / 16;
-  constexpr int SK = DK + kPad, SV = DV + kPad;
   constexpr int QL = kC * DK / 8 / NT, VL = kC * DV / 8 / NT;  // 16-byte pieces per thread
-  __shared__ __align__(16) uint16_t s_q[SUM ? 8 : kC * SK], s_k[kC * SK], s_v[kC * SV];
-  __shared__ bf16x8 s_p[SUM ? 1 : 2][SUM ? 1 : 4][2][64];
-  __shared__ __align__(16) float s_hi[kC], s_lo[kC], s_w[kC];
-  __shared__ float s_all;
+  __shared__ __align__(16) uint16_t s_q[SUM ? 8 : kC * DK], s_k[kC * DK], s_v[kC * DV];
+  __shared__ bf16x8 s_p[NP][SUM ? 1 : 4][2][64];
+  __shared__ __align__(16) float s_hi[2][kC], s_lo[2][kC], s_w[2][kC];
+  __shared__ float s_all[2];
 
   const int job = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
   Job j;
@@ -180,61 +213,83 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
           S[kt][c][x] = in[Sh::key(kt >> 1, kt & 1, 4 * g + x) * DV + Sh::value(wave, c, l15)];
   }
 
-  const char* const qp = p.q + hk * p.q_head;
-  const char* const kp = p.k + hk * p.k_head;
-  const char* const vp = p.v + h * p.v_head;
+  const char* const qp = p.q + row0 * p.q_token + hk * p.q_head;
+  const char* const kp = p.k + row0 * p.k_token + hk * p.k_head;
+  const char* const vp = p.v + row0 * p.v_token + h * p.v_head;
+  const unsigned q_row = (unsigned)p.q_token, k_row = (unsigned)p.k_token, v_row = (unsigned)p.v_token;
   u32x4 rq[SUM ? 1 : QL], rk[QL], rv[VL];
-  float gate = 0.f;
-  auto fetch = [&](int c0) {  // rows past the end are zeros
+  uint32_t gate = 0;   // wave 0: a token's
+  double total = 0.0;  // wave 0: of the chunks so far, to base 2
+  // The chunk's rows; those past the end are the last one again: o has no room for theirs, and to the
+  // state they do not count (s_w).
+  auto fetch = [&](int c0) {
+    const unsigned most = len - 1 - c0;
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
-      const int x = t + i * NT, r = x / (DK / 8), e = x % (DK / 8) * 16;
-      const bool real = c0 + r < len;
-      const int64_t row = row0 + c0 + r;
-      rk[i] = real ? *reinterpret_cast<const u32x4*>(kp + row * p.k_token + e) : u32x4{0, 0, 0, 0};
-      if (!SUM) rq[i] = real ? *reinterpret_cast<const u32x4*>(qp + row * p.q_token + e) : u32x4{0, 0, 0, 0};
+      const unsigned x = t + i * NT, r = min(x / (DK / 8), most), e = x % (DK / 8) * 16;
+      rk[i] = *reinterpret_cast<const u32x4*>(kp + c0 * p.k_token + (r * k_row + e));
+      if (!SUM) rq[i] = *reinterpret_cast<const u32x4*>(qp + c0 * p.q_token + (r * q_row + e));
     }
 #pragma unroll
     for (int i = 0; i < VL; ++i) {
-      const int x = t + i * NT, r = x / (DV / 8), e = x % (DV / 8) * 16;
-      rv[i] = c0 + r < len ? *reinterpret_cast<const u32x4*>(vp + (row0 + c0 + r) * p.v_token + e) : u32x4{0, 0, 0, 0};
+      const unsigned x = t + i * NT, r = min(x / (DV / 8), most), e = x % (DV / 8) * 16;
+      rv[i] = *reinterpret_cast<const u32x4*>(vp + c0 * p.v_token + (r * v_row + e));
     }
-    if (wave == 0) gate = c0 + lane < len ? lin_gate(p, row0 + c0 + lane, h) : 0.f;
   };
-  double total = 0.0;  // SUM, wave 0: of the chunks so far, log2
-  if (len > 0) fetch(0);
+  auto fetch_gate = [&](int c0) {  // as it is in memory: converting it would wait for it here
+    const int64_t i = p.fixed ? h : (row0 + min(c0 + lane, len - 1)) * p.H + h;
+    gate = p.gate_bf16 ? static_cast<const uint16_t*>(p.g)[i] : static_cast<const uint32_t*>(p.g)[i];
+  };
+  // The chunk's sums of logarithms (to base 2), and the factors that the state takes.
+  auto sum_gates = [&](uint32_t gate, int c0, int to) {
+    // a decay below e^-1000 is 0 in any case, and -infinity would leave differences undefined
+    const bool real = c0 + lane < len;
+    const float ln = __uint_as_float(p.gate_bf16 ? gate << 16 : gate);
+    double G = real ? (double)(ln < -1000.f ? -1000.f : ln) * 1.4426950408889634 : 0.0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double y = __shfl_up(G, d, 64);
+      if (lane >= d) G += y;
+    }
+    const double all = __shfl(G, 63, 64);
+    const float hi = (float)G;
+    s_hi[to][lane] = hi;
+    s_lo[to][lane] = (float)(G - (double)hi);
+    s_w[to][lane] = real ? exp2_of((float)(all - G)) : 0.f;
+    if (lane == 0) s_all[to] = exp2_of((float)all);
+    total += all;
+  };
+  if (len > 0) {
+    if (wave == 0) {
+      fetch_gate(0);
+      const uint32_t had = gate;
+      fetch_gate(kC);
+      sum_gates(had, 0, 0);
+    }
+    fetch(0);
+  }
 
   for (int c0 = 0; c0 < len; c0 += kC) {
-    if (c0) __syncthreads();
+    const int now = c0 / kC & 1;
+    if (c0) lds_barrier();
 #pragma unroll
     for (int i = 0; i < QL; ++i) {
-      const int x = t + i * NT, at = x / (DK / 8) * SK + x % (DK / 8) * 8;
+      const int x = t + i * NT, at = tile_at<DK>(x / (DK / 8), x % (DK / 8) * 8);
       *reinterpret_cast<u32x4*>(&s_k[at]) = rk[i];
       if (!SUM) *reinterpret_cast<u32x4*>(&s_q[at]) = rq[i];
     }
 #pragma unroll
     for (int i = 0; i < VL; ++i) {
       const int x = t + i * NT;
-      *reinterpret_cast<u32x4*>(&s_v[x / (DV / 8) * SV + x % (DV / 8) * 8]) = rv[i];
+      *reinterpret_cast<u32x4*>(&s_v[tile_at<DV>(x / (DV / 8), x % (DV / 8) * 8)]) = rv[i];
     }
-    if (wave == 0) {
-      // a decay below e^-1000 is 0 in any case, and -infinity would leave differences undefined
-      double G = (double)(gate < -1000.f ? -1000.f : gate) * 1.4426950408889634;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(G, d, 64);
-        if (lane >= d) G += y;
-      }
-      const double all = __shfl(G, 63, 64);
-      const float hi = (float)G;
-      s_hi[lane] = hi;
-      s_lo[lane] = (float)(G - (double)hi);
-      s_w[lane] = exp2_of((float)(all - G));
-      if (lane == 0) s_all = exp2_of((float)all);
-      total += all;
+    lds_barrier();
+    if (c0 + kC < len) {
+      const uint32_t had = gate;
+      if (wave == 0) fetch_gate(c0 + 2 * kC);
+      fetch(c0 + kC);
+      if (wave == 0) sum_gates(had, c0 + kC, now ^ 1);  // the wave with the fewest weights to form
     }
-    __syncthreads();
-    if (c0 + kC < len) fetch(c0 + kC);
 
     if (!SUM) {
       // weights (q_i . k_j) e^{G_i - G_j} of i tile `it`, transposed: rows j, columns i
@@ -242,10 +297,10 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
       for (int x = 0; x < 4 / NW; ++x) {
         const int it = x ? 3 - wave : wave;
         const int i = it * 16 + l15;
-        const float hi = s_hi[i], lo = s_lo[i];
+        const float hi = s_hi[now][i], lo = s_lo[now][i];
         bf16x8 q[DK / 32];
 #pragma unroll
-        for (int ks = 0; ks < DK / 32; ++ks) q[ks] = *reinterpret_cast<const bf16x8*>(&s_q[i * SK + ks * 32 + 8 * g]);
+        for (int ks = 0; ks < DK / 32; ++ks) q[ks] = *reinterpret_cast<const bf16x8*>(&s_q[tile_at<DK>(i, ks * 32 + 8 * g)]);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (2 * s > it) continue;
@@ -257,18 +312,18 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
             if (jt <= it) {
 #pragma unroll
               for (int ks = 0; ks < DK / 32; ++ks)
-                d = mfma_bf16(*reinterpret_cast<const bf16x8*>(&s_k[(jt * 16 + l15) * SK + ks * 32 + 8 * g]), q[ks], d);
+                d = mfma_bf16(*reinterpret_cast<const bf16x8*>(&s_k[tile_at<DK>(jt * 16 + l15, ks * 32 + 8 * g)]), q[ks], d);
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const int jj = jt * 16 + 4 * g + y;
-              w[4 * e + y] = jj <= i ? d[y] * exp2_of((hi - s_hi[jj]) + (lo - s_lo[jj])) : 0.f;
+              w[4 * e + y] = jj <= i ? d[y] * exp2_of((hi - s_hi[now][jj]) + (lo - s_lo[now][jj])) : 0.f;
             }
           }
-          bf16x8 parts[2];
-          parts_of<2>(w, parts);
-          s_p[0][it][s][lane] = parts[0];
-          s_p[1][it][s][lane] = parts[1];
+          bf16x8 parts[NP];
+          parts_of<NP>(w, parts);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) s_p[k][it][s][lane] = parts[k];
         }
       }
       // S^T q
@@ -279,19 +334,19 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
         for (int c = 0; c < CT; ++c) o[it][c] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ks = 0; ks < DK / 32; ++ks) {
-        bf16x8 sp[CT][2];
+        bf16x8 sp[CT][NP];
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           const float x[8] = {S[2 * ks][c][0],     S[2 * ks][c][1],     S[2 * ks][c][2],     S[2 * ks][c][3],
                               S[2 * ks + 1][c][0], S[2 * ks + 1][c][1], S[2 * ks + 1][c][2], S[2 * ks + 1][c][3]};
-          parts_of<2>(x, sp[c]);
+          parts_of<NP>(x, sp[c]);
         }
         bf16x8 q[4];
 #pragma unroll
         for (int it = 0; it < 4; ++it)
-          q[it] = *reinterpret_cast<const bf16x8*>(&s_q[(it * 16 + l15) * SK + ks * 32 + 8 * g]);
+          q[it] = *reinterpret_cast<const bf16x8*>(&s_q[tile_at<DK>(it * 16 + l15, ks * 32 + 8 * g)]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < NP; ++k)
 #pragma unroll
           for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -299,21 +354,21 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
       }
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const float a = exp2_of(s_hi[it * 16 + l15]);
+        const float a = exp2_of(s_hi[now][it * 16 + l15]);
 #pragma unroll
         for (int c = 0; c < CT; ++c) o[it][c] *= a;
       }
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         bf16x8 v[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          const uint16_t* at = &s_v[(32 * s + 4 * g + (l15 >> 2)) * SV + Sh::value(wave, c, 4 * (l15 & 3))];
-          v[c] = pair(read_tr(at), read_tr(at + 16 * SV));
+          const uint16_t* at = &s_v[tile_at<DV>(32 * s + 4 * g + (l15 >> 2), Sh::value(wave, c, 4 * (l15 & 3)))];
+          v[c] = pair(read_tr(at), read_tr(at + 16 * DV));
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < NP; ++k)
 #pragma unroll
           for (int it = 2 * s; it < 4; ++it) {
             const bf16x8 w = s_p[k][it][s][lane];
@@ -325,27 +380,15 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
       for (int it = 0; it < 4; ++it) {
         const int i = c0 + it * 16 + l15;
         if (i < len) {
-          const int64_t e = ((row0 + i) * p.H + h) * DV + Sh::value(wave, 0, 4 * g);
-          if (p.out_bf16) {
-            uint16_t* out = static_cast<uint16_t*>(p.o) + e;
+          O* out = static_cast<O*>(p.o) + ((row0 + i) * p.H + h) * DV + Sh::value(wave, 0, 4 * g);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              s16x4 y;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) y[x] = (short)lin_bf16(p.scale * o[it][c][x]);
-              *reinterpret_cast<s16x4*>(out + 4 * c) = y;
-            }
-          } else {
-            float* out = static_cast<float*>(p.o) + e;
-#pragma unroll
-            for (int c = 0; c < CT; ++c) *reinterpret_cast<floatx4*>(out + 4 * c) = p.scale * o[it][c];
-          }
+          for (int c = 0; c < CT; ++c) store4(out + 4 * c, p.scale * o[it][c]);
         }
       }
     }
 
     // the state that leaves the chunk
-    const float all = s_all;
+    const float all = s_all[now];
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -353,12 +396,12 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       bf16x8 vw[CT][3];
-      const floatx4 w0 = *reinterpret_cast<const floatx4*>(&s_w[32 * s + 4 * g]);
-      const floatx4 w1 = *reinterpret_cast<const floatx4*>(&s_w[32 * s + 16 + 4 * g]);
+      const floatx4 w0 = *reinterpret_cast<const floatx4*>(&s_w[now][32 * s + 4 * g]);
+      const floatx4 w1 = *reinterpret_cast<const floatx4*>(&s_w[now][32 * s + 16 + 4 * g]);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const uint16_t* at = &s_v[(32 * s + 4 * g + (l15 >> 2)) * SV + Sh::value(wave, c, 4 * (l15 & 3))];
-        const s16x4 a = read_tr(at), b = read_tr(at + 16 * SV);
+        const uint16_t* at = &s_v[tile_at<DV>(32 * s + 4 * g + (l15 >> 2), Sh::value(wave, c, 4 * (l15 & 3)))];
+        const s16x4 a = read_tr(at), b = read_tr(at + 16 * DV);
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -369,8 +412,8 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
       }
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt) {
-        const uint16_t* at = &s_k[(32 * s + 4 * g + (l15 >> 2)) * SK + Sh::key(kt >> 1, kt & 1, 4 * (l15 & 3))];
-        const bf16x8 k = pair(read_tr(at), read_tr(at + 16 * SK));
+        const uint16_t* at = &s_k[tile_at<DK>(32 * s + 4 * g + (l15 >> 2), Sh::key(kt >> 1, kt & 1, 4 * (l15 & 3)))];
+        const bf16x8 k = pair(read_tr(at), read_tr(at + 16 * DK));
 #pragma unroll
         for (int y = 0; y < 3; ++y)
 #pragma unroll
@@ -463,11 +506,14 @@ hipError_t launch(const LinPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.jobs * p.H));
   constexpr int threads = Shape<DK, DV>::kThreads;
   if (p.T > p.seg) {
-    lin_walk_kernel<DK, DV, true><<<grid, threads, 0, stream>>>(p);
+    lin_walk_kernel<DK, DV, 0, float><<<grid, threads, 0, stream>>>(p);
     constexpr int groups = (DK * DV / 4 + 255) / 256;
     lin_entries_kernel<DK, DV><<<dim3((unsigned)((int64_t)p.n_seq * p.H * groups)), 256, 0, stream>>>(p);
   }
-  lin_walk_kernel<DK, DV, false><<<grid, threads, 0, stream>>>(p);
+  if (p.out_bf16)
+    lin_walk_kernel<DK, DV, 2, uint16_t><<<grid, threads, 0, stream>>>(p);
+  else
+    lin_walk_kernel<DK, DV, 3, float><<<grid, threads, 0, stream>>>(p);
   return hipGetLastError();
 }
 

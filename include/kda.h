@@ -458,7 +458,8 @@ kda_status kda_verify_drafts(const kda_verify_args* args, void* hip_stream);
  *              2^-16 of its largest terms, S by 2^-22.
  *   q, k, v    [B, T, heads, d] (decode: [N, m, heads, d]): token t = b * T + j of head h begins at
  *              t * token_stride + h * head_stride (elements), so views of a fused projection can be
- *              passed. Pointers and strides are multiples of 16 bytes.
+ *              passed. Pointers and strides are multiples of 16 bytes (kda_lin_chunk_fwd: token
+ *              strides below 2^26 bytes).
  *   g          natural logarithm of each token's decay, contiguous [B, T, H] (decode [N, m, H]); with
  *              KDA_LIN_FIXED_DECAY [H], the same for every token. -infinity is a decay of 0, which
  *              ends the memory of all earlier tokens. Values above 0 (growth) are taken as they are.
