@@ -40,7 +40,8 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kC = 64;      // tokens of a chunk
+constexpr int kC = 64;          // tokens of a chunk
+constexpr double kHeld = 24.0;  // most that a state may be off by in the accumulators, in powers of 2
 
 // Which segment of which sequence job `job` is: false if there is none.
 struct Job {
@@ -137,6 +138,29 @@ __device__ __forceinline__ void parts_of(const float* x, bf16x8* y) {
   }
 }
 
+// Sums over the lanes up to each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double plus_lane(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_of(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sums(double x) {
+  x = plus_lane<0x111, 0xf>(x);  // row_shr: 1, 2, 4, 8: within 16 lanes
+  x = plus_lane<0x112, 0xf>(x);
+  x = plus_lane<0x114, 0xf>(x);
+  x = plus_lane<0x118, 0xf>(x);
+  x = plus_lane<0x142, 0xa>(x);  // row_bcast: lane 15 to the next row, lane 31 to the upper half
+  return plus_lane<0x143, 0xc>(x);
+}
+
 __device__ __forceinline__ void store4(float* p, const floatx4& x) { *reinterpret_cast<floatx4*>(p) = x; }
 __device__ __forceinline__ void store4(uint16_t* p, const floatx4& x) {
   s16x4 y;
@@ -177,8 +201,8 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
   constexpr int QL = kC * DK / 8 / NT, VL = kC * DV / 8 / NT;  // 16-byte pieces per thread
   __shared__ __align__(16) uint16_t s_q[SUM ? 8 : kC * DK], s_k[kC * DK], s_v[kC * DV];
   __shared__ bf16x8 s_p[NP][SUM ? 1 : 4][2][64];
-  __shared__ __align__(16) float s_hi[2][kC], s_lo[2][kC], s_w[2][kC];
-  __shared__ float s_all[2];
+  __shared__ __align__(16) float s_hi[2][kC], s_lo[2][kC], s_w[2][kC], s_e[2][kC];
+  __shared__ float s_settle[2], s_held;
 
   const int job = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
   Job j;
@@ -240,24 +264,26 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
     const int64_t i = p.fixed ? h : (row0 + min(c0 + lane, len - 1)) * p.H + h;
     gate = p.gate_bf16 ? static_cast<const uint16_t*>(p.g)[i] : static_cast<const uint32_t*>(p.g)[i];
   };
-  // The chunk's sums of logarithms (to base 2), and the factors that the state takes.
+  // The chunk's sums of logarithms (to base 2), and its factors. The state in the accumulators times
+  // 2^held is the one meant: while 2^held is near 1, only new values are scaled (by its inverse) and the
+  // accumulators stay as they are.
+  double held = 0.0;
   auto sum_gates = [&](uint32_t gate, int c0, int to) {
     // a decay below e^-1000 is 0 in any case, and -infinity would leave differences undefined
     const bool real = c0 + lane < len;
     const float ln = __uint_as_float(p.gate_bf16 ? gate << 16 : gate);
-    double G = real ? (double)(ln < -1000.f ? -1000.f : ln) * 1.4426950408889634 : 0.0;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double y = __shfl_up(G, d, 64);
-      if (lane >= d) G += y;
-    }
-    const double all = __shfl(G, 63, 64);
+    const double G = wave_sums(real ? (double)(ln < -1000.f ? -1000.f : ln) * 1.4426950408889634 : 0.0);
+    const double all = lane_of(G, 63);
     const float hi = (float)G;
     s_hi[to][lane] = hi;
     s_lo[to][lane] = (float)(G - (double)hi);
-    s_w[to][lane] = real ? exp2_of((float)(all - G)) : 0.f;
-    if (lane == 0) s_all[to] = exp2_of((float)all);
-    total += all;
+    s_e[to][lane] = p.scale * exp2_of((float)(G + held));
+    const double next = held + all;
+    const bool settle = !(fabs(next) <= kHeld);
+    s_w[to][lane] = real ? exp2_of((float)(settle ? all - G : -(held + G))) : 0.f;
+    if (lane == 0) s_settle[to] = settle ? exp2_of((float)next) : 1.f;
+    held = lane_of(settle ? 0.0 : next, 0);
+    if (SUM) total = lane_of(total + all, 0);
   };
   if (len > 0) {
     if (wave == 0) {
@@ -307,17 +333,22 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
           float w[8];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int jt = 2 * s + e;
-            floatx4 d{0.f, 0.f, 0.f, 0.f};
-            if (jt <= it) {
+            const int jt = 2 * s + e, j0 = jt * 16 + 4 * g;
+            if (jt > it) {
 #pragma unroll
-              for (int ks = 0; ks < DK / 32; ++ks)
-                d = mfma_bf16(*reinterpret_cast<const bf16x8*>(&s_k[tile_at<DK>(jt * 16 + l15, ks * 32 + 8 * g)]), q[ks], d);
+              for (int y = 0; y < 4; ++y) w[4 * e + y] = 0.f;
+              continue;
             }
+            floatx4 d{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < DK / 32; ++ks)
+              d = mfma_bf16(*reinterpret_cast<const bf16x8*>(&s_k[tile_at<DK>(jt * 16 + l15, ks * 32 + 8 * g)]), q[ks], d);
+            const floatx4 jhi = *reinterpret_cast<const floatx4*>(&s_hi[now][j0]);
+            const floatx4 jlo = *reinterpret_cast<const floatx4*>(&s_lo[now][j0]);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const int jj = jt * 16 + 4 * g + y;
-              w[4 * e + y] = jj <= i ? d[y] * exp2_of((hi - s_hi[now][jj]) + (lo - s_lo[now][jj])) : 0.f;
+              const float x = d[y] * (p.scale * exp2_of((hi - jhi[y]) + (lo - jlo[y])));
+              w[4 * e + y] = j0 + y <= i ? x : 0.f;
             }
           }
           bf16x8 parts[NP];
@@ -326,7 +357,8 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
           for (int k = 0; k < NP; ++k) s_p[k][it][s][lane] = parts[k];
         }
       }
-      // S^T q
+      // S^T q, while the other workgroup's waves are in front of their products as far as may be
+      __builtin_amdgcn_s_setprio(1);
       floatx4 o[4][CT];
 #pragma unroll
       for (int it = 0; it < 4; ++it)
@@ -354,7 +386,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
       }
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const float a = exp2_of(s_hi[now][it * 16 + l15]);
+        const float a = s_e[now][it * 16 + l15];
 #pragma unroll
         for (int c = 0; c < CT; ++c) o[it][c] *= a;
       }
@@ -382,17 +414,20 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
         if (i < len) {
           O* out = static_cast<O*>(p.o) + ((row0 + i) * p.H + h) * DV + Sh::value(wave, 0, 4 * g);
 #pragma unroll
-          for (int c = 0; c < CT; ++c) store4(out + 4 * c, p.scale * o[it][c]);
+          for (int c = 0; c < CT; ++c) store4(out + 4 * c, o[it][c]);
         }
       }
     }
 
     // the state that leaves the chunk
-    const float all = s_all[now];
+    if (!SUM) __builtin_amdgcn_s_setprio(0);
+    const float settle = s_settle[now];
+    if (settle != 1.f) {
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int c = 0; c < CT; ++c) S[kt][c] *= all;
+        for (int c = 0; c < CT; ++c) S[kt][c] *= settle;
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       bf16x8 vw[CT][3];
@@ -422,6 +457,15 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
     }
   }
 
+  if (SUM || (last && p.S_T)) {
+    if (t == 0) s_held = exp2_of((float)held);
+    lds_barrier();
+    const float f = s_held;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) S[kt][c] *= f;
+  }
   if (SUM) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
