@@ -38,9 +38,11 @@ namespace kda {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kC = 64;          // tokens of a chunk
+constexpr unsigned kTileI = 0xffa94, kTileJ = 0xe4910;  // tiles (0, 0), (1, 0), (1, 1), (2, 0), ..., two bits each
 constexpr double kHeld = 24.0;  // most that a state may be off by in the accumulators, in powers of 2
 
 // Which segment of which sequence job `job` is: false if there is none.
@@ -61,6 +63,22 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, int job, Job* j) {
   }
   const int lane = threadIdx.x & 63;
   int before = 0;
+  if (p.T <= p.seg && p.n_seq <= 64) {  // one segment each: the longest sequences first
+    int64_t first;
+    int len = -1, above = 0;
+    if (lane < p.n_seq) lin_tokens(p, lane, &first, &len);
+    for (int m = 0; m < p.n_seq; ++m) {
+      const int x = __shfl(len, m, 64);
+      above += x > len || (x == len && m < lane);
+    }
+    const uint64_t which = __ballot(lane < p.n_seq && above == job);
+    if (!which) return false;
+    j->n = __builtin_ctzll(which);
+    j->s = 0;
+    j->segments = 1;
+    lin_tokens(p, j->n, &j->first, &j->len);
+    return true;
+  }
   for (int n0 = 0; n0 < p.n_seq; n0 += 64) {
     int64_t first;
     int len = 0, x = 0;
@@ -106,6 +124,15 @@ __device__ __forceinline__ int tile_at(int r, int c) {
   return r * D + ((((c >> 3) ^ ((r >> 2 & 3) | ((r & 3) >> kLog) << 2)) << 3) | (c & 7));
 }
 
+// Which (job, head), in this order, workgroup b takes. Workgroups b and b + 256 share a CU, where the
+// earlier goes first: of up to 512 in order of length, the second half goes backwards, so that long ones
+// share with short ones. Where heads share queries and keys, an XCD (b mod 8) takes neighbouring ones.
+__device__ __forceinline__ unsigned place_of(const LinPlan& p, unsigned b) {
+  const unsigned all = gridDim.x;
+  if (p.cu_seqlens && p.T <= p.seg && p.n_seq <= 64) return b < 256 || all > 512 ? b : all - 1 - (b - 256);
+  return p.H != p.Hk && all % 8 == 0 ? b % 8 * (all / 8) + b / 8 : b;
+}
+
 // Four 4 x 16 blocks of 16-bit values, one per 16 lanes, transposed on the way out of the LDS.
 __device__ __forceinline__ s16x4 read_tr(const uint16_t* p) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -116,13 +143,13 @@ __device__ __forceinline__ bf16x8 pair(s16x4 a, s16x4 b) {
   return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 }
 
-// The bf16 parts of eight values.
-template <int PARTS>
-__device__ __forceinline__ void parts_of(const float* x, bf16x8* y) {
+// The bf16 parts of N values.
+template <int PARTS, int N, typename V>
+__device__ __forceinline__ void parts_of(const float* x, V* y) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
+  for (int i = 0; i < N; i += 2) {
     f32x2 r{x[i], x[i + 1]};
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) {
@@ -200,15 +227,17 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
   constexpr int NT = Sh::kThreads, NW = Sh::kWaves, CT = Sh::kTiles, KT = DK / 16;
   constexpr int QL = kC * DK / 8 / NT, VL = kC * DV / 8 / NT;  // 16-byte pieces per thread
   __shared__ __align__(16) uint16_t s_q[SUM ? 8 : kC * DK], s_k[kC * DK], s_v[kC * DV];
-  __shared__ bf16x8 s_p[NP][SUM ? 1 : 4][2][64];
+  __shared__ bf16x4 s_p[NP][SUM ? 1 : 4][2][64][2];  // [part][i tile][j pair][lane][j tile of the pair]
   __shared__ __align__(16) float s_hi[2][kC], s_lo[2][kC], s_w[2][kC], s_e[2][kC];
   __shared__ float s_settle[2], s_held;
 
-  const int job = blockIdx.x / p.H, h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
+  const unsigned at = place_of(p, blockIdx.x);
+  const int job = at / p.H, h = at % p.H, hk = h / (p.H / p.Hk);
   Job j;
   if (!lin_job(p, job, &j)) return;
   if (SUM && j.s == j.segments - 1) return;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, l15 = lane & 15, g = lane >> 4;
+  const int wave_s = __builtin_amdgcn_readfirstlane(wave);
   const int begin = j.s * p.seg, len = min(p.seg, j.len - begin);
   const int64_t row0 = j.first + begin;
   const bool last = j.s == j.segments - 1;
@@ -242,8 +271,9 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
   const char* const vp = p.v + row0 * p.v_token + h * p.v_head;
   const unsigned q_row = (unsigned)p.q_token, k_row = (unsigned)p.k_token, v_row = (unsigned)p.v_token;
   u32x4 rq[SUM ? 1 : QL], rk[QL], rv[VL];
-  uint32_t gate = 0;   // wave 0: a token's
-  double total = 0.0;  // wave 0: of the chunks so far, to base 2
+  constexpr int kGates = NW - 1;  // a wave with fewer weights to form than others
+  uint32_t gate = 0;   // that wave: a token's
+  double total = 0.0;  // that wave: of the chunks so far, to base 2
   // The chunk's rows; those past the end are the last one again: o has no room for theirs, and to the
   // state they do not count (s_w).
   auto fetch = [&](int c0) {
@@ -285,8 +315,15 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
     held = lane_of(settle ? 0.0 : next, 0);
     if (SUM) total = lane_of(total + all, 0);
   };
+  if (!SUM && t < 64) {  // weights above the diagonal that products read: tiles (0, 1) and (2, 3)
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      s_p[k][0][0][t][1] = bf16x4{0.f, 0.f, 0.f, 0.f};
+      s_p[k][2][1][t][1] = bf16x4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
   if (len > 0) {
-    if (wave == 0) {
+    if (wave == kGates) {
       fetch_gate(0);
       const uint32_t had = gate;
       fetch_gate(kC);
@@ -312,50 +349,51 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
     lds_barrier();
     if (c0 + kC < len) {
       const uint32_t had = gate;
-      if (wave == 0) fetch_gate(c0 + 2 * kC);
+      if (wave == kGates) fetch_gate(c0 + 2 * kC);
       fetch(c0 + kC);
-      if (wave == 0) sum_gates(had, c0 + kC, now ^ 1);  // the wave with the fewest weights to form
+      if (wave == kGates) sum_gates(had, c0 + kC, now ^ 1);
     }
 
-    if (!SUM) {
-      // weights (q_i . k_j) e^{G_i - G_j} of i tile `it`, transposed: rows j, columns i
+    // values, a column each
+    bf16x8 v[2][CT];
+    auto read_values = [&] {
 #pragma unroll
-      for (int x = 0; x < 4 / NW; ++x) {
-        const int it = x ? 3 - wave : wave;
-        const int i = it * 16 + l15;
-        const float hi = s_hi[now][i], lo = s_lo[now][i];
-        bf16x8 q[DK / 32];
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int ks = 0; ks < DK / 32; ++ks) q[ks] = *reinterpret_cast<const bf16x8*>(&s_q[tile_at<DK>(i, ks * 32 + 8 * g)]);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (2 * s > it) continue;
-          float w[8];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int jt = 2 * s + e, j0 = jt * 16 + 4 * g;
-            if (jt > it) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y) w[4 * e + y] = 0.f;
-              continue;
-            }
-            floatx4 d{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < DK / 32; ++ks)
-              d = mfma_bf16(*reinterpret_cast<const bf16x8*>(&s_k[tile_at<DK>(jt * 16 + l15, ks * 32 + 8 * g)]), q[ks], d);
-            const floatx4 jhi = *reinterpret_cast<const floatx4*>(&s_hi[now][j0]);
-            const floatx4 jlo = *reinterpret_cast<const floatx4*>(&s_lo[now][j0]);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float x = d[y] * (p.scale * exp2_of((hi - jhi[y]) + (lo - jlo[y])));
-              w[4 * e + y] = j0 + y <= i ? x : 0.f;
-            }
-          }
-          bf16x8 parts[NP];
-          parts_of<NP>(w, parts);
-#pragma unroll
-          for (int k = 0; k < NP; ++k) s_p[k][it][s][lane] = parts[k];
+        for (int c = 0; c < CT; ++c) {
+          const uint16_t* at = &s_v[tile_at<DV>(4 * g + (l15 >> 2), Sh::value(wave, c, 4 * (l15 & 3))) + 32 * s * DV];
+          v[s][c] = pair(read_tr(at), read_tr(at + 16 * DV));
         }
+    };
+    if (SUM) read_values();
+    if (!SUM) {
+      // Weights (q_i . k_j) e^{G_i - G_j}, 16 x 16 at a time, transposed (rows j, columns i). The ten
+      // tiles with j <= i go round the waves.
+#pragma unroll
+      for (int x = 0; x < (10 + NW - 1) / NW; ++x) {
+        int n = wave_s + x * NW;
+        if (n >= 10) break;
+        asm volatile("" : "+s"(n));  // keeps the tiles' LDS addresses out of registers between chunks
+        const int it = kTileI >> (2 * n) & 3, jt = kTileJ >> (2 * n) & 3;
+        floatx4 d{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < DK / 32; ++ks)
+          d = mfma_bf16(*reinterpret_cast<const bf16x8*>(&s_k[tile_at<DK>(l15, ks * 32 + 8 * g) + jt * 16 * DK]),
+                        *reinterpret_cast<const bf16x8*>(&s_q[tile_at<DK>(l15, ks * 32 + 8 * g) + it * 16 * DK]), d);
+        const int i = it * 16 + l15, j0 = jt * 16 + 4 * g;
+        const float hi = s_hi[now][i], lo = s_lo[now][i];
+        const floatx4 jhi = *reinterpret_cast<const floatx4*>(&s_hi[now][j0]);
+        const floatx4 jlo = *reinterpret_cast<const floatx4*>(&s_lo[now][j0]);
+        float w[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float z = d[y] * (p.scale * exp2_of((hi - jhi[y]) + (lo - jlo[y])));
+          w[y] = j0 + y <= i ? z : 0.f;
+        }
+        bf16x4 parts[NP];
+        parts_of<NP, 4>(w, parts);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) s_p[k][it][jt >> 1][lane][jt & 1] = parts[k];
       }
       // S^T q, while the other workgroup's waves are in front of their products as far as may be
       __builtin_amdgcn_s_setprio(1);
@@ -371,7 +409,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
         for (int c = 0; c < CT; ++c) {
           const float x[8] = {S[2 * ks][c][0],     S[2 * ks][c][1],     S[2 * ks][c][2],     S[2 * ks][c][3],
                               S[2 * ks + 1][c][0], S[2 * ks + 1][c][1], S[2 * ks + 1][c][2], S[2 * ks + 1][c][3]};
-          parts_of<NP>(x, sp[c]);
+          parts_of<NP, 8>(x, sp[c]);
         }
         bf16x8 q[4];
 #pragma unroll
@@ -391,21 +429,16 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
         for (int c = 0; c < CT; ++c) o[it][c] *= a;
       }
       lds_barrier();
+      read_values();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        bf16x8 v[CT];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const uint16_t* at = &s_v[tile_at<DV>(32 * s + 4 * g + (l15 >> 2), Sh::value(wave, c, 4 * (l15 & 3)))];
-          v[c] = pair(read_tr(at), read_tr(at + 16 * DV));
-        }
 #pragma unroll
         for (int k = 0; k < NP; ++k)
 #pragma unroll
           for (int it = 2 * s; it < 4; ++it) {
-            const bf16x8 w = s_p[k][it][s][lane];
+            const bf16x8 w = *reinterpret_cast<const bf16x8*>(&s_p[k][it][s][lane]);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) o[it][c] = mfma_bf16(v[c], w, o[it][c]);
+            for (int c = 0; c < CT; ++c) o[it][c] = mfma_bf16(v[s][c], w, o[it][c]);
           }
       }
 #pragma unroll
@@ -435,30 +468,34 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
       const floatx4 w1 = *reinterpret_cast<const floatx4*>(&s_w[now][32 * s + 16 + 4 * g]);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const uint16_t* at = &s_v[tile_at<DV>(32 * s + 4 * g + (l15 >> 2), Sh::value(wave, c, 4 * (l15 & 3)))];
-        const s16x4 a = read_tr(at), b = read_tr(at + 16 * DV);
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = bf16_bits_to_f32((uint16_t)a[i]) * w0[i];
-          x[4 + i] = bf16_bits_to_f32((uint16_t)b[i]) * w1[i];
-        }
-        parts_of<3>(x, vw[c]);
+        for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(v[s][c][i]) * (i < 4 ? w0[i] : w1[i - 4]);
+        parts_of<3, 8>(x, vw[c]);
       }
+      constexpr int kAtOnce = KT < 4 ? KT : 4;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const uint16_t* at = &s_k[tile_at<DK>(32 * s + 4 * g + (l15 >> 2), Sh::key(kt >> 1, kt & 1, 4 * (l15 & 3)))];
-        const bf16x8 k = pair(read_tr(at), read_tr(at + 16 * DK));
+      for (int k0 = 0; k0 < KT; k0 += kAtOnce) {
+        bf16x8 k[kAtOnce];
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+          const int kt = k0 + x;
+          const uint16_t* at =
+              &s_k[tile_at<DK>(4 * g + (l15 >> 2), Sh::key(kt >> 1, kt & 1, 4 * (l15 & 3))) + 32 * s * DK];
+          k[x] = pair(read_tr(at), read_tr(at + 16 * DK));
+        }
 #pragma unroll
         for (int y = 0; y < 3; ++y)
 #pragma unroll
-          for (int c = 0; c < CT; ++c) S[kt][c] = mfma_bf16(k, vw[c][y], S[kt][c]);
+          for (int x = 0; x < kAtOnce; ++x)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) S[k0 + x][c] = mfma_bf16(k[x], vw[c][y], S[k0 + x][c]);
       }
     }
   }
 
   if (SUM || (last && p.S_T)) {
-    if (t == 0) s_held = exp2_of((float)held);
+    if (t == kGates * 64) s_held = exp2_of((float)held);
     lds_barrier();
     const float f = s_held;
 #pragma unroll
@@ -471,7 +508,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int c = 0; c < CT; ++c) slots[((wave * KT + kt) * CT + c) * 64 + lane] = S[kt][c];
-    if (t == 0) decays_of(p)[(int64_t)job * p.H + h] = exp2_of((float)total);
+    if (t == kGates * 64) decays_of(p)[(int64_t)job * p.H + h] = exp2_of((float)total);
   } else if (last && p.S_T) {
     float* out = p.S_T + ((int64_t)j.n * p.H + h) * Sh::kState;
 #pragma unroll
@@ -522,7 +559,7 @@ __global__ __launch_bounds__(256) void lin_entries_kernel(const LinPlan p) {
   }
   floatx4* at = static_cast<floatx4*>(p.workspace) + i;
   const float* decays = decays_of(p);
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   for (int s0 = 0; s0 < there; s0 += kAhead) {
     floatx4 z[kAhead];
     float a[kAhead];
@@ -566,9 +603,6 @@ hipError_t launch_dk(const LinPlan& p, hipStream_t stream) {
   return p.dv == 32 ? launch<DK, 32>(p, stream) : p.dv == 64 ? launch<DK, 64>(p, stream) : launch<DK, 128>(p, stream);
 }
 
-// Two workgroups fit a CU: enough segments for 512 workgroups, of 256 tokens at least.
-constexpr int kWalks = 512, kShortest = 256;
-
 }  // namespace
 
 size_t plan_lin_chunk(LinPlan* p) {
@@ -577,11 +611,26 @@ size_t plan_lin_chunk(LinPlan* p) {
     p->jobs = p->n_seq;
     return 0;
   }
-  const int64_t tokens = p->cu_seqlens ? p->T : (int64_t)p->n_seq * p->T;
-  const int64_t want = (tokens * p->H + kWalks - 1) / kWalks;
-  p->seg = (int)std::min<int64_t>(std::max<int64_t>(kShortest, (want + kC - 1) / kC * kC), 1 << 30);
+  // Workgroups: two fit a CU and there are 256 CUs. With 256 pairs of sequence and head there are no
+  // segments (8 x 32 pairs of 8,448 tokens: 674 us, in two segments each 772: a segment's sum is work
+  // that the walk proper does again). Below, segments of 512 tokens or more for 512 workgroups (16 pairs of
+  // 16,384 tokens: 122 us, with 256 workgroups 138), shorter ones, of 128 at least, for 256, which are
+  // done sooner each (16 pairs of 4,096: 52 us, with 512 workgroups 57; 8 pairs of 1,024: 28 us in segments of 128,
+  // 38 of 256, 70 in one). Packed sequences, whose lengths the host does not know, are cut as if
+  // all tokens were one sequence.
+  const int64_t pairs = (int64_t)p->n_seq * p->H, tokens = p->cu_seqlens ? p->T : (int64_t)p->n_seq * p->T;
+  const auto cut = [&](int64_t groups) {
+    const int64_t len = p->cu_seqlens ? (tokens * p->H + groups - 1) / groups
+                                      : ((int64_t)p->T + std::max<int64_t>(1, groups / pairs) - 1) /
+                                            std::max<int64_t>(1, groups / pairs);
+    return std::min<int64_t>(std::max<int64_t>(128, (len + kC - 1) / kC * kC), 1 << 30);
+  };
+  int64_t seg = cut(256);
+  if (pairs < 256 && seg > 512) seg = std::max<int64_t>(512, cut(512));
+  if (p->T <= 256) seg = 256;
+  p->seg = (int)seg;
   const int64_t per = std::max<int64_t>(1, ((int64_t)p->T + p->seg - 1) / p->seg);
-  p->jobs = (int)(p->cu_seqlens ? p->T / p->seg + p->n_seq : per * p->n_seq);
+  p->jobs = (int)(p->cu_seqlens && p->T > p->seg ? p->T / p->seg + p->n_seq : per * p->n_seq);
   if (p->T <= p->seg) return 0;
   return sizeof(float) * (size_t)p->jobs * p->H * ((size_t)p->dk * p->dv + 1);
 }
