@@ -45,40 +45,77 @@ constexpr int kC = 64;          // tokens of a chunk
 constexpr unsigned kTileI = 0xffa94, kTileJ = 0xe4910;  // tiles (0, 0), (1, 0), (1, 1), (2, 0), ..., two bits each
 constexpr double kHeld = 24.0;  // most that a state may be off by in the accumulators, in powers of 2
 
-// Which segment of which sequence job `job` is: false if there is none.
+// What a workgroup walks: segment s of `segments` of sequence n, head h.
 struct Job {
-  int n, s, segments;
+  int n, s, segments, h;
+  int slot;        // segments of sequences before it, and of its own
   int64_t first;   // the sequence's first row
   int len;         // its tokens
 };
 __device__ __forceinline__ int segments_of(const LinPlan& p, int len) { return len ? (len - 1) / p.seg + 1 : 1; }
 
-__device__ __forceinline__ bool lin_job(const LinPlan& p, int job, Job* j) {
+// Sums over the lanes up to each.
+__device__ __forceinline__ int sums_to(int x) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d, 64);
+    if ((int)(threadIdx.x & 63) >= d) x += y;
+  }
+  return x;
+}
+
+// Workgroup b's: false if there is none.
+//
+// Workgroups b and b + 256 share a CU, where the earlier goes first. Up to 64 packed sequences are taken
+// by length: whole segments, then the sequences' last ones from long to short, and where no more than
+// 512 workgroups have work, the second half backwards, so that long ones share with short ones (512 pairs of
+// 994 .. 15,902 tokens: in the sequences' order from short to long 1.51 ms, so @@ ms). Where heads share
+// queries and keys, an XCD (b mod 8) takes neighbouring ones of a dense batch.
+__device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
   if (!p.cu_seqlens) {
+    const unsigned all = gridDim.x;
+    if (p.H != p.Hk && all % 8 == 0) b = b % 8 * (all / 8) + b / 8;
     j->segments = segments_of(p, p.T);
-    j->n = job / j->segments;
-    j->s = job % j->segments;
+    j->slot = b / p.H;
+    j->h = b % p.H;
+    j->n = j->slot / j->segments;
+    j->s = j->slot % j->segments;
     lin_tokens(p, j->n, &j->first, &j->len);
     return true;
   }
   const int lane = threadIdx.x & 63;
-  int before = 0;
-  if (p.T <= p.seg && p.n_seq <= 64) {  // one segment each: the longest sequences first
+  if (p.n_seq <= 64) {
     int64_t first;
-    int len = -1, above = 0;
-    if (lane < p.n_seq) lin_tokens(p, lane, &first, &len);
-    for (int m = 0; m < p.n_seq; ++m) {
-      const int x = __shfl(len, m, 64);
-      above += x > len || (x == len && m < lane);
+    int len = 0, x = 0;
+    if (lane < p.n_seq) {
+      lin_tokens(p, lane, &first, &len);
+      x = segments_of(p, len);
     }
-    const uint64_t which = __ballot(lane < p.n_seq && above == job);
+    const int to = sums_to(x);
+    const unsigned all = (unsigned)min((int64_t)__shfl(to, 63, 64) * p.H, (int64_t)gridDim.x);
+    if (b >= all) return false;
+    const unsigned place = b < 256 || all > 512 ? b : all - 1 - (b - 256);
+    const int k = place / p.H;
+    const int whole = sums_to(max(x - 1, 0)), wholes = __shfl(whole, 63, 64);
+    const int rest = lane < p.n_seq ? len - (x - 1) * p.seg : -1;
+    int above = 0;
+    for (int m = 0; m < p.n_seq; ++m) {
+      const int y = __shfl(rest, m, 64);
+      above += y > rest || (y == rest && m < lane);
+    }
+    const uint64_t which = k < wholes ? __ballot(whole > k) : __ballot(lane < p.n_seq && above == k - wholes);
     if (!which) return false;
-    j->n = __builtin_ctzll(which);
-    j->s = 0;
-    j->segments = 1;
-    lin_tokens(p, j->n, &j->first, &j->len);
-    return true;
+    const int l = __builtin_ctzll(which);
+    j->n = l;
+    j->segments = __shfl(x, l, 64);
+    j->s = k < wholes ? k - (__shfl(whole, l, 64) - (j->segments - 1)) : j->segments - 1;
+    j->slot = __shfl(to, l, 64) - j->segments + j->s;
+    j->h = place % p.H;
+    lin_tokens(p, l, &j->first, &j->len);
+    return j->slot < p.jobs;
   }
+  const int job = b / p.H;
+  int before = 0;
   for (int n0 = 0; n0 < p.n_seq; n0 += 64) {
     int64_t first;
     int len = 0, x = 0;
@@ -86,18 +123,15 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, int job, Job* j) {
       lin_tokens(p, n0 + lane, &first, &len);
       x = segments_of(p, len);
     }
-    int to = x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int y = __shfl_up(to, d, 64);
-      if (lane >= d) to += y;
-    }
+    const int to = sums_to(x);
     const uint64_t past = __ballot(before + to > job);
     if (past) {
       const int l = __builtin_ctzll(past);
       j->n = n0 + l;
-      j->s = job - before - __shfl(to - x, l, 64);
       j->segments = __shfl(x, l, 64);
+      j->s = job - before - (__shfl(to, l, 64) - j->segments);
+      j->slot = job;
+      j->h = b % p.H;
       lin_tokens(p, j->n, &j->first, &j->len);
       return true;
     }
@@ -122,15 +156,6 @@ template <int D>
 __device__ __forceinline__ int tile_at(int r, int c) {
   constexpr int kLog = D == 128 ? 0 : D == 64 ? 1 : 2;  // rows of 64 banks
   return r * D + ((((c >> 3) ^ ((r >> 2 & 3) | ((r & 3) >> kLog) << 2)) << 3) | (c & 7));
-}
-
-// Which (job, head), in this order, workgroup b takes. Workgroups b and b + 256 share a CU, where the
-// earlier goes first: of up to 512 in order of length, the second half goes backwards, so that long ones
-// share with short ones. Where heads share queries and keys, an XCD (b mod 8) takes neighbouring ones.
-__device__ __forceinline__ unsigned place_of(const LinPlan& p, unsigned b) {
-  const unsigned all = gridDim.x;
-  if (p.cu_seqlens && p.T <= p.seg && p.n_seq <= 64) return b < 256 || all > 512 ? b : all - 1 - (b - 256);
-  return p.H != p.Hk && all % 8 == 0 ? b % 8 * (all / 8) + b / 8 : b;
 }
 
 // Four 4 x 16 blocks of 16-bit values, one per 16 lanes, transposed on the way out of the LDS.
@@ -231,10 +256,9 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
   __shared__ __align__(16) float s_hi[2][kC], s_lo[2][kC], s_w[2][kC], s_e[2][kC];
   __shared__ float s_settle[2], s_held;
 
-  const unsigned at = place_of(p, blockIdx.x);
-  const int job = at / p.H, h = at % p.H, hk = h / (p.H / p.Hk);
   Job j;
-  if (!lin_job(p, job, &j)) return;
+  if (!lin_job(p, blockIdx.x, &j)) return;
+  const int h = j.h, hk = h / (p.H / p.Hk);
   if (SUM && j.s == j.segments - 1) return;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, l15 = lane & 15, g = lane >> 4;
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
@@ -244,7 +268,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
 
   // the state that enters
   floatx4 S[KT][CT];
-  const int64_t slot = slot_of<DK, DV>(p, job, h);
+  const int64_t slot = slot_of<DK, DV>(p, j.slot, h);
   floatx4* const slots = static_cast<floatx4*>(p.workspace) + slot;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
@@ -508,7 +532,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int c = 0; c < CT; ++c) slots[((wave * KT + kt) * CT + c) * 64 + lane] = S[kt][c];
-    if (t == kGates * 64) decays_of(p)[(int64_t)job * p.H + h] = exp2_of((float)total);
+    if (t == kGates * 64) decays_of(p)[(int64_t)j.slot * p.H + h] = exp2_of((float)total);
   } else if (last && p.S_T) {
     float* out = p.S_T + ((int64_t)j.n * p.H + h) * Sh::kState;
 #pragma unroll
