@@ -170,6 +170,7 @@ hipError_t launch_lin_recurrent(const LinPlan& p, hipStream_t stream);
 // Chooses seg and jobs, and returns the workspace bytes.
 size_t plan_lin_chunk(LinPlan* p);
 hipError_t launch_lin_chunk(const LinPlan& p, hipStream_t stream);
+hipError_t launch_lin_chunk_f32(const LinPlan& p, hipStream_t stream);  // fp32 activations
 
 struct PagePlan {
   int N, page_size, max_pages, max_tokens, cap;

@@ -31,122 +31,18 @@
 // differences after it nothing.
 #include <algorithm>
 
-#include "kda_lin.h"
+#include "kda_lin_chunk.h"
 
 namespace kda {
 
 namespace {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kC = 64;          // tokens of a chunk
 constexpr unsigned kTileI = 0xffa94, kTileJ = 0xe4910;  // tiles (0, 0), (1, 0), (1, 1), (2, 0), ..., two bits each
 constexpr double kHeld = 24.0;  // most that a state may be off by in the accumulators, in powers of 2
-
-// What a workgroup walks: segment s of `segments` of sequence n, head h.
-struct Job {
-  int n, s, segments, h;
-  int slot;        // segments of sequences before it, and of its own
-  int64_t first;   // the sequence's first row
-  int len;         // its tokens
-};
-__device__ __forceinline__ int segments_of(const LinPlan& p, int len) { return len ? (len - 1) / p.seg + 1 : 1; }
-
-// Sums over the lanes up to each.
-__device__ __forceinline__ int sums_to(int x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d, 64);
-    if ((int)(threadIdx.x & 63) >= d) x += y;
-  }
-  return x;
-}
-
-// Workgroup b's: false if there is none.
-//
-// Workgroups b and b + 256 share a CU, where the earlier goes first. Up to 64 packed sequences are taken
-// by length: whole segments, then the sequences' last ones from long to short, and where no more than
-// 512 workgroups have work, the second half backwards, so that long ones share with short ones (512 pairs of
-// 994 .. 15,902 tokens: in the sequences' order from short to long 1.51 ms, so @@ ms). Where heads share
-// queries and keys, an XCD (b mod 8) takes neighbouring ones of a dense batch.
-__device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
-  if (!p.cu_seqlens) {
-    const unsigned all = gridDim.x;
-    if (p.H != p.Hk && all % 8 == 0) b = b % 8 * (all / 8) + b / 8;
-    j->segments = segments_of(p, p.T);
-    j->slot = b / p.H;
-    j->h = b % p.H;
-    j->n = j->slot / j->segments;
-    j->s = j->slot % j->segments;
-    lin_tokens(p, j->n, &j->first, &j->len);
-    return true;
-  }
-  const int lane = threadIdx.x & 63;
-  if (p.n_seq <= 64) {
-    int64_t first;
-    int len = 0, x = 0;
-    if (lane < p.n_seq) {
-      lin_tokens(p, lane, &first, &len);
-      x = segments_of(p, len);
-    }
-    const int to = sums_to(x);
-    const unsigned all = (unsigned)min((int64_t)__shfl(to, 63, 64) * p.H, (int64_t)gridDim.x);
-    if (b >= all) return false;
-    const unsigned place = b < 256 || all > 512 ? b : all - 1 - (b - 256);
-    const int k = place / p.H;
-    const int whole = sums_to(max(x - 1, 0)), wholes = __shfl(whole, 63, 64);
-    const int rest = lane < p.n_seq ? len - (x - 1) * p.seg : -1;
-    int above = 0;
-    for (int m = 0; m < p.n_seq; ++m) {
-      const int y = __shfl(rest, m, 64);
-      above += y > rest || (y == rest && m < lane);
-    }
-    const uint64_t which = k < wholes ? __ballot(whole > k) : __ballot(lane < p.n_seq && above == k - wholes);
-    if (!which) return false;
-    const int l = __builtin_ctzll(which);
-    j->n = l;
-    j->segments = __shfl(x, l, 64);
-    j->s = k < wholes ? k - (__shfl(whole, l, 64) - (j->segments - 1)) : j->segments - 1;
-    j->slot = __shfl(to, l, 64) - j->segments + j->s;
-    j->h = place % p.H;
-    lin_tokens(p, l, &j->first, &j->len);
-    return j->slot < p.jobs;
-  }
-  const int job = b / p.H;
-  int before = 0;
-  for (int n0 = 0; n0 < p.n_seq; n0 += 64) {
-    int64_t first;
-    int len = 0, x = 0;
-    if (n0 + lane < p.n_seq) {
-      lin_tokens(p, n0 + lane, &first, &len);
-      x = segments_of(p, len);
-    }
-    const int to = sums_to(x);
-    const uint64_t past = __ballot(before + to > job);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      j->n = n0 + l;
-      j->segments = __shfl(x, l, 64);
-      j->s = job - before - (__shfl(to, l, 64) - j->segments);
-      j->slot = job;
-      j->h = b % p.H;
-      lin_tokens(p, j->n, &j->first, &j->len);
-      return true;
-    }
-    before += __shfl(to, 63, 64);
-  }
-  return false;
-}
-
-// A barrier that orders the LDS only: rows of the next chunk stay on their way across it, and so do
-// results. (__syncthreads waits for both: 14 us per chunk where this takes @@.)
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
 
 // Where channel c of row r lies in an LDS tile of rows of D. 16-byte pieces of a row change places with
 // the row, so that 16 lanes that read one piece of 16 rows, and 16 lanes that read a quarter of a
@@ -190,58 +86,16 @@ __device__ __forceinline__ void parts_of(const float* x, V* y) {
   }
 }
 
-// Sums over the lanes up to each.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double plus_lane(double x) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
-  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double lane_of(double x, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double wave_sums(double x) {
-  x = plus_lane<0x111, 0xf>(x);  // row_shr: 1, 2, 4, 8: within 16 lanes
-  x = plus_lane<0x112, 0xf>(x);
-  x = plus_lane<0x114, 0xf>(x);
-  x = plus_lane<0x118, 0xf>(x);
-  x = plus_lane<0x142, 0xa>(x);  // row_bcast: lane 15 to the next row, lane 31 to the upper half
-  return plus_lane<0x143, 0xc>(x);
-}
-
-__device__ __forceinline__ void store4(float* p, const floatx4& x) { *reinterpret_cast<floatx4*>(p) = x; }
-__device__ __forceinline__ void store4(uint16_t* p, const floatx4& x) {
-  s16x4 y;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = (short)lin_bf16(x[i]);
-  *reinterpret_cast<s16x4*>(p) = y;
-}
-
-__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
-
 template <int DK, int DV>
 struct Shape {
   static constexpr int kWaves = DV == 32 ? 2 : 4, kThreads = 64 * kWaves, kTiles = DV / 16 / kWaves;
-  static constexpr int kState = DK * DV;
+  static constexpr int kDK = DK, kDV = DV, kState = DK * DV;
   // Value channel of row r of a wave's tile c, and key channel of row r of a 32-channel block's tile e.
   static __device__ __forceinline__ int value(int wave, int c, int r) {
     return kTiles == 2 ? wave * 32 + 8 * (r >> 2) + 4 * c + (r & 3) : wave * 16 + r;
   }
   static __device__ __forceinline__ int key(int p, int e, int r) { return 32 * p + 8 * (r >> 2) + 4 * e + (r & 3); }
 };
-
-// A state in the workspace: [wave][key tile][value tile][lane] of four key rows each.
-template <int DK, int DV>
-__device__ __forceinline__ int64_t slot_of(const LinPlan& p, int64_t job, int h) {
-  return (job * p.H + h) * (DK * DV / 4);
-}
-__device__ __forceinline__ float* decays_of(const LinPlan& p) {
-  return static_cast<float*>(p.workspace) + (int64_t)p.jobs * p.H * p.dk * p.dv;
-}
 
 // PARTS: bf16 parts of states and weights in what becomes o; 0: sums of segments only.
 template <int DK, int DV, int PARTS, typename O>
@@ -268,7 +122,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
 
   // the state that enters
   floatx4 S[KT][CT];
-  const int64_t slot = slot_of<DK, DV>(p, j.slot, h);
+  const int64_t slot = slot_of<Sh>(p, j.slot, h);
   floatx4* const slots = static_cast<floatx4*>(p.workspace) + slot;
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
@@ -545,75 +399,13 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(
   }
 }
 
-// From the sums of a sequence's segments to the states that enter them, in the sums' place. A thread
-// takes four key rows of a value channel through all segments.
-template <int DK, int DV>
-__global__ __launch_bounds__(256) void lin_entries_kernel(const LinPlan p) {
-  using Sh = Shape<DK, DV>;
-  constexpr int CT = Sh::kTiles, KT = DK / 16;
-  constexpr int kGroups = (Sh::kState / 4 + 255) / 256;
-  const int part = blockIdx.x % kGroups, nh = blockIdx.x / kGroups, n = nh / p.H, h = nh % p.H;
-  const int i = part * 256 + threadIdx.x;
-  int64_t first;
-  int len, job = 0;
-  lin_tokens(p, n, &first, &len);
-  const int segments = segments_of(p, len);
-  if (segments == 1) return;
-  if (p.cu_seqlens) {
-    for (int m = threadIdx.x & 63; m < n; m += 64) {
-      int64_t f;
-      int l;
-      lin_tokens(p, m, &f, &l);
-      job += segments_of(p, l);
-    }
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) job += __shfl_xor(job, d, 64);
-  } else {
-    job = n * segments;
-  }
-  const int there = min(segments, p.jobs - job);  // offsets that overlap give more segments than jobs
-  if (i >= Sh::kState / 4) return;
-  floatx4 e{0.f, 0.f, 0.f, 0.f};
-  if (p.S0) {
-    const int lane = i % 64, tile = i / 64, c = tile % CT, kt = tile / CT % KT, wave = tile / CT / KT;
-    const float* in = p.S0 + (int64_t)nh * Sh::kState;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      e[x] = in[Sh::key(kt >> 1, kt & 1, 4 * (lane >> 4) + x) * DV + Sh::value(wave, c, lane & 15)];
-  }
-  floatx4* at = static_cast<floatx4*>(p.workspace) + i;
-  const float* decays = decays_of(p);
-  constexpr int kAhead = 16;
-  for (int s0 = 0; s0 < there; s0 += kAhead) {
-    floatx4 z[kAhead];
-    float a[kAhead];
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      z[s] = floatx4{0.f, 0.f, 0.f, 0.f};
-      a[s] = 1.f;
-      if (s0 + s < there && s0 + s + 1 < segments) {
-        z[s] = at[slot_of<DK, DV>(p, job + s0 + s, h)];
-        a[s] = decays[(int64_t)(job + s0 + s) * p.H + h];
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      if (s0 + s < there) {
-        at[slot_of<DK, DV>(p, job + s0 + s, h)] = e;
-        e = e * a[s] + z[s];
-      }
-    }
-  }
-}
-
 template <int DK, int DV>
 hipError_t launch(const LinPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.jobs * p.H));
   constexpr int threads = Shape<DK, DV>::kThreads;
   if (p.T > p.seg) {
     lin_walk_kernel<DK, DV, 0, float><<<grid, threads, 0, stream>>>(p);
-    constexpr int groups = (DK * DV / 4 + 255) / 256;
-    lin_entries_kernel<DK, DV><<<dim3((unsigned)((int64_t)p.n_seq * p.H * groups)), 256, 0, stream>>>(p);
+    launch_entries<Shape<DK, DV>>(p, stream);
   }
   if (p.out_bf16)
     lin_walk_kernel<DK, DV, 2, uint16_t><<<grid, threads, 0, stream>>>(p);
@@ -630,11 +422,6 @@ hipError_t launch_dk(const LinPlan& p, hipStream_t stream) {
 }  // namespace
 
 size_t plan_lin_chunk(LinPlan* p) {
-  if (!p->act_bf16) {
-    p->seg = std::max(p->T, 1);
-    p->jobs = p->n_seq;
-    return 0;
-  }
   // Workgroups: two fit a CU and there are 256 CUs. With 256 pairs of sequence and head there are no
   // segments (8 x 32 pairs of 8,448 tokens: 674 us, in two segments each 772: a segment's sum is work
   // that the walk proper does again). Below, segments of 512 tokens or more for 512 workgroups (16 pairs of
@@ -660,7 +447,7 @@ size_t plan_lin_chunk(LinPlan* p) {
 }
 
 hipError_t launch_lin_chunk(const LinPlan& p, hipStream_t stream) {
-  if (!p.act_bf16) return launch_lin_recurrent(p, stream);
+  if (!p.act_bf16) return launch_lin_chunk_f32(p, stream);
   return p.dk == 32 ? launch_dk<32>(p, stream) : p.dk == 64 ? launch_dk<64>(p, stream) : launch_dk<128>(p, stream);
 }
 
