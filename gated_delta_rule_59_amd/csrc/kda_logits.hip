@@ -5,11 +5,12 @@
 // values) and every result written once; the second read comes from the caches where the batch fits
 // them. HBM bounds a batch, the launches one row.
 //
-// A workgroup takes a block of kBlock tokens of one sequence, for all of its rows or for one. It first
-// writes down in LDS what the history holds of its tokens: a word per token, the number of times past
-// the prompt in 31 bits and in the top bit whether it is there at all; and of the biases the last
-// entry's number. Adding whole numbers and taking their maximum gives the same whatever the order, so
-// results are the same on every run. Row j's drafts are the first j: a row adds the one before it.
+// A workgroup takes a block of tokens of one sequence, for all of its rows or for one, and has the next
+// row's logits on their way while it works on this one's. It first writes down in LDS what the history
+// holds of its tokens: a word per token, the number of times past the prompt in 31 bits and in the top
+// bit whether it is there at all; and of the biases the last entry's number. Adding whole numbers and
+// taking their maximum gives the same whatever the order, so results are the same on every run. Row j's
+// drafts are the first j: a row adds the one before it.
 #include <algorithm>
 
 #include "kda_device.h"
@@ -19,79 +20,104 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256, kE = 4, kBlock = 4096, kSteps = kBlock / (kThreads * kE);
+constexpr int kThreads = 256, kE = 4;  // a thread takes kE neighbouring tokens at a time
 constexpr unsigned kThere = 0x80000000u;
 
 struct Stat {   // of a block of a row
   float top;    // largest value, NaN aside (-inf if there is none)
   float sum;    // of e^{x - top}; 0 if top is -inf, NaN if a value is
-  int at;       // first token that has it
+  int at;       // first token that has it (greedy rows only)
   int pad;
 };
 
 enum Mode { kAdjust, kStats, kProbs };
 
-// e^x for x <= 0 (below 2^-126: 0): the product with log2 e in two parts, so that its rounding stays
-// out of the exponent. (Far below, the first part would be infinite.)
-__device__ __forceinline__ float exp_of(float x) {
-  x = x < -150.f ? -150.f : x;
-  const float hi = x * kLog2e;
-  const float lo = fmaf(x, kLog2e, -hi) + x * 1.9259629911e-8f;
-  const float y = __builtin_amdgcn_exp2f(hi);
-  return fmaf(y, lo * 0.6931471805599453f, y);
+// e^{x - top} for values that are not above `top`. The product with log2 e is formed in two parts, so that
+// its error stays out of the exponent.
+__device__ __forceinline__ float exp_finite(float x, float top) {
+  const float d = x - top;
+  return __builtin_amdgcn_exp2f(fmaf(d, kLog2e, d * 1.9259629911e-8f));
 }
-// e^{x - top}, with infinite ones alike.
-__device__ __forceinline__ float exp_from(float x, float top) {
-  return x == top ? 1.f : top == INFINITY ? (x == x ? 0.f : x) : x == -INFINITY ? 0.f : exp_of(x - top);
+// top is +inf: infinite values share; -inf: there is nothing; NaN stays
+__device__ __forceinline__ float exp_infinite(float x) { return x != x ? x : x == INFINITY ? 1.f : 0.f; }
+__device__ __forceinline__ float exp_of(float x, float top) {
+  return fabsf(top) < INFINITY ? exp_finite(x, top) : exp_infinite(x);
+}
+// A value that all lanes have, as a scalar: choices by it are scalar ones.
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 
-// kE neighbouring values, whatever their alignment.
-__device__ __forceinline__ void load4(const float* p, float* x) {
-  typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
-  const vec y = *reinterpret_cast<const vec*>(p);
+// kE neighbouring values as they lie in memory, whatever their alignment, and as floats.
+template <typename T>
+struct Raw {
+  typedef T vec __attribute__((ext_vector_type(kE), aligned(sizeof(T))));
+  T x[kE];
+  __device__ __forceinline__ void load(const T* p) {
+    const vec y = *reinterpret_cast<const vec*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = y[i];
-}
-__device__ __forceinline__ void load4(const uint16_t* p, float* x) {
-  typedef uint16_t vec __attribute__((ext_vector_type(4), aligned(2)));
-  const vec y = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = bf16_bits_to_f32(y[i]);
-}
+    for (int i = 0; i < kE; ++i) x[i] = y[i];
+  }
+};
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(uint16_t x) { return bf16_bits_to_f32(x); }
+__device__ __forceinline__ void lowest(float* x) { *x = -INFINITY; }
+__device__ __forceinline__ void lowest(uint16_t* x) { *x = 0xff80; }
 __device__ __forceinline__ uint16_t to_bf16(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
 __device__ __forceinline__ void store4(float* p, const float* x) {
   typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
-  *reinterpret_cast<vec*>(p) = vec{x[0], x[1], x[2], x[3]};
+  __builtin_nontemporal_store(vec{x[0], x[1], x[2], x[3]}, reinterpret_cast<vec*>(p));
 }
 __device__ __forceinline__ void store4(uint16_t* p, const float* x) {
   typedef uint16_t vec __attribute__((ext_vector_type(4), aligned(2)));
-  *reinterpret_cast<vec*>(p) = vec{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])};
+  __builtin_nontemporal_store(vec{to_bf16(x[0]), to_bf16(x[1]), to_bf16(x[2]), to_bf16(x[3])},
+                              reinterpret_cast<vec*>(p));
 }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = to_bf16(x); }
 
-struct Row {  // what holds for all tokens of a sequence
-  float repetition, frequency, presence, temperature;
-  bool scaled, greedy;
-};
-
-// Two stats of the same row; equal maxima: the first token.
-__device__ __forceinline__ void join(Stat& a, float top, float sum, int at) {
-  if (top > a.top || (top == a.top && at < a.at)) a.at = at;
-  const float m = fmaxf(a.top, top);
-  a.sum = (a.sum == 0.f ? 0.f : a.sum * exp_from(a.top, m)) + (sum == 0.f ? 0.f : sum * exp_from(top, m));
-  a.top = m;
+// The larger of two, of equal ones the first token.
+__device__ __forceinline__ void larger(float& top, int& at, float y, int i) {
+  if (y > top || (y == top && i < at)) top = y, at = i;
 }
-__device__ __forceinline__ void join_lanes(Stat& s) {
+__device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1)
-    join(s, __shfl_xor(s.top, d, 64), __shfl_xor(s.sum, d, 64), __shfl_xor(s.at, d, 64));
+  for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
+  return x;
+}
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+  return x;
+}
+__device__ __forceinline__ int wave_min(int x) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) x = min(x, __shfl_xor(x, d, 64));
+  return x;
 }
 
-template <typename T, typename O, Mode MODE>
+// Every stat of a row in one, by one wave.
+__device__ __forceinline__ Stat join(const Stat* s, int n, bool greedy) {
+  const int lane = threadIdx.x & 63;
+  Stat mine{-INFINITY, 0.f, INT32_MAX, 0};
+  for (int i = lane; i < n; i += 64) {
+    const Stat x = s[i];
+    const float top = fmaxf(mine.top, x.top);
+    mine.sum = mine.sum * exp_of(mine.top, top) + x.sum * exp_of(x.top, top);
+    larger(mine.top, mine.at, x.top, x.at);
+  }
+  const float top = uniform(wave_max(mine.top));
+  Stat all{top, wave_sum(mine.sum * exp_of(mine.top, top)), INT32_MAX, 0};
+  if (greedy) all.at = wave_min(mine.top == top ? mine.at : INT32_MAX);
+  return all;
+}
+
+// STEPS: times kE tokens of each thread are a block.
+template <typename T, typename O, Mode MODE, int STEPS>
 __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, int blocks, int splits) {
-  extern __shared__ unsigned s_mem[];
-  __shared__ Stat s_stat[kThreads / 64];
+  constexpr int kBlock = STEPS * kThreads * kE;
+  extern __shared__ __align__(16) unsigned s_mem[];
+  __shared__ Stat s_stat[2][kThreads / 64];
   const int t = threadIdx.x;
   const unsigned item = blockIdx.x;  // (sequence, split of its rows, block)
   const int b = item % blocks, part = item / blocks % splits, n = item / blocks / splits;
@@ -101,25 +127,67 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   unsigned* const s_said = s_mem;
   unsigned* const s_bias = s_mem + (said ? kBlock : 0);
 
-  Row row;
-  row.repetition = p.repetition ? p.repetition[n] : 1.f;
-  row.frequency = p.frequency ? p.frequency[n] : 0.f;
-  row.presence = p.presence ? p.presence[n] : 0.f;
-  row.temperature = p.temperature ? p.temperature[n] : 1.f;
-  row.greedy = !(row.temperature > 0.f);
-  row.scaled = p.temperature && !row.greedy;
+  Raw<T> next[STEPS];
+  unsigned next_mask[STEPS];
+#pragma unroll
+  for (int c = 0; c < STEPS; ++c) next_mask[c] = ~0u;
+  auto fetch = [&](int j) {  // row j's block, tokens past the vocabulary as -inf
+    const T* in = static_cast<const T*>(p.logits) + n * p.seq + j * p.row + base;
+    const uint32_t* mask = p.mask + n * p.mask_seq + j * p.mask_row + base / 32;
+    if (here == kBlock) {
+#pragma unroll
+      for (int c = 0; c < STEPS; ++c) next[c].load(in + (c * kThreads + t) * kE);
+      if (p.mask) {
+#pragma unroll
+        for (int c = 0; c < STEPS; ++c) next_mask[c] = mask[(c * kThreads + t) * kE / 32];
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < STEPS; ++c) {
+        const int i = (c * kThreads + t) * kE;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          lowest(&next[c].x[e]);
+          if (i + e < here) next[c].x[e] = in[i + e];
+        }
+        if (p.mask && i < here) next_mask[c] = mask[i / 32];
+      }
+    }
+  };
+  fetch(j0);
+
+  const float repetition = p.repetition ? p.repetition[n] : 1.f;
+  const float frequency = p.frequency ? p.frequency[n] : 0.f;
+  const float presence = p.presence ? p.presence[n] : 0.f;
+  const float temperature = p.temperature ? p.temperature[n] : 1.f;
+  const bool greedy = !(temperature > 0.f);
+  // one over the temperature, where that is a normal number (2^-126 .. 2^126)
+  const bool scaled = !greedy && temperature != 1.f, inverse = temperature > 0x1p-126f && temperature < 0x1p126f;
+  const float scale = 1.f / temperature, once = 1.f / repetition;
 
   if (said || biased) {
-    for (int i = t; i < kBlock * ((said ? 1 : 0) + (biased ? 1 : 0)); i += kThreads) s_mem[i] = 0;
+    typedef unsigned vec __attribute__((ext_vector_type(4)));
+    for (int i = t; i < kBlock / 4 * ((said ? 1 : 0) + (biased ? 1 : 0)); i += kThreads)
+      reinterpret_cast<vec*>(s_mem)[i] = vec{0, 0, 0, 0};
     __syncthreads();
     if (p.history) {
       const int32_t* ids = p.history + n * p.history_stride;
       const int len = min(max(p.history_lens[n], 0), p.max_history);
       const int prompt = p.prompt_lens ? min(max(p.prompt_lens[n], 0), len) : 0;
-      for (int i = t; i < len; i += kThreads) {
-        const unsigned x = (unsigned)ids[i] - (unsigned)base;
+      auto count = [&](int i, int id) {
+        const unsigned x = (unsigned)id - (unsigned)base;
         if (x < (unsigned)here) {
           if (i < prompt) atomicOr(&s_said[x], kThere); else atomicAdd(&s_said[x], 1u);
+        }
+      };
+      typedef int ids4 __attribute__((ext_vector_type(4), aligned(4)));
+      for (int i = 4 * t; i < len; i += 4 * kThreads) {
+        if (i + 4 <= len) {
+          const ids4 x = *reinterpret_cast<const ids4*>(ids + i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) count(i + e, x[e]);
+        } else {
+          for (int e = i; e < len; ++e) count(e, ids[e]);
         }
       }
     }
@@ -149,89 +217,110 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
         __syncthreads();
       }
     }
-    const T* in = static_cast<const T*>(p.logits) + n * p.seq + j * p.row + base;
-    const uint32_t* mask = p.mask ? p.mask + n * p.mask_seq + j * p.mask_row + base / 32 : nullptr;
-    Stat whole{-INFINITY, 0.f, INT32_MAX, 0};
-    float scale = 0.f;
-    if (MODE == kProbs) {  // the row's maximum and sum out of its blocks'
-      const Stat* of = static_cast<const Stat*>(p.workspace) + ((int64_t)n * p.R + j) * blocks;
-      for (int i = t & 63; i < blocks; i += 64) {
-        const Stat x = of[i];
-        join(whole, x.top, x.sum, x.at);
-      }
-      join_lanes(whole);
-      scale = 1.f / whole.sum;
+    float x[STEPS][kE];
+    unsigned mask[STEPS];
+#pragma unroll
+    for (int c = 0; c < STEPS; ++c) {
+      mask[c] = next_mask[c];
+#pragma unroll
+      for (int e = 0; e < kE; ++e) x[c][e] = as_float(next[c].x[e]);
     }
-    float x[kSteps][kE];
+    if (j + 1 < j1) fetch(j + 1);
+    Stat row{0.f, 0.f, 0, 0};
+    if (MODE == kProbs)  // the row's maximum and sum out of its blocks'
+      row = join(static_cast<const Stat*>(p.workspace) + ((int64_t)n * p.R + j) * blocks, blocks, greedy);
 #pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
+    for (int c = 0; c < STEPS; ++c) {
       const int i = (c * kThreads + t) * kE;
-      if (i + kE <= here) {
-        load4(in + i, x[c]);
-      } else {
+      typedef unsigned vec __attribute__((ext_vector_type(4)));
+      if (said) {
+        const vec w = *reinterpret_cast<const vec*>(&s_said[i]);
+        if (w[0] | w[1] | w[2] | w[3]) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) x[c][e] = i + e < here ? ld(in, i + e) : -INFINITY;
+          for (int e = 0; e < kE; ++e) {
+            // no branches: with a history of thousands, some lane has such a token nearly every time
+            float y = x[c][e];
+            const unsigned times = w[e] & ~kThere;
+            y = w[e] ? y * (y > 0.f ? once : repetition) : y;
+            x[c][e] = times ? y - (frequency * (float)times + presence) : y;
+          }
+        }
       }
-    }
+      if (biased) {
+        const vec w = *reinterpret_cast<const vec*>(&s_bias[i]);
+        if (w[0] | w[1] | w[2] | w[3]) {
 #pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
-      const int i = (c * kThreads + t) * kE;
-      const unsigned allowed = mask && i < here ? mask[i / 32] >> (i % 32) : ~0u;
+          for (int e = 0; e < kE; ++e)
+            if (w[e]) x[c][e] += p.bias[(int64_t)n * p.max_bias + w[e] - 1];
+        }
+      }
+      if (p.mask) {
+        const unsigned allowed = mask[c] >> (i % 32);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        float y = x[c][e];
-        if (said) {
-          const unsigned w = s_said[i + e];
-          if (w) y = y > 0.f ? y / row.repetition : y * row.repetition;
-          // each operation rounded by itself
-          if (w & ~kThere)
-            y = __fsub_rn(y, __fadd_rn(__fmul_rn(row.frequency, (float)(w & ~kThere)), row.presence));
+        for (int e = 0; e < kE; ++e) x[c][e] = allowed & 1u << e ? x[c][e] : -INFINITY;
+      }
+      if (scaled) {
+        if (inverse) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) x[c][e] *= scale;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) x[c][e] /= temperature;
         }
-        if (biased) {
-          const unsigned w = s_bias[i + e];
-          if (w) y = __fadd_rn(y, p.bias[(int64_t)n * p.max_bias + w - 1]);
-        }
-        if (!(allowed >> e & 1)) y = -INFINITY;
-        if (row.scaled) y = y / row.temperature;
-        if (i + e >= here) y = -INFINITY;
-        x[c][e] = y;
       }
     }
     if (MODE == kStats) {
       Stat s{-INFINITY, 0.f, INT32_MAX, 0};
+      float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c)
+      for (int c = 0; c < STEPS; ++c)
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          if (x[c][e] > s.top) s.top = x[c][e], s.at = base + (c * kThreads + t) * kE + e;
-        }
+        for (int e = 0; e < kE; ++e) top = fmaxf(top, x[c][e]);
+      s.top = uniform(wave_max(top));
+      if (fabsf(s.top) < INFINITY) {
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c)
+        for (int c = 0; c < STEPS; ++c)
 #pragma unroll
-        for (int e = 0; e < kE; ++e) s.sum += x[c][e] == -INFINITY ? 0.f : exp_from(x[c][e], s.top);
-      join_lanes(s);
-      if ((t & 63) == 0) s_stat[t >> 6] = s;
-      __syncthreads();
-      if (t == 0) {
+          for (int e = 0; e < kE; ++e) s.sum += exp_finite(x[c][e], s.top);
+      } else {
 #pragma unroll
-        for (int w = 1; w < kThreads / 64; ++w) join(s, s_stat[w].top, s_stat[w].sum, s_stat[w].at);
-        static_cast<Stat*>(p.workspace)[((int64_t)n * p.R + j) * blocks + b] = s;
+        for (int c = 0; c < STEPS; ++c)
+#pragma unroll
+          for (int e = 0; e < kE; ++e) s.sum += exp_infinite(x[c][e]);
       }
+      s.sum = wave_sum(s.sum);
+      if (greedy) {
+#pragma unroll
+        for (int c = STEPS - 1; c >= 0; --c)
+#pragma unroll
+          for (int e = kE - 1; e >= 0; --e)
+            if (x[c][e] == s.top && s.top > -INFINITY) s.at = base + (c * kThreads + t) * kE + e;
+        s.at = wave_min(s.at);
+      }
+      // two rows' stats in turn, so that one barrier does
+      if ((t & 63) == 0) s_stat[j & 1][t >> 6] = s;
       __syncthreads();
+      if (t < 64) {
+        s = join(s_stat[j & 1], kThreads / 64, greedy);
+        if (t == 0) static_cast<Stat*>(p.workspace)[((int64_t)n * p.R + j) * blocks + b] = s;
+      }
       continue;
     }
     O* out = static_cast<O*>(p.out) + n * p.out_seq + j * p.out_row + base;
+    const float share = row.sum == 0.f ? 0.f : 1.f / row.sum;
 #pragma unroll
-    for (int c = 0; c < kSteps; ++c) {
+    for (int c = 0; c < STEPS; ++c) {
       const int i = (c * kThreads + t) * kE;
       if (MODE == kProbs) {
+        if (greedy) {
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float y = x[c][e];
-          if (row.greedy)
-            x[c][e] = base + i + e == whole.at ? 1.f : 0.f;
-          else
-            x[c][e] = whole.sum == 0.f ? 0.f : (y == -INFINITY ? 0.f : exp_from(y, whole.top)) * scale;
+          for (int e = 0; e < kE; ++e) x[c][e] = base + i + e == row.at ? 1.f : 0.f;
+        } else if (fabsf(row.top) < INFINITY) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) x[c][e] = exp_finite(x[c][e], row.top) * share;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) x[c][e] = exp_infinite(x[c][e]) * share;
         }
       }
       if (i + kE <= here) {
@@ -245,27 +334,39 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   }
 }
 
-template <typename T, typename O, Mode MODE>
+// Blocks of 1,024 tokens while that many fit the card's places at once, else of 4,096.
+int steps_of(int N, int R, int V) { return (int64_t)N * R * ((V + 1023) / 1024) <= 2048 ? 1 : 4; }
+int block_of(int N, int R, int V) { return steps_of(N, R, V) * kThreads * kE; }
+
+template <typename T, typename O, Mode MODE, int STEPS>
 hipError_t launch(const LogitsPlan& p, hipStream_t stream) {
+  constexpr int kBlock = STEPS * kThreads * kE;
   const int blocks = (p.V + kBlock - 1) / kBlock;
   // one row of a sequence to a workgroup while all rows' blocks fit the card's places at once
   const int splits = (int64_t)p.N * p.R * blocks <= 2048 ? p.R : 1;
   const size_t lds = sizeof(unsigned) * kBlock * ((p.history || p.drafts ? 1 : 0) + (p.bias_ids ? 1 : 0));
-  logits_kernel<T, O, MODE><<<dim3((unsigned)((int64_t)p.N * splits * blocks)), kThreads, lds, stream>>>(p, blocks, splits);
+  logits_kernel<T, O, MODE, STEPS>
+      <<<dim3((unsigned)((int64_t)p.N * splits * blocks)), kThreads, lds, stream>>>(p, blocks, splits);
   return hipGetLastError();
+}
+
+template <typename T, typename O, int STEPS>
+hipError_t launch_steps(const LogitsPlan& p, hipStream_t stream) {
+  if (!p.probs) return launch<T, O, kAdjust, STEPS>(p, stream);
+  const hipError_t e = launch<T, O, kStats, STEPS>(p, stream);
+  return e == hipSuccess ? launch<T, O, kProbs, STEPS>(p, stream) : e;
 }
 
 template <typename T, typename O>
 hipError_t launch_all(const LogitsPlan& p, hipStream_t stream) {
-  if (!p.probs) return launch<T, O, kAdjust>(p, stream);
-  const hipError_t e = launch<T, O, kStats>(p, stream);
-  return e == hipSuccess ? launch<T, O, kProbs>(p, stream) : e;
+  return steps_of(p.N, p.R, p.V) == 1 ? launch_steps<T, O, 1>(p, stream) : launch_steps<T, O, 4>(p, stream);
 }
 
 }  // namespace
 
 size_t logits_workspace_bytes(int N, int R, int V) {
-  return sizeof(Stat) * (size_t)N * R * ((V + kBlock - 1) / kBlock);
+  const int block = block_of(N, R, V);
+  return sizeof(Stat) * (size_t)N * R * (((int64_t)V + block - 1) / block);
 }
 
 hipError_t launch_logits(const LogitsPlan& p, hipStream_t stream) {
