@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 256, kE = 4;  // a thread takes kE neighbouring tokens at a time
 constexpr unsigned kThere = 0x80000000u;
 
-struct Stat {   // of a block of a row
+struct Stat {   // of a wave's part of a row
   float top;    // largest value, NaN aside (-inf if there is none)
   float sum;    // of e^{x - top}; 0 if top is -inf, NaN if a value is
   int at;       // first token that has it (greedy rows only)
@@ -43,11 +43,6 @@ __device__ __forceinline__ float exp_infinite(float x) { return x != x ? x : x =
 __device__ __forceinline__ float exp_of(float x, float top) {
   return fabsf(top) < INFINITY ? exp_finite(x, top) : exp_infinite(x);
 }
-// A value that all lanes have, as a scalar: choices by it are scalar ones.
-__device__ __forceinline__ float uniform(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
-}
-
 // kE neighbouring values as they lie in memory, whatever their alignment, and as floats.
 template <typename T>
 struct Raw {
@@ -80,33 +75,56 @@ __device__ __forceinline__ void store1(uint16_t* p, float x) { *p = to_bf16(x); 
 __device__ __forceinline__ void larger(float& top, int& at, float y, int i) {
   if (y > top || (y == top && i < at)) top = y, at = i;
 }
+// Another lane's value on the way up to lane 63 (16 lanes in four steps, then rows of 16 in two); `none`
+// where there is none.
+template <int STEP>
+__device__ __forceinline__ int lane_below(int none, int x) {
+  constexpr int kCtrl[] = {0x111, 0x112, 0x114, 0x118, 0x142, 0x143}, kRows[] = {0xf, 0xf, 0xf, 0xf, 0xa, 0xc};
+  return __builtin_amdgcn_update_dpp(none, x, kCtrl[STEP], kRows[STEP], 0xf, false);
+}
+template <int STEP>
+__device__ __forceinline__ float lane_below(float none, float x) {
+  return __builtin_bit_cast(float, lane_below<STEP>(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x)));
+}
+// Over the wave's lanes, as scalars.
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
-  return x;
+  x = fmaxf(x, lane_below<0>(-INFINITY, x));
+  x = fmaxf(x, lane_below<1>(-INFINITY, x));
+  x = fmaxf(x, lane_below<2>(-INFINITY, x));
+  x = fmaxf(x, lane_below<3>(-INFINITY, x));
+  x = fmaxf(x, lane_below<4>(-INFINITY, x));
+  x = fmaxf(x, lane_below<5>(-INFINITY, x));
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
-  return x;
+  x += lane_below<0>(0.f, x);
+  x += lane_below<1>(0.f, x);
+  x += lane_below<2>(0.f, x);
+  x += lane_below<3>(0.f, x);
+  x += lane_below<4>(0.f, x);
+  x += lane_below<5>(0.f, x);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
 }
 __device__ __forceinline__ int wave_min(int x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x = min(x, __shfl_xor(x, d, 64));
-  return x;
+  x = min(x, lane_below<0>(INT32_MAX, x));
+  x = min(x, lane_below<1>(INT32_MAX, x));
+  x = min(x, lane_below<2>(INT32_MAX, x));
+  x = min(x, lane_below<3>(INT32_MAX, x));
+  x = min(x, lane_below<4>(INT32_MAX, x));
+  x = min(x, lane_below<5>(INT32_MAX, x));
+  return __builtin_amdgcn_readlane(x, 63);
 }
 
-// Every stat of a row in one, by one wave.
-__device__ __forceinline__ Stat join(const Stat* s, int n, bool greedy) {
+// Every stat of a row in one, by one wave; `mine` is the lane's first.
+__device__ __forceinline__ Stat join(Stat mine, const Stat* s, int n, bool greedy) {
   const int lane = threadIdx.x & 63;
-  Stat mine{-INFINITY, 0.f, INT32_MAX, 0};
-  for (int i = lane; i < n; i += 64) {
+  for (int i = lane + 64; i < n; i += 64) {
     const Stat x = s[i];
     const float top = fmaxf(mine.top, x.top);
     mine.sum = mine.sum * exp_of(mine.top, top) + x.sum * exp_of(x.top, top);
     larger(mine.top, mine.at, x.top, x.at);
   }
-  const float top = uniform(wave_max(mine.top));
+  const float top = wave_max(mine.top);
   Stat all{top, wave_sum(mine.sum * exp_of(mine.top, top)), INT32_MAX, 0};
   if (greedy) all.at = wave_min(mine.top == top ? mine.at : INT32_MAX);
   return all;
@@ -117,7 +135,6 @@ template <typename T, typename O, Mode MODE, int STEPS>
 __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, int blocks, int splits) {
   constexpr int kBlock = STEPS * kThreads * kE;
   extern __shared__ __align__(16) unsigned s_mem[];
-  __shared__ Stat s_stat[2][kThreads / 64];
   const int t = threadIdx.x;
   const unsigned item = blockIdx.x;  // (sequence, split of its rows, block)
   const int b = item % blocks, part = item / blocks % splits, n = item / blocks / splits;
@@ -129,11 +146,17 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
 
   Raw<T> next[STEPS];
   unsigned next_mask[STEPS];
+  int next_draft = -1;
+  const int stats = blocks * (kThreads / 64);  // of a row: one per wave
+  Stat next_stat{-INFINITY, 0.f, INT32_MAX, 0};
 #pragma unroll
   for (int c = 0; c < STEPS; ++c) next_mask[c] = ~0u;
   auto fetch = [&](int j) {  // row j's block, tokens past the vocabulary as -inf
     const T* in = static_cast<const T*>(p.logits) + n * p.seq + j * p.row + base;
     const uint32_t* mask = p.mask + n * p.mask_seq + j * p.mask_row + base / 32;
+    if (p.drafts && j > 0) next_draft = p.drafts[(int64_t)n * (p.R - 1) + j - 1];
+    if (MODE == kProbs && (t & 63) < stats)
+      next_stat = static_cast<const Stat*>(p.workspace)[((int64_t)n * p.R + j) * stats + (t & 63)];
     if (here == kBlock) {
 #pragma unroll
       for (int c = 0; c < STEPS; ++c) next[c].load(in + (c * kThreads + t) * kE);
@@ -210,7 +233,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
 
   for (int j = j0; j < j1; ++j) {
     if (j > j0 && p.drafts) {
-      const unsigned x = (unsigned)p.drafts[(int64_t)n * (p.R - 1) + j - 1] - (unsigned)base;
+      const unsigned x = (unsigned)next_draft - (unsigned)base;
       if (x < (unsigned)here) {  // the same for all threads
         __syncthreads();
         if (t == 0) s_said[x] += 1;
@@ -225,10 +248,11 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
 #pragma unroll
       for (int e = 0; e < kE; ++e) x[c][e] = as_float(next[c].x[e]);
     }
+    const Stat mine = next_stat;
     if (j + 1 < j1) fetch(j + 1);
     Stat row{0.f, 0.f, 0, 0};
-    if (MODE == kProbs)  // the row's maximum and sum out of its blocks'
-      row = join(static_cast<const Stat*>(p.workspace) + ((int64_t)n * p.R + j) * blocks, blocks, greedy);
+    if (MODE == kProbs)  // the row's maximum and sum
+      row = join(mine, static_cast<const Stat*>(p.workspace) + ((int64_t)n * p.R + j) * stats, stats, greedy);
 #pragma unroll
     for (int c = 0; c < STEPS; ++c) {
       const int i = (c * kThreads + t) * kE;
@@ -276,7 +300,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
       for (int c = 0; c < STEPS; ++c)
 #pragma unroll
         for (int e = 0; e < kE; ++e) top = fmaxf(top, x[c][e]);
-      s.top = uniform(wave_max(top));
+      s.top = wave_max(top);
       if (fabsf(s.top) < INFINITY) {
 #pragma unroll
         for (int c = 0; c < STEPS; ++c)
@@ -297,13 +321,8 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
             if (x[c][e] == s.top && s.top > -INFINITY) s.at = base + (c * kThreads + t) * kE + e;
         s.at = wave_min(s.at);
       }
-      // two rows' stats in turn, so that one barrier does
-      if ((t & 63) == 0) s_stat[j & 1][t >> 6] = s;
-      __syncthreads();
-      if (t < 64) {
-        s = join(s_stat[j & 1], kThreads / 64, greedy);
-        if (t == 0) static_cast<Stat*>(p.workspace)[((int64_t)n * p.R + j) * blocks + b] = s;
-      }
+      if ((t & 63) == 0)
+        static_cast<Stat*>(p.workspace)[((int64_t)n * p.R + j) * stats + b * (kThreads / 64) + (t >> 6)] = s;
       continue;
     }
     O* out = static_cast<O*>(p.out) + n * p.out_seq + j * p.out_row + base;
@@ -366,7 +385,7 @@ hipError_t launch_all(const LogitsPlan& p, hipStream_t stream) {
 
 size_t logits_workspace_bytes(int N, int R, int V) {
   const int block = block_of(N, R, V);
-  return sizeof(Stat) * (size_t)N * R * (((int64_t)V + block - 1) / block);
+  return sizeof(Stat) * (kThreads / 64) * (size_t)N * R * (((int64_t)V + block - 1) / block);
 }
 
 hipError_t launch_logits(const LogitsPlan& p, hipStream_t stream) {
