@@ -6,11 +6,13 @@
 // them. HBM bounds a batch, the launches one row.
 //
 // A workgroup takes a block of tokens of one sequence, for all of its rows or for one, and has the next
-// row's logits on their way while it works on this one's. It first writes down in LDS what the history
-// holds of its tokens: a word per token, the number of times past the prompt in 31 bits and in the top
-// bit whether it is there at all; and of the biases the last entry's number. Adding whole numbers and
-// taking their maximum gives the same whatever the order, so results are the same on every run. Row j's
-// drafts are the first j: a row adds the one before it.
+// row's logits on their way while it works on this one's. It first counts in LDS what the history holds of
+// its tokens: a word per token, the number of times past the prompt in 31 bits and in the top bit
+// whether it is there at all; and of the biases it keeps the last entry's number. Adding whole numbers and
+// taking their maximum gives the same whatever the order, so results are the same on every run. Both make
+// one word per token that a row's tokens are looked up in: what is added to the logit, its lowest bit (2^-24
+// of it) taken for whether the repetition factor holds; 0 for most tokens. Row j's drafts are the first
+// j: a row counts the one before it.
 #include <algorithm>
 
 #include "kda_device.h"
@@ -141,9 +143,9 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   const int j0 = splits == 1 ? 0 : part, j1 = splits == 1 ? p.R : part + 1;
   const int base = b * kBlock, here = min(kBlock, p.V - base);
   const bool said = p.history || p.drafts, biased = p.bias_ids;
-  unsigned* const s_said = s_mem;
-  unsigned* const s_bias = s_mem + (said ? kBlock : 0);
-
+  unsigned* const s_add = s_mem;              // first the biases' numbers, then what is added
+  unsigned* const s_said = s_mem + kBlock;    // only if `said`
+  __shared__ int s_found;
   Raw<T> next[STEPS];
   unsigned next_mask[STEPS];
   int next_draft = -1;
@@ -188,10 +190,15 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   const bool scaled = !greedy && temperature != 1.f, inverse = temperature > 0x1p-126f && temperature < 0x1p126f;
   const float scale = 1.f / temperature, once = 1.f / repetition;
 
+  // What is added to a token that is `w` in the counts and has this bias, and whether it repeats.
+  auto add_of = [&](unsigned w, float bias) {
+    const unsigned times = w & ~kThere;
+    const float less = times ? frequency * (float)times + presence : 0.f;
+    return (__builtin_bit_cast(unsigned, bias - less) & ~1u) | (w ? 1u : 0u);
+  };
   if (said || biased) {
     typedef unsigned vec __attribute__((ext_vector_type(4)));
-    for (int i = t; i < kBlock / 4 * ((said ? 1 : 0) + (biased ? 1 : 0)); i += kThreads)
-      reinterpret_cast<vec*>(s_mem)[i] = vec{0, 0, 0, 0};
+    for (int i = t; i < kBlock / 4 * (said ? 2 : 1); i += kThreads) reinterpret_cast<vec*>(s_mem)[i] = vec{0, 0, 0, 0};
     __syncthreads();
     if (p.history) {
       const int32_t* ids = p.history + n * p.history_stride;
@@ -225,8 +232,18 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
       const int32_t* ids = p.bias_ids + (int64_t)n * p.max_bias;
       for (int i = t; i < count; i += kThreads) {
         const unsigned x = (unsigned)ids[i] - (unsigned)base;
-        if (x < (unsigned)here) atomicMax(&s_bias[x], (unsigned)i + 1);
+        if (x < (unsigned)here) atomicMax(&s_add[x], (unsigned)i + 1);
       }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < STEPS; ++c) {
+      const int i = (c * kThreads + t) * kE;
+      const vec w = said ? *reinterpret_cast<const vec*>(&s_said[i]) : vec{0, 0, 0, 0};
+      const vec b = *reinterpret_cast<const vec*>(&s_add[i]);
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (w[e] | b[e]) s_add[i + e] = add_of(w[e], b[e] ? p.bias[(int64_t)n * p.max_bias + b[e] - 1] : 0.f);
     }
     __syncthreads();
   }
@@ -236,7 +253,18 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
       const unsigned x = (unsigned)next_draft - (unsigned)base;
       if (x < (unsigned)here) {  // the same for all threads
         __syncthreads();
-        if (t == 0) s_said[x] += 1;
+        if (t == 0) s_found = 0;
+        __syncthreads();
+        if (biased) {
+          const int count = p.bias_counts ? min(max(p.bias_counts[n], 0), p.max_bias) : p.max_bias;
+          for (int i = t; i < count; i += kThreads)
+            if (p.bias_ids[(int64_t)n * p.max_bias + i] == next_draft) atomicMax(&s_found, i + 1);
+        }
+        __syncthreads();
+        if (t == 0) {
+          s_said[x] += 1;
+          s_add[x] = add_of(s_said[x], s_found ? p.bias[(int64_t)n * p.max_bias + s_found - 1] : 0.f);
+        }
         __syncthreads();
       }
     }
@@ -257,25 +285,14 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
     for (int c = 0; c < STEPS; ++c) {
       const int i = (c * kThreads + t) * kE;
       typedef unsigned vec __attribute__((ext_vector_type(4)));
-      if (said) {
-        const vec w = *reinterpret_cast<const vec*>(&s_said[i]);
+      if (said || biased) {
+        const vec w = *reinterpret_cast<const vec*>(&s_add[i]);
         if (w[0] | w[1] | w[2] | w[3]) {
 #pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            // no branches: with a history of thousands, some lane has such a token nearly every time
-            float y = x[c][e];
-            const unsigned times = w[e] & ~kThere;
-            y = w[e] ? y * (y > 0.f ? once : repetition) : y;
-            x[c][e] = times ? y - (frequency * (float)times + presence) : y;
+          for (int e = 0; e < kE; ++e) {  // no branches: with a history of thousands, some lane has such a token nearly every time
+            const float y = x[c][e], z = y * (y > 0.f ? once : repetition);
+            x[c][e] = (w[e] & 1u ? z : y) + __builtin_bit_cast(float, w[e] & ~1u);
           }
-        }
-      }
-      if (biased) {
-        const vec w = *reinterpret_cast<const vec*>(&s_bias[i]);
-        if (w[0] | w[1] | w[2] | w[3]) {
-#pragma unroll
-          for (int e = 0; e < kE; ++e)
-            if (w[e]) x[c][e] += p.bias[(int64_t)n * p.max_bias + w[e] - 1];
         }
       }
       if (p.mask) {
@@ -363,7 +380,7 @@ hipError_t launch(const LogitsPlan& p, hipStream_t stream) {
   const int blocks = (p.V + kBlock - 1) / kBlock;
   // one row of a sequence to a workgroup while all rows' blocks fit the card's places at once
   const int splits = (int64_t)p.N * p.R * blocks <= 2048 ? p.R : 1;
-  const size_t lds = sizeof(unsigned) * kBlock * ((p.history || p.drafts ? 1 : 0) + (p.bias_ids ? 1 : 0));
+  const size_t lds = sizeof(unsigned) * kBlock * (p.history || p.drafts ? 2 : p.bias_ids ? 1 : 0);
   logits_kernel<T, O, MODE, STEPS>
       <<<dim3((unsigned)((int64_t)p.N * splits * blocks)), kThreads, lds, stream>>>(p, blocks, splits);
   return hipGetLastError();

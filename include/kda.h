@@ -576,13 +576,13 @@ typedef struct {
 } kda_page_plan_args;
 
 /* Arguments of kda_adjust_logits: R rows of logits of each of N sequences, row j for the token after
- * j drafts (R = 1: plain decode; R = m + 1 beside kda_verify_drafts). For each row, in 32 bits and in
- * this order, x being the logit of token i:
+ * j drafts (R = 1: plain decode; R = m + 1 beside kda_verify_drafts). For each row, in 32 bits (to 2^-22
+ * of the largest of the terms) and in this order, x being the logit of token i:
  *   - if i is in the sequence's history or among its first j drafts: x = x / repetition[n] where x > 0,
  *     x * repetition[n] elsewhere.
- *   - if it is c > 0 times in the history past the prompt and among the first j drafts: x = x -
- *     (frequency[n] * c + presence[n]).
- *   - x = x + bias; of a token that is listed twice the last entry counts.
+ *   - x = x + (bias - less), where less = frequency[n] * c + presence[n] if i is c > 0 times in the
+ *     history past the prompt and among the first j drafts, else 0, and the bias is the last entry's that
+ *     lists i, else 0.
  *   - where the mask's bit i is 0, x = -infinity (whatever x was, NaN too).
  *   - x = x / temperature[n]. Temperatures that are not above 0 stand for the limit: x stays, and with
  *     KDA_LOGITS_PROBS the row is 1 at its largest x (the first of equal ones; NaN is never it) and
