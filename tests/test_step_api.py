@@ -70,6 +70,7 @@ LIN = [
 @pytest.mark.parametrize("change,status", LIN + [
     (dict(B=0), BAD_SHAPE), (dict(T=-1), BAD_SHAPE), (dict(o=None), NULL_PTR),
     (dict(cu_seqlens=at(9), N=3), BAD_SHAPE), (dict(B=1, cu_seqlens=at(9), N=0), BAD_SHAPE),
+    (dict(k_token_stride=1 << 25), BAD_SHAPE), (dict(v_token_stride=1 << 30), BAD_SHAPE),
     (dict(B=1 << 15, T=1 << 20), BAD_SHAPE), (dict(S0=at(4) + 4), BAD_SHAPE), (dict(S_T=at(6) + 8), BAD_SHAPE),
     (dict(o=at(4)), ALIAS), (dict(S_T=at(4) + 64), ALIAS), (dict(S_T=at(1)), ALIAS), (dict(S_T=at(5)), ALIAS),
     (dict(B=1, cu_seqlens=at(5), N=1), ALIAS)])
