@@ -165,6 +165,7 @@ struct LinPlan {
   int seg;                       // prompts: tokens of a segment
   int jobs;                      // segments there may be at most, of all sequences
   void* workspace;
+  size_t tables;                 // packed prompts of many sequences: where their table lies in it
 };
 hipError_t launch_lin_recurrent(const LinPlan& p, hipStream_t stream);
 // Chooses seg and jobs, and returns the workspace bytes.

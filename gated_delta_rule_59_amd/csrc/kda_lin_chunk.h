@@ -29,6 +29,43 @@ __device__ __forceinline__ int sums_to(int x) {
   return x;
 }
 
+// In the workspace behind the states and their decays, for more than 64 packed sequences: the segments of
+// the sequences before each, and of each segment its sequence and its number there (-1: there is none).
+// (A walk over the offsets in every workgroup, which 64 sequences take, would take longer than the work
+// for thousands.)
+__device__ __forceinline__ int* starts_of(const LinPlan& p) {
+  return reinterpret_cast<int*>(static_cast<char*>(p.workspace) + p.tables);
+}
+__device__ __forceinline__ int2* jobs_of(const LinPlan& p) {
+  return reinterpret_cast<int2*>(starts_of(p) + (p.n_seq + 1) / 2 * 2);
+}
+__global__ __launch_bounds__(1024) void lin_jobs_kernel(const LinPlan p) {
+  __shared__ int s_sum[16];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int64_t done = 0;
+  for (int n0 = 0; n0 < p.n_seq; n0 += 1024) {
+    const int n = n0 + t;
+    int64_t first;
+    int len = 0, x = 0;
+    if (n < p.n_seq) {
+      lin_tokens(p, n, &first, &len);
+      x = segments_of(p, len);
+    }
+    const int to = sums_to(x);
+    if (lane == 63) s_sum[wave] = to;
+    __syncthreads();
+    int64_t at = done + to - x;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) at += s_sum[w];
+      done += s_sum[w];
+    }
+    __syncthreads();
+    if (n < p.n_seq) starts_of(p)[n] = (int)min(at, (int64_t)p.jobs);  // offsets that overlap give more
+    for (int s = 0; s < x && at + s < p.jobs; ++s) jobs_of(p)[at + s] = int2{n, s};
+  }
+  for (int64_t i = done + t; i < p.jobs; i += 1024) jobs_of(p)[i] = int2{-1, 0};
+}
+
 // Workgroup b's: false if there is none.
 //
 // Workgroups b and b + 256 share a CU, where the earlier goes first. Up to 64 packed sequences are taken
@@ -79,30 +116,15 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
     lin_tokens(p, l, &j->first, &j->len);
     return j->slot < p.jobs;
   }
-  const int job = b / p.H;
-  int before = 0;
-  for (int n0 = 0; n0 < p.n_seq; n0 += 64) {
-    int64_t first;
-    int len = 0, x = 0;
-    if (n0 + lane < p.n_seq) {
-      lin_tokens(p, n0 + lane, &first, &len);
-      x = segments_of(p, len);
-    }
-    const int to = sums_to(x);
-    const uint64_t past = __ballot(before + to > job);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      j->n = n0 + l;
-      j->segments = __shfl(x, l, 64);
-      j->s = job - before - (__shfl(to, l, 64) - j->segments);
-      j->slot = job;
-      j->h = b % p.H;
-      lin_tokens(p, j->n, &j->first, &j->len);
-      return true;
-    }
-    before += __shfl(to, 63, 64);
-  }
-  return false;
+  const int2 which = jobs_of(p)[b / p.H];
+  if (which.x < 0) return false;
+  j->n = which.x;
+  j->s = which.y;
+  j->slot = b / p.H;
+  j->h = b % p.H;
+  lin_tokens(p, j->n, &j->first, &j->len);
+  j->segments = segments_of(p, j->len);
+  return true;
 }
 
 // A barrier that orders the LDS only: rows of the next chunk stay on their way across it, and so do
@@ -156,69 +178,79 @@ __device__ __forceinline__ float* decays_of(const LinPlan& p) {
 }
 
 // From the sums of a sequence's segments to the states that enter them, in the sums' place. A thread
-// takes four key rows of a value channel through all segments.
+// takes four key rows of a value channel through all segments, kAhead of them on their way at a time.
 template <typename Sh>
 __global__ __launch_bounds__(256) void lin_entries_kernel(const LinPlan p) {
-  constexpr int CT = Sh::kTiles, KT = Sh::kDK / 16;
+  constexpr int CT = Sh::kTiles, KT = Sh::kDK / 16, kAhead = 16;
   constexpr int kGroups = (Sh::kState / 4 + 255) / 256;
-  const int part = blockIdx.x % kGroups, nh = blockIdx.x / kGroups, n = nh / p.H, h = nh % p.H;
-  const int i = part * 256 + threadIdx.x;
-  int64_t first;
-  int len, job = 0;
-  lin_tokens(p, n, &first, &len);
-  const int segments = segments_of(p, len);
-  if (segments == 1) return;
-  if (p.cu_seqlens) {
-    for (int m = threadIdx.x & 63; m < n; m += 64) {
-      int64_t f;
-      int l;
-      lin_tokens(p, m, &f, &l);
-      job += segments_of(p, l);
-    }
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) job += __shfl_xor(job, d, 64);
-  } else {
-    job = n * segments;
-  }
-  const int there = min(segments, p.jobs - job);  // offsets that overlap give more segments than jobs
-  if (i >= Sh::kState / 4) return;
-  floatx4 e{0.f, 0.f, 0.f, 0.f};
-  if (p.S0) {
-    const int lane = i % 64, tile = i / 64, c = tile % CT, kt = tile / CT % KT, wave = tile / CT / KT;
-    const float* in = p.S0 + (int64_t)nh * Sh::kState;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      e[x] = in[Sh::key(kt >> 1, kt & 1, 4 * (lane >> 4) + x) * Sh::kDV + Sh::value(wave, c, lane & 15)];
-  }
-  floatx4* at = static_cast<floatx4*>(p.workspace) + i;
-  const float* decays = decays_of(p);
-  constexpr int kAhead = 16;
-  for (int s0 = 0; s0 < there; s0 += kAhead) {
-    floatx4 z[kAhead];
-    float a[kAhead];
-#pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      z[s] = floatx4{0.f, 0.f, 0.f, 0.f};
-      a[s] = 1.f;
-      if (s0 + s < there && s0 + s + 1 < segments) {
-        z[s] = at[slot_of<Sh>(p, job + s0 + s, h)];
-        a[s] = decays[(int64_t)(job + s0 + s) * p.H + h];
+  const int64_t items = (int64_t)p.n_seq * p.H * kGroups;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t nh = item / kGroups;
+    const int part = (int)(item % kGroups), n = (int)(nh / p.H), h = (int)(nh % p.H);
+    const int i = part * 256 + threadIdx.x;
+    int64_t first;
+    int len, job = 0;
+    lin_tokens(p, n, &first, &len);
+    const int segments = segments_of(p, len);
+    if (segments == 1) continue;
+    if (!p.cu_seqlens) {
+      job = n * segments;
+    } else if (p.n_seq > 64) {
+      job = starts_of(p)[n];
+    } else {
+      const int m = threadIdx.x & 63;
+      if (m < n) {
+        lin_tokens(p, m, &first, &len);
+        job = segments_of(p, len);
       }
-    }
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      if (s0 + s < there) {
-        at[slot_of<Sh>(p, job + s0 + s, h)] = e;
-        e = e * a[s] + z[s];
+      for (int d = 32; d >= 1; d >>= 1) job += __shfl_xor(job, d, 64);
+    }
+    const int there = min(segments, p.jobs - job);  // offsets that overlap give more segments than jobs
+    if (i >= Sh::kState / 4) continue;
+    floatx4 e{0.f, 0.f, 0.f, 0.f};
+    if (p.S0) {
+      const int lane = i % 64, tile = i / 64, c = tile % CT, kt = tile / CT % KT, wave = tile / CT / KT;
+      const float* in = p.S0 + nh * Sh::kState;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        e[x] = in[Sh::key(kt >> 1, kt & 1, 4 * (lane >> 4) + x) * Sh::kDV + Sh::value(wave, c, lane & 15)];
+    }
+    floatx4* at = static_cast<floatx4*>(p.workspace) + i;
+    const float* decays = decays_of(p);
+    for (int s0 = 0; s0 < there; s0 += kAhead) {
+      floatx4 z[kAhead];
+      float a[kAhead];
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        z[s] = floatx4{0.f, 0.f, 0.f, 0.f};
+        a[s] = 1.f;
+        if (s0 + s < there && s0 + s + 1 < segments) {
+          z[s] = at[slot_of<Sh>(p, job + s0 + s, h)];
+          a[s] = decays[(int64_t)(job + s0 + s) * p.H + h];
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        if (s0 + s < there) {
+          at[slot_of<Sh>(p, job + s0 + s, h)] = e;
+          e = e * a[s] + z[s];
+        }
       }
     }
   }
 }
 
-template <typename Sh>
-void launch_entries(const LinPlan& p, hipStream_t stream) {
+// What comes before the walks: the jobs' table, and with segments their sums (`sum` launches them) and
+// the states that enter them.
+template <typename Sh, typename Sum>
+void launch_before(const LinPlan& p, hipStream_t stream, Sum sum) {
+  if (p.cu_seqlens && p.n_seq > 64) lin_jobs_kernel<<<1, 1024, 0, stream>>>(p);
+  if (p.T <= p.seg) return;
+  sum();
   constexpr int groups = (Sh::kState / 4 + 255) / 256;
-  lin_entries_kernel<Sh><<<dim3((unsigned)((int64_t)p.n_seq * p.H * groups)), 256, 0, stream>>>(p);
+  const int64_t items = (int64_t)p.n_seq * p.H * groups;
+  lin_entries_kernel<Sh><<<dim3((unsigned)(items < (1 << 20) ? items : 1 << 20)), 256, 0, stream>>>(p);
 }
 
 }  // namespace

@@ -403,10 +403,7 @@ template <int DK, int DV>
 hipError_t launch(const LinPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.jobs * p.H));
   constexpr int threads = Shape<DK, DV>::kThreads;
-  if (p.T > p.seg) {
-    lin_walk_kernel<DK, DV, 0, float><<<grid, threads, 0, stream>>>(p);
-    launch_entries<Shape<DK, DV>>(p, stream);
-  }
+  launch_before<Shape<DK, DV>>(p, stream, [&] { lin_walk_kernel<DK, DV, 0, float><<<grid, threads, 0, stream>>>(p); });
   if (p.out_bf16)
     lin_walk_kernel<DK, DV, 2, uint16_t><<<grid, threads, 0, stream>>>(p);
   else
@@ -442,8 +439,10 @@ size_t plan_lin_chunk(LinPlan* p) {
   p->seg = (int)seg;
   const int64_t per = std::max<int64_t>(1, ((int64_t)p->T + p->seg - 1) / p->seg);
   p->jobs = (int)(p->cu_seqlens && p->T > p->seg ? p->T / p->seg + p->n_seq : per * p->n_seq);
-  if (p->T <= p->seg) return 0;
-  return sizeof(float) * (size_t)p->jobs * p->H * ((size_t)p->dk * p->dv + 1);
+  const size_t states = p->T > p->seg ? sizeof(float) * (size_t)p->jobs * p->H * ((size_t)p->dk * p->dv + 1) : 0;
+  if (!p->cu_seqlens || p->n_seq <= 64) return states;
+  p->tables = (states + 15) / 16 * 16;
+  return p->tables + sizeof(int) * (((size_t)p->n_seq + 1) / 2 * 2 + 2 * (size_t)p->jobs);
 }
 
 hipError_t launch_lin_chunk(const LinPlan& p, hipStream_t stream) {

@@ -466,6 +466,7 @@ kda_status kda_verify_drafts(const kda_verify_args* args, void* hip_stream);
  *   scale      finite.
  *   flags      0 or KDA_LIN_FIXED_DECAY.
  *
+ * States of more than 2^100 may become infinite in kda_lin_chunk_fwd before their formula does.
  * A value of q, k, v or g that is not finite reaches results of its own sequence and the heads that
  * read it only; in kda_lin_chunk_fwd, tokens up to 63 places before it too, in the decode calls
  * only its own token and later ones.

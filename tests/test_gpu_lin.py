@@ -109,6 +109,16 @@ def test_packed(lengths, first):
     prompt(x, lengths)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("N,most,long", [(65, 200, 0), (200, 40, 3000), (1100, 9, 700), (64, 150, 2600)])
+def test_many_packed(N, most, long, act):
+    """More sequences than lanes of a wave or threads of a workgroup, empty ones and a long one among them."""
+    print(f"lin packed {N} of up to {most} and {long} {act}", flush=True)
+    lengths = [int(x) for x in np.random.default_rng((12, N)).integers(0, most + 1, N)]
+    lengths[N // 2] = max(lengths[N // 2], long)
+    prompt(make((13, N), sum(lengths), 1, 2, 32, 32, N, act), lengths, act=act)
+
+
 @pytest.mark.parametrize("fixed,gate", [(True, "f32"), (True, "bf16"), (False, "bf16")])
 def test_decay_forms(fixed, gate):
     prompt(make((5, fixed), 500, 3, 6, 32, 64, 1, gate=gate, fixed=fixed), gate=gate)
