@@ -128,7 +128,7 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
 }
 
 // A barrier that orders the LDS only: rows of the next chunk stay on their way across it, and so do
-// results. (__syncthreads waits for both: 14 us per chunk where this takes @@.)
+// results. (__syncthreads waits for both: 14 us per chunk where this takes 10.)
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
