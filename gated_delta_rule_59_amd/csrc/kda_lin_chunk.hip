@@ -99,7 +99,7 @@ struct Shape {
 
 // PARTS: bf16 parts of states and weights in what becomes o; 0: sums of segments only.
 template <int DK, int DV, int PARTS, typename O>
-__global__ __launch_bounds__((Shape<DK, DV>::kThreads), 2) void lin_walk_kernel(const LinPlan p) {
+__global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ? 1 : 2)) void lin_walk_kernel(const LinPlan p) {
   using Sh = Shape<DK, DV>;
   constexpr bool SUM = PARTS == 0;
   constexpr int NP = SUM ? 1 : PARTS;

@@ -10,7 +10,7 @@
 // its tokens: a word per token, the number of times past the prompt in 31 bits and in the top bit
 // whether it is there at all; and of the biases it keeps the last entry's number. Adding whole numbers and
 // taking their maximum gives the same whatever the order, so results are the same on every run. Both make
-// one word per token that a row's tokens are looked up in: what is added to the logit, its lowest bit (2^-24
+// one word per token that a row's tokens are looked up in: what is added to the logit, its lowest bit (2^-23
 // of it) taken for whether the repetition factor holds; 0 for most tokens. Row j's drafts are the first
 // j: a row counts the one before it.
 #include <algorithm>
@@ -34,11 +34,9 @@ struct Stat {   // of a wave's part of a row
 
 enum Mode { kAdjust, kStats, kProbs };
 
-// e^{x - top} for values that are not above `top`. The product with log2 e is formed in two parts, so that
-// its error stays out of the exponent.
+// e^{x - top} for values that are not above `top`: off by 2^-22 |x - top| relative, nothing at the top.
 __device__ __forceinline__ float exp_finite(float x, float top) {
-  const float d = x - top;
-  return __builtin_amdgcn_exp2f(fmaf(d, kLog2e, d * 1.9259629911e-8f));
+  return __builtin_amdgcn_exp2f((x - top) * kLog2e);
 }
 // top is +inf: infinite values share; -inf: there is nothing; NaN stays
 __device__ __forceinline__ float exp_infinite(float x) { return x != x ? x : x == INFINITY ? 1.f : 0.f; }
@@ -47,19 +45,42 @@ __device__ __forceinline__ float exp_of(float x, float top) {
 }
 // kE neighbouring values as they lie in memory, whatever their alignment, and as floats.
 template <typename T>
-struct Raw {
-  typedef T vec __attribute__((ext_vector_type(kE), aligned(sizeof(T))));
-  T x[kE];
-  __device__ __forceinline__ void load(const T* p) {
+struct Raw;
+template <>
+struct Raw<float> {
+  float x[kE];
+  __device__ __forceinline__ void load(const float* p) {
+    typedef float vec __attribute__((ext_vector_type(kE), aligned(4)));
     const vec y = *reinterpret_cast<const vec*>(p);
 #pragma unroll
     for (int i = 0; i < kE; ++i) x[i] = y[i];
   }
+  __device__ __forceinline__ void put(int i, const float* p) { x[i] = p ? *p : -INFINITY; }
+  __device__ __forceinline__ float at(int i) const { return x[i]; }
 };
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(uint16_t x) { return bf16_bits_to_f32(x); }
-__device__ __forceinline__ void lowest(float* x) { *x = -INFINITY; }
-__device__ __forceinline__ void lowest(uint16_t* x) { *x = 0xff80; }
+template <>
+struct Raw<uint16_t> {
+  unsigned x[kE / 2];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    typedef unsigned vec __attribute__((ext_vector_type(kE / 2), aligned(2)));
+    const vec y = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int i = 0; i < kE / 2; ++i) x[i] = y[i];
+  }
+  __device__ __forceinline__ void put(int i, const uint16_t* p) {
+    const unsigned y = p ? *p : 0xff80u;
+    x[i / 2] = i % 2 ? (x[i / 2] & 0xffffu) | y << 16 : y;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i % 2 ? x[i / 2] & 0xffff0000u : x[i / 2] << 16);
+  }
+};
+// Where the bits of m are 1 those of a, else b's.
+__device__ __forceinline__ float choose(unsigned m, float a, float b) {
+  return __uint_as_float((m & __float_as_uint(a)) | (~m & __float_as_uint(b)));
+}
+// Bit i of x in every bit.
+__device__ __forceinline__ unsigned bit(unsigned x, int i) { return (unsigned)__builtin_amdgcn_sbfe((int)x, i, 1); }
 __device__ __forceinline__ uint16_t to_bf16(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
 __device__ __forceinline__ void store4(float* p, const float* x) {
   typedef float vec __attribute__((ext_vector_type(4), aligned(4)));
@@ -171,10 +192,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
       for (int c = 0; c < STEPS; ++c) {
         const int i = (c * kThreads + t) * kE;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          lowest(&next[c].x[e]);
-          if (i + e < here) next[c].x[e] = in[i + e];
-        }
+        for (int e = 0; e < kE; ++e) next[c].put(e, i + e < here ? in + i + e : nullptr);
         if (p.mask && i < here) next_mask[c] = mask[i / 32];
       }
     }
@@ -274,7 +292,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
     for (int c = 0; c < STEPS; ++c) {
       mask[c] = next_mask[c];
 #pragma unroll
-      for (int e = 0; e < kE; ++e) x[c][e] = as_float(next[c].x[e]);
+      for (int e = 0; e < kE; ++e) x[c][e] = next[c].at(e);
     }
     const Stat mine = next_stat;
     if (j + 1 < j1) fetch(j + 1);
@@ -289,16 +307,17 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
         const vec w = *reinterpret_cast<const vec*>(&s_add[i]);
         if (w[0] | w[1] | w[2] | w[3]) {
 #pragma unroll
-          for (int e = 0; e < kE; ++e) {  // no branches: with a history of thousands, some lane has such a token nearly every time
-            const float y = x[c][e], z = y * (y > 0.f ? once : repetition);
-            x[c][e] = (w[e] & 1u ? z : y) + __builtin_bit_cast(float, w[e] & ~1u);
+          for (int e = 0; e < kE; ++e) {
+            // no branches: with a history of thousands, some lane has such a token nearly every time
+            const float y = x[c][e], z = y * choose(bit(__float_as_uint(y), 31), repetition, once);
+            x[c][e] = choose(bit(w[e], 0), z, y) + __uint_as_float(w[e]);
           }
         }
       }
       if (p.mask) {
         const unsigned allowed = mask[c] >> (i % 32);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) x[c][e] = allowed & 1u << e ? x[c][e] : -INFINITY;
+        for (int e = 0; e < kE; ++e) x[c][e] = choose(bit(allowed, e), x[c][e], -INFINITY);
       }
       if (scaled) {
         if (inverse) {

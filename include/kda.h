@@ -601,7 +601,7 @@ typedef struct {
  *              NULL: 0) are its prompt. NULL: none. Ids outside [0, V) are no token's.
  *   drafts     int32 [N, R - 1], or NULL: none count.
  *   repetition, frequency, presence
- *              fp32 [N] each, or NULL for 1, 0, 0.
+ *              fp32 [N] each, or NULL for 1, 0, 0. repetition within 2^-126 .. 2^126.
  *   bias_ids, bias
  *              int32 and fp32 [N, max_bias], of which the first bias_counts[n] (device int32 [N] or
  *              NULL: all; taken as within [0, max_bias]) count. NULL: none.
