@@ -212,7 +212,10 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   auto add_of = [&](unsigned w, float bias) {
     const unsigned times = w & ~kThere;
     const float less = times ? frequency * (float)times + presence : 0.f;
-    return (__builtin_bit_cast(unsigned, bias - less) & ~1u) | (w ? 1u : 0u);
+    const float add = bias - less;
+    const unsigned bits = __builtin_bit_cast(unsigned, add);
+    // beside an infinite one the factor makes no difference, and its bit would make it a NaN
+    return fabsf(add) < INFINITY ? (bits & ~1u) | (w ? 1u : 0u) : bits;
   };
   if (said || biased) {
     typedef unsigned vec __attribute__((ext_vector_type(4)));

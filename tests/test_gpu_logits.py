@@ -53,7 +53,7 @@ def size_of(x, kw):
     r, most = one("repetition", 1.0), float(kw["history"].shape[1] if "history" in kw else 0) + x.shape[1]
     s = np.where(np.isfinite(x), np.abs(x), 0).max((1, 2)) * np.maximum(r, 1 / np.maximum(r, 1e-9))
     s = s + one("frequency", 0.0) * most + one("presence", 0.0)
-    s = s + (np.abs(kw["bias"]).max(1) if "bias" in kw else 0.0)
+    s = s + (np.where(np.isfinite(kw["bias"]), np.abs(kw["bias"]), 0).max(1) if "bias" in kw else 0.0)
     t = one("temperature", 1.0)
     return (s / np.where(t > 0, t, 1.0))[:, None, None]
 
@@ -170,6 +170,23 @@ def test_extreme_temperatures():
     x, kw = make((87, 1), 4, 1, 3000, act="f32")
     kw["temperature"][:] = [1e-3, 1e4, 1e-30, 1e30]
     check(x, kw, act="f32")
+
+
+def test_infinite_biases():
+    """A bias that bans or forces a token holds for tokens of the history and drafts too."""
+    x, kw = make((89, 1), 4, 3, 5000, biases=6)
+    kw["bias_ids"][:] = np.arange(6) * 3
+    kw["bias"][:, ::2] = -np.inf
+    kw["bias"][3, 1] = np.inf
+    kw["bias_counts"][:] = 6
+    kw["history"][0, :6] = np.arange(6) * 3
+    kw["history"][3, 5] = 3
+    kw["history_lens"][:] = 40
+    kw["prompt_lens"][:] = [0, 40, 20, 3]
+    kw["drafts"][1] = [6, 12]
+    kw["mask"][:, :, 0] = -1
+    _, p = check(x, kw)
+    assert (p[:, :, [0, 6, 12]] == 0).all() and (p[3, :, 3] == 1).all()
 
 
 def test_in_place_and_strided():
