@@ -14,6 +14,7 @@
 // of it) taken for whether the repetition factor holds; 0 for most tokens. Row j's drafts are the first
 // j: a row counts the one before it.
 #include <algorithm>
+#include <cfloat>
 
 #include "kda_device.h"
 #include "kda_internal.h"
@@ -202,7 +203,8 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   const float repetition = p.repetition ? p.repetition[n] : 1.f;
   const float frequency = p.frequency ? p.frequency[n] : 0.f;
   const float presence = p.presence ? p.presence[n] : 0.f;
-  const float temperature = p.temperature ? p.temperature[n] : 1.f;
+  // an infinite one would make what is masked (and the end of the last block) a NaN
+  const float heat = p.temperature ? p.temperature[n] : 1.f, temperature = heat == INFINITY ? FLT_MAX : heat;
   const bool greedy = !(temperature > 0.f);
   // one over the temperature, where that is a normal number (2^-126 .. 2^126)
   const bool scaled = !greedy && temperature != 1.f, inverse = temperature > 0x1p-126f && temperature < 0x1p126f;

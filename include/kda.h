@@ -587,7 +587,7 @@ typedef struct {
  *   - where the mask's bit i is 0, x = -infinity (whatever x was, NaN too).
  *   - x = x / temperature[n]. Temperatures that are not above 0 stand for the limit: x stays, and with
  *     KDA_LOGITS_PROBS the row is 1 at its largest x (the first of equal ones; NaN is never it) and
- *     0 elsewhere.
+ *     0 elsewhere. +infinity is taken as the largest finite number.
  *   - with KDA_LOGITS_PROBS softmax over the row: 0 everywhere if every x is -infinity; infinite ones
  *     share the row evenly; a NaN makes the row NaN.
  *

@@ -189,6 +189,18 @@ def test_infinite_biases():
     assert (p[:, :, [0, 6, 12]] == 0).all() and (p[3, :, 3] == 1).all()
 
 
+def test_infinite_temperatures():
+    """What is allowed shares the row evenly; what is masked, and the end of the last block, stay out."""
+    x, kw = make((90, 1), 3, 2, 5000)
+    kw["temperature"][:] = np.inf
+    kw["mask"][0] = -1
+    p = run(x, kw, probs=True).double().cpu().numpy()
+    y = run(x, kw).double().cpu().numpy()
+    on = (kw["mask"].view(np.uint32)[:, :, np.arange(5000) // 32] >> (np.arange(5000) % 32)) & 1 == 1
+    assert (p[~on] == 0).all() and (y[~on] == -np.inf).all() and (np.abs(y[on]) < 1e-35).all()
+    assert (np.abs(p * on.sum(-1, keepdims=True) - 1)[on] <= 2.0 ** -20).all()
+
+
 def test_in_place_and_strided():
     import torch
     from gated_delta_rule_59_amd import binding
