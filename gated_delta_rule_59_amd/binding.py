@@ -551,8 +551,8 @@ def page_plan(block_table, held, lens, new_lens, free_pages, ring, *, page_size,
     place; held [N]: pages of each sequence; lens [N]: its tokens that stand (`start` of kv_append);
     new_lens [N]: its tokens of this step, below 0 where it has ended and gives its pages back; ring [2]:
     head and number of the free pages. Returns (held, ring, both after the call; seq_lens [N];
-    cu_seqlens [N + 1]; slots [max_tokens]; positions [max_tokens]), in new tensors where none are
-    given. A sequence that the pages or max_tokens do not suffice for gets no tokens in this step (see
+    cu_seqlens [N + 1]; slots [max_tokens]; positions [max_tokens]), in new tensors (parts of one
+    allocation) where none are given. A sequence that the pages or max_tokens do not suffice for gets no tokens in this step (see
     kda_page_plan_args)."""
     return (_ops or _marshal()).page_plan(block_table, held, lens, new_lens, free_pages, ring, page_size,
                                           max_tokens, held_out, ring_out, seq_lens, cu_seqlens, slots,

@@ -151,7 +151,7 @@ def calls():
     table, held, lens, fresh, free, ring, page = make_plan((112, 1), 40, 16, 300, 6, 3)
     i32 = lambda x: torch.from_numpy(np.array(x, np.int64).astype(np.int32)).cuda()  # noqa: E731
     dp = [i32(x) for x in (table, held, lens, fresh, free, ring)]
-    yield "page_plan", 6, lambda **kw: binding.page_plan(*dp, page_size=page, max_tokens=400, **kw)
+    yield "page_plan", 1, lambda **kw: binding.page_plan(*dp, page_size=page, max_tokens=400, **kw)
     x, kw0 = make_logits((113, 1), 4, 3, 9000)
     dl = {a: torch.from_numpy(b).cuda() for a, b in kw0.items()}
     lx = torch.from_numpy(x).bfloat16().cuda()
