@@ -118,24 +118,28 @@ at::ScalarType out_type(Opt given, PyObject* dtype) {
   return t;
 }
 
-// Token and head strides of a [lead0, lead1, heads, d] view whose tokens lie evenly apart.
+// Token and head strides of a [lead0, lead1, heads, d] view whose tokens lie evenly apart, or of a [lead0,
+// heads, d] one (dim 3).
 void heads(const On& on, const char* name, const at::Tensor& t, at::ScalarType type, int64_t lead0,
-           int64_t lead1, int64_t d, int64_t* token, int64_t* head) {
+           int64_t lead1, int64_t d, int64_t* token, int64_t* head, int dim = 4) {
   on.also(name, &t);
   of_type(name, t, type);
-  if (t.dim() != 4 || t.size(0) != lead0 || t.size(1) != lead1 || t.size(3) != d)
+  if (t.dim() != dim || t.size(0) != lead0 || (dim == 4 && t.size(1) != lead1) || t.size(dim - 1) != d) {
+    if (dim == 3) value_error("%s must be of shape [%lld, heads, %lld]", name, (long long)lead0, (long long)d);
     value_error("%s must be of shape [%lld, %lld, heads, %lld]", name, (long long)lead0,
                             (long long)lead1, (long long)d);
-  const int64_t H = t.size(2);
+  }
+  if (dim == 3) lead1 = 1;
+  const int64_t H = t.size(dim - 2);
   *token = H * d;
   *head = d;
   if (t.numel() == 0) return;
   const auto s = t.strides();
-  if ((s[3] != 1 && d > 1) || (lead0 > 1 && lead1 > 1 && s[0] != lead1 * s[1]))
+  if ((s[dim - 1] != 1 && d > 1) || (lead0 > 1 && lead1 > 1 && s[0] != lead1 * s[1]))
     value_error("%s must have contiguous channels and evenly spaced tokens", name);
   if (lead1 > 1) *token = s[1];
   else if (lead0 > 1) *token = s[0];
-  if (H > 1) *head = s[2];
+  if (H > 1) *head = s[dim - 2];
 }
 
 void page_cache(const On& on, const at::Tensor& k, const at::Tensor& v, const at::Tensor& table, Opt k_scale,
@@ -388,21 +392,24 @@ PyObject* paged_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 // Heads, dims, types, strides and decays of linear attention: q, k [lead0, lead1, Hk, dk], v [lead0, lead1,
-// H, dv], g [lead0, lead1, H] or [H].
+// H, dv], g [lead0, lead1, H] or [H]; or all of one token, without lead1.
 template <typename Args>
 void linear(const On& on, const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, const at::Tensor& g,
             PyObject* scale, Args* a) {
-  const int64_t lead0 = q.size(0), lead1 = q.size(1), dk = q.size(3), H = v.size(2), dv = v.size(3);
+  const int dim = (int)q.dim();
+  const int64_t lead0 = q.size(0), lead1 = dim == 3 ? 1 : q.size(1), dk = q.size(dim - 1);
+  const int64_t Hk = q.size(dim - 2), H = v.size(dim - 2), dv = v.size(dim - 1);
   a->act_dtype = act_type(q, "q");
-  heads(on, "q", q, q.scalar_type(), lead0, lead1, dk, &a->q_token_stride, &a->q_head_stride);
-  heads(on, "k", k, q.scalar_type(), lead0, lead1, dk, &a->k_token_stride, &a->k_head_stride);
-  heads(on, "v", v, q.scalar_type(), lead0, lead1, dv, &a->v_token_stride, &a->v_head_stride);
-  if (k.size(2) != q.size(2)) value_error("q and k must have the same heads");
+  heads(on, "q", q, q.scalar_type(), lead0, lead1, dk, &a->q_token_stride, &a->q_head_stride, dim);
+  heads(on, "k", k, q.scalar_type(), lead0, lead1, dk, &a->k_token_stride, &a->k_head_stride, dim);
+  heads(on, "v", v, q.scalar_type(), lead0, lead1, dv, &a->v_token_stride, &a->v_head_stride, dim);
+  if (k.size(dim - 2) != Hk) value_error("q and k must have the same heads");
   a->gate_dtype = act_type(g, "g");
   const bool fixed = g.dim() == 1;
-  const int64_t shape[] = {lead0, lead1, H};
-  plain(on, "g", &g, g.scalar_type(), at::IntArrayRef(shape + (fixed ? 2 : 0), shape + 3));
-  a->Hk = to_int("Hk", q.size(2)), a->H = to_int("H", H);
+  const int64_t three[] = {lead0, lead1, H}, two[] = {lead0, H};
+  plain(on, "g", &g, g.scalar_type(),
+        fixed ? at::IntArrayRef(two + 1, two + 2) : dim == 3 ? at::IntArrayRef(two) : at::IntArrayRef(three));
+  a->Hk = to_int("Hk", Hk), a->H = to_int("H", H);
   a->dk = to_int("dk", dk), a->dv = to_int("dv", dv);
   a->q = q.data_ptr(), a->k = k.data_ptr(), a->v = v.data_ptr(), a->g = g.data_ptr();
   a->scale = (float)PyFloat_AsDouble(scale);
@@ -477,10 +484,7 @@ PyObject* lin_decode(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   }
   const at::ScalarType out = out_type(o, args[9]);
   kda_lin_decode_args a{};
-  if (step)
-    linear(on, q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), g.dim() == 1 ? g : g.unsqueeze(1), args[6], &a);
-  else
-    linear(on, q, k, v, g, args[6], &a);
+  linear(on, q, k, v, g, args[6], &a);
   const int64_t N = q.size(0);
   plain(on, "S", &S, at::kFloat, {N, a.H, a.dk, a.dv});
   plain(on, "accept", accept, at::kInt, {N});
