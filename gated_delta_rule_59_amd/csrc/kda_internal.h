@@ -205,6 +205,7 @@ struct LogitsPlan {
   const uint32_t* mask;
   int64_t mask_seq, mask_row;    // words
   const float* temperature;
+  bool kept;  // the adjusted logits stand in out between the passes
   void* workspace;
 };
 size_t logits_workspace_bytes(int N, int R, int V);

@@ -2,10 +2,11 @@
 // mask, a temperature, and the softmax.
 //
 // Every logit is read (twice for probabilities: once for the row's maximum and sum, once for the
-// values) and every result written once; the second read comes from the caches where the batch fits
-// them. The launches bound one row (9.1 us for 32,000 tokens). For 256 sequences of five rows of 131,072, bf16
-// to fp32, with everything there is, the first pass takes 151 us, which its instructions bound (about 75
-// where nothing is adjusted), the second 226, of which 180 go to reading and writing 1 GB.
+// values; of a few rows the second pass reads what the first made of them) and every result written once;
+// the second read comes from the caches where the batch fits them. The launches bound one row (7.8 us for
+// 32,000 tokens). For 256 sequences of five rows of 131,072, bf16 to fp32, with everything there is, the first
+// pass takes 151 us, which its instructions bound (about 75 where nothing is adjusted), the second 226, of
+// which 180 go to reading and writing 1 GB.
 //
 // A workgroup takes a block of tokens of one sequence, for all of its rows or for one, and has the next
 // row's logits on their way while it works on this one's. It first counts in LDS what the history holds of
@@ -156,6 +157,12 @@ __device__ __forceinline__ Stat join(Stat mine, const Stat* s, int n, bool greed
   return all;
 }
 
+// Where the first pass may leave the adjusted logits in out for the second: fp32 results of a few rows, which
+// stay in the caches (with a history, one row of 32,000 tokens: 9.5 us, so 7.8; five of 131,072: 14.0, 12.5; 48 of
+// 32,000: 15.7, 14.4). Large batches would pay for the bytes (16 x 5 of 131,072: 33.9, so 42.5).
+template <typename O, int STEPS>
+constexpr bool kKeeps = STEPS == 1 && sizeof(O) == sizeof(float);
+
 // STEPS: times kE tokens of each thread are a block.
 template <typename T, typename O, Mode MODE, int STEPS>
 __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, int blocks, int splits) {
@@ -209,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   const float heat = p.temperature ? p.temperature[n] : 1.f, temperature = heat == INFINITY ? FLT_MAX : heat;
   const bool greedy = !(temperature > 0.f);
   // one over the temperature, where that is a normal number (2^-126 .. 2^126)
-  const bool scaled = !greedy && temperature != 1.f, inverse = temperature > 0x1p-126f && temperature < 0x1p126f;
+  const bool scaled = !greedy && temperature != 1.f && !(MODE == kProbs && p.kept), inverse = temperature > 0x1p-126f && temperature < 0x1p126f;
   const float scale = 1.f / temperature, once = 1.f / repetition;
 
   // What is added to a token that is `w` in the counts and has this bias, and whether it repeats.
@@ -336,7 +343,13 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
         }
       }
     }
+    O* out = static_cast<O*>(p.out) + n * p.out_seq + j * p.out_row + base;
     if (MODE == kStats) {
+      if (kKeeps<O, STEPS> && p.kept) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+          if (t * kE + e < here) store1(out + t * kE + e, x[0][e]);
+      }
       Stat s{-INFINITY, 0.f, INT32_MAX, 0};
       float top = -INFINITY;
 #pragma unroll
@@ -368,7 +381,6 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
         static_cast<Stat*>(p.workspace)[((int64_t)n * p.R + j) * stats + b * (kThreads / 64) + (t >> 6)] = s;
       continue;
     }
-    O* out = static_cast<O*>(p.out) + n * p.out_seq + j * p.out_row + base;
     const float share = row.sum == 0.f ? 0.f : 1.f / row.sum;
 #pragma unroll
     for (int c = 0; c < STEPS; ++c) {
@@ -420,6 +432,18 @@ hipError_t launch(const LogitsPlan& p, hipStream_t stream) {
 template <typename T, typename O, int STEPS>
 hipError_t launch_steps(const LogitsPlan& p, hipStream_t stream) {
   if (!p.probs) return launch<T, O, kAdjust, STEPS>(p, stream);
+  if constexpr (kKeeps<O, STEPS>) {
+    if (p.history || p.drafts || p.bias_ids) {
+      LogitsPlan q = p;
+      q.kept = true;
+      const hipError_t e = launch<T, O, kStats, STEPS>(q, stream);
+      if (e != hipSuccess) return e;
+      q.logits = p.out, q.seq = p.out_seq, q.row = p.out_row;
+      q.history = q.drafts = q.bias_ids = nullptr;
+      q.mask = nullptr;
+      return launch<O, O, kProbs, STEPS>(q, stream);
+    }
+  }
   const hipError_t e = launch<T, O, kStats, STEPS>(p, stream);
   return e == hipSuccess ? launch<T, O, kProbs, STEPS>(p, stream) : e;
 }

@@ -218,6 +218,10 @@ def test_in_place_and_strided():
         turned = torch.empty(2, 3, 1001, device="cuda").transpose(0, 1)
         binding.adjust_logits(torch.from_numpy(x).cuda(), **d, probs=probs, out=turned)
         assert torch.equal(turned, run(x, kw, act="f32", probs=probs))
+        # fp32 in place, rows outermost
+        y = torch.from_numpy(x).cuda().transpose(0, 1).contiguous().transpose(0, 1)
+        assert binding.adjust_logits(y, **d, probs=probs, out=y) is y
+        assert torch.equal(y, run(x, kw, act="f32", probs=probs))
     # one mask for all rows, a wide history
     kw["mask"] = kw["mask"][:1, :1]
     d["mask"] = torch.from_numpy(kw["mask"].copy()).cuda().expand(3, 2, -1)
