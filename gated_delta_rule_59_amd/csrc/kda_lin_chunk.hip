@@ -27,8 +27,8 @@
 // Precision. bf16 inputs go into products as they are. What is no bf16 number goes in parts, each the
 // rounded rest of the one before. Decayed values go in three (2^-25: the state is a 32-bit result); two
 // would leave it off by 1.6e-6. So do the state and the weights (q_i . k_j) e^{G_i - G_j} where o is
-// fp32; where it is bf16, two (2^-17) are as good. G is summed in 64 bits and kept in two 32-bit parts, so that a strong decay costs the
-// differences after it nothing.
+// fp32; where it is bf16, two (2^-17) are as good. G is summed in 64 bits and kept in two 32-bit parts, so
+// that a strong decay costs the differences after it nothing.
 #include <algorithm>
 
 #include "kda_lin_chunk.h"
@@ -99,7 +99,8 @@ struct Shape {
 
 // PARTS: bf16 parts of states and weights in what becomes o; 0: sums of segments only.
 template <int DK, int DV, int PARTS, typename O>
-__global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ? 1 : 2)) void lin_walk_kernel(const LinPlan p) {
+__global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ? 1 : 2)) void lin_walk_kernel(
+    const LinPlan p) {
   using Sh = Shape<DK, DV>;
   constexpr bool SUM = PARTS == 0;
   constexpr int NP = SUM ? 1 : PARTS;
@@ -403,7 +404,8 @@ template <int DK, int DV>
 hipError_t launch(const LinPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.jobs * p.H));
   constexpr int threads = Shape<DK, DV>::kThreads;
-  launch_before<Shape<DK, DV>>(p, stream, [&] { lin_walk_kernel<DK, DV, 0, float><<<grid, threads, 0, stream>>>(p); });
+  launch_before<Shape<DK, DV>>(
+      p, stream, [&] { lin_walk_kernel<DK, DV, 0, float><<<sums_grid(p), threads, 0, stream>>>(p); });
   if (p.out_bf16)
     lin_walk_kernel<DK, DV, 2, uint16_t><<<grid, threads, 0, stream>>>(p);
   else

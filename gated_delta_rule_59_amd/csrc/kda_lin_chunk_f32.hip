@@ -249,7 +249,7 @@ hipError_t launch_f32(const LinPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.jobs * p.H));
   constexpr int threads = ShapeF32<DK, DV>::kThreads;
   launch_before<ShapeF32<DK, DV>>(
-      p, stream, [&] { lin_walk_f32_kernel<DK, DV, true, float><<<grid, threads, 0, stream>>>(p); });
+      p, stream, [&] { lin_walk_f32_kernel<DK, DV, true, float><<<sums_grid(p), threads, 0, stream>>>(p); });
   if (p.out_bf16)
     lin_walk_f32_kernel<DK, DV, false, uint16_t><<<grid, threads, 0, stream>>>(p);
   else
