@@ -13,9 +13,10 @@
 // its tokens: a word per token, the number of times past the prompt in 31 bits and in the top bit
 // whether it is there at all; and of the biases it keeps the last entry's number. Adding whole numbers and
 // taking their maximum gives the same whatever the order, so results are the same on every run. Both make
-// one word per token that a row's tokens are looked up in: what is added to the logit, its lowest bit (2^-23
-// of it) taken for whether the repetition factor holds; 0 for most tokens. Row j's drafts are the first
-// j: a row counts the one before it.
+// one word per token that a row's tokens are looked up in: what is added to the logit, +0 for most tokens, which
+// nothing is done with; -0, which changes no value, for one that only the repetition factor holds for. Which
+// tokens that holds for is a bit each, in a register of the thread that has the token in every row. Row j's
+// drafts are the first j: a row counts the one before it.
 #include <algorithm>
 #include <cfloat>
 
@@ -79,9 +80,10 @@ struct Raw<uint16_t> {
     return __uint_as_float(i % 2 ? x[i / 2] & 0xffff0000u : x[i / 2] << 16);
   }
 };
-// Where the bits of m are 1 those of a, else b's.
+// Where the bits of m are 1 those of a, else b's. (Written with & and |, the compiler makes comparisons and up to
+// six instructions of it.)
 __device__ __forceinline__ float choose(unsigned m, float a, float b) {
-  return __uint_as_float((m & __float_as_uint(a)) | (~m & __float_as_uint(b)));
+  return __uint_as_float(__builtin_amdgcn_bitop3_b32(m, __float_as_uint(a), __float_as_uint(b), 0xca));
 }
 // Bit i of x in every bit.
 __device__ __forceinline__ unsigned bit(unsigned x, int i) { return (unsigned)__builtin_amdgcn_sbfe((int)x, i, 1); }
@@ -163,9 +165,10 @@ __device__ __forceinline__ Stat join(Stat mine, const Stat* s, int n, bool greed
 template <typename O, int STEPS>
 constexpr bool kKeeps = STEPS == 1 && sizeof(O) == sizeof(float);
 
-// STEPS: times kE tokens of each thread are a block.
+// STEPS: times kE tokens of each thread are a block. Of large blocks the LDS takes five to a CU, and so shall the
+// registers.
 template <typename T, typename O, Mode MODE, int STEPS>
-__global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, int blocks, int splits) {
+__global__ __launch_bounds__(kThreads, STEPS == 4 ? 5 : 1) void logits_kernel(const LogitsPlan p, int blocks, int splits) {
   constexpr int kBlock = STEPS * kThreads * kE;
   extern __shared__ __align__(16) unsigned s_mem[];
   const int t = threadIdx.x;
@@ -180,6 +183,10 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   Raw<T> next[STEPS];
   unsigned next_mask[STEPS];
   int next_draft = -1;
+  // A zero that the compiler does not know to be the same in all lanes: a draft read at a scalar's address would go
+  // to a scalar register, which waits for it, and for the row, where it is asked for.
+  int lane_zero;
+  asm("v_mov_b32 %0, 0" : "=v"(lane_zero));
   const int stats = blocks * (kThreads / 64);  // of a row: one per wave
   Stat next_stat{-INFINITY, 0.f, INT32_MAX, 0};
 #pragma unroll
@@ -187,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   auto fetch = [&](int j) {  // row j's block, tokens past the vocabulary as -inf
     const T* in = static_cast<const T*>(p.logits) + n * p.seq + j * p.row + base;
     const uint32_t* mask = p.mask + n * p.mask_seq + j * p.mask_row + base / 32;
-    if (p.drafts && j > 0) next_draft = p.drafts[(int64_t)n * (p.R - 1) + j - 1];
+    if (p.drafts && j > 0) next_draft = (p.drafts + (int64_t)n * (p.R - 1) + j - 1)[lane_zero];
     if (MODE == kProbs && (t & 63) < stats)
       next_stat = static_cast<const Stat*>(p.workspace)[((int64_t)n * p.R + j) * stats + (t & 63)];
     if (here == kBlock) {
@@ -219,14 +226,15 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
   const bool scaled = !greedy && temperature != 1.f && !(MODE == kProbs && p.kept), inverse = temperature > 0x1p-126f && temperature < 0x1p126f;
   const float scale = 1.f / temperature, once = 1.f / repetition;
 
+  unsigned repeats = 0;  // this thread's tokens that the repetition factor holds for: bit c kE + e
   // What is added to a token that is `w` in the counts and has this bias, and whether it repeats.
-  auto add_of = [&](unsigned w, float bias) {
+  auto adjust = [&](unsigned x, unsigned w, float bias, int i) {
     const unsigned times = w & ~kThere;
     const float less = times ? frequency * (float)times + presence : 0.f;
     const float add = bias - less;
-    const unsigned bits = __builtin_bit_cast(unsigned, add);
-    // beside an infinite one the factor makes no difference, and its bit would make it a NaN
-    return fabsf(add) < INFINITY ? (bits & ~1u) | (w ? 1u : 0u) : bits;
+    s_add[x] = add == 0.f ? 0x80000000u : __builtin_bit_cast(unsigned, add);
+    // beside an infinite one the factor makes no difference; a product out of range would make it a NaN
+    repeats = (repeats & ~(1u << i)) | (w && fabsf(add) < INFINITY ? 1u : 0u) << i;
   };
   if (said || biased) {
     typedef unsigned vec __attribute__((ext_vector_type(4)));
@@ -275,14 +283,15 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
       const vec b = *reinterpret_cast<const vec*>(&s_add[i]);
 #pragma unroll
       for (int e = 0; e < kE; ++e)
-        if (w[e] | b[e]) s_add[i + e] = add_of(w[e], b[e] ? p.bias[(int64_t)n * p.max_bias + b[e] - 1] : 0.f);
+        if (w[e] | b[e]) adjust(i + e, w[e], b[e] ? p.bias[(int64_t)n * p.max_bias + b[e] - 1] : 0.f, c * kE + e);
     }
     __syncthreads();
   }
 
   for (int j = j0; j < j1; ++j) {
     if (j > j0 && p.drafts) {
-      const unsigned x = (unsigned)next_draft - (unsigned)base;
+      const int draft = __builtin_amdgcn_readfirstlane(next_draft);
+      const unsigned x = (unsigned)draft - (unsigned)base;
       if (x < (unsigned)here) {  // the same for all threads
         __syncthreads();
         if (t == 0) s_found = 0;
@@ -290,13 +299,12 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
         if (biased) {
           const int count = p.bias_counts ? min(max(p.bias_counts[n], 0), p.max_bias) : p.max_bias;
           for (int i = t; i < count; i += kThreads)
-            if (p.bias_ids[(int64_t)n * p.max_bias + i] == next_draft) atomicMax(&s_found, i + 1);
+            if (p.bias_ids[(int64_t)n * p.max_bias + i] == draft) atomicMax(&s_found, i + 1);
         }
         __syncthreads();
-        if (t == 0) {
-          s_said[x] += 1;
-          s_add[x] = add_of(s_said[x], s_found ? p.bias[(int64_t)n * p.max_bias + s_found - 1] : 0.f);
-        }
+        if (t == (int)(x / kE % kThreads))
+          adjust(x, s_said[x] += 1, s_found ? p.bias[(int64_t)n * p.max_bias + s_found - 1] : 0.f,
+                 x / kE / kThreads * kE + x % kE);
         __syncthreads();
       }
     }
@@ -305,6 +313,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
 #pragma unroll
     for (int c = 0; c < STEPS; ++c) {
       mask[c] = next_mask[c];
+      asm volatile("" : "+v"(mask[c]));  // here, not behind the next row's loads, which the copy would wait for
 #pragma unroll
       for (int e = 0; e < kE; ++e) x[c][e] = next[c].at(e);
     }
@@ -324,7 +333,7 @@ __global__ __launch_bounds__(kThreads) void logits_kernel(const LogitsPlan p, in
           for (int e = 0; e < kE; ++e) {
             // no branches: with a history of thousands, some lane has such a token nearly every time
             const float y = x[c][e], z = y * choose(bit(__float_as_uint(y), 31), repetition, once);
-            x[c][e] = choose(bit(w[e], 0), z, y) + __uint_as_float(w[e]);
+            x[c][e] = choose(bit(repeats, c * kE + e), z, y) + __uint_as_float(w[e]);
           }
         }
       }
