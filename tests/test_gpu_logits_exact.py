@@ -61,3 +61,63 @@ def test_biases_and_penalties_are_added_exactly(N, R, V, history):
     want = plain(x, **kw)
     assert (want == want.astype(np.float32)).all()
     assert (run(x, kw, act="f32").double().cpu().numpy() == want).all()
+
+
+def quotients(divisors, V):
+    """Rows of logits that are products of a divisor and a 12-bit number, exact in 32 bits; the numbers."""
+    rng = np.random.default_rng(95)
+    q = (rng.integers(2048, 4096, (len(divisors), 1, V)) * 2.0 ** rng.integers(-14, -8, (len(divisors), 1, V)))
+    q = q * rng.choice([-1.0, 1.0], q.shape)
+    d = np.asarray(divisors, np.float32)
+    x = q * d.astype(np.float64)[:, None, None]
+    assert (x == x.astype(np.float32)).all()
+    return x.astype(np.float32), q, d
+
+
+DIVISORS = [1.5, 1.25, 1.125, 1.3125, 0.75, 1.75, 0.6875, 3.0, 1.0009765625, 1 / 1024]
+
+
+@pytest.mark.parametrize("V", [900, 140000])
+def test_temperatures_divide(V):
+    """x / temperature is the quotient rounded once: the very number where there is one."""
+    x, q, d = quotients(DIVISORS, V)
+    y = run(x, dict(temperature=d), act="f32").double().cpu().numpy()
+    assert (y == q).all(), np.argwhere(y != q)[:4]
+    x = np.random.default_rng(96).standard_normal(x.shape).astype(np.float32)
+    want = x.astype(np.float64) / d.astype(np.float64)[:, None, None]
+    y = run(x, dict(temperature=d), act="f32").double().cpu().numpy()
+    # half a step, and 2^-45 for what the second part of the reciprocal leaves
+    assert (np.abs(y - want) <= 0.5 * np.spacing(np.abs(want).astype(np.float32)) + 2.0 ** -45 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("V", [900, 140000])
+def test_repetition_divides(V):
+    """So is x / repetition, so that a greedy row chooses the first of equal ones where one of them was
+    divided; x * repetition where x is below 0."""
+    x, q, d = quotients(DIVISORS, V)
+    N = len(d)
+    x, q = np.abs(x), np.abs(q)
+    x[:, 0, 1::2] *= -1
+    q[:, 0, 1::2] = x[:, 0, 1::2].astype(np.float64) * d.astype(np.float64)[:, None]
+    kw = dict(history=np.tile(np.arange(800, dtype=np.int32), (N, 1)), history_lens=np.full(N, 800, np.int32), repetition=d)
+    y = run(x, kw, act="f32").double().cpu().numpy()
+    assert (y[:, :, 800:] == x[:, :, 800:]).all()
+    want, got = q[:, :, :800], y[:, :, :800]
+    assert (got[:, :, ::2] == want[:, :, ::2]).all(), np.argwhere(got[:, :, ::2] != want[:, :, ::2])[:4]
+    assert (np.abs(got - want) <= 0.5 * np.spacing(np.abs(want).astype(np.float32))).all()
+    # token 20 is not in the history and equal to a later one's quotient
+    x = np.zeros((N, 1, V), np.float32)
+    most = np.float32(1 + 126 / 128)
+    x[:, 0, 20], x[:, 0, 30] = most, most * d
+    kw.update(history=np.full((N, 1), 30, np.int32), history_lens=np.ones(N, np.int32), temperature=np.zeros(N, np.float32))
+    p = run(x, kw, act="f32", probs=True).cpu().numpy()
+    assert (p[:, 0, 20] == 1).all() and (p.sum(-1) == 1).all()
+
+
+def test_infinite_logits_stay_infinite():
+    x = np.zeros((2, 1, 3000), np.float32)
+    x[:, 0, 3::7], x[:, 0, 4::7] = np.inf, -np.inf
+    kw = dict(temperature=np.array([0.7, 3.0], np.float32), repetition=np.array([1.3, 0.8], np.float32),
+              history=np.tile(np.arange(3000, dtype=np.int32), (2, 1)), history_lens=np.full(2, 2000, np.int32))
+    y = run(x, kw, act="f32").cpu().numpy()
+    assert (y == plain(x, **kw)).all()
