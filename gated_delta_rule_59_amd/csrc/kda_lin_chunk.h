@@ -93,19 +93,23 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
       lin_tokens(p, lane, &first, &len);
       x = segments_of(p, len);
     }
-    const int to = sums_to(x);
-    const unsigned all = (unsigned)min((int64_t)__shfl(to, 63, 64) * p.H, (int64_t)gridDim.x);
+    // segments of the sequences up to each: whole segments, and one more of each sequence. Offsets that overlap
+    // give more than there is room for: from the first sequence that finds none on, nothing is done.
+    const int whole = sums_to(max(x - 1, 0)), to = whole + lane + 1;
+    const int n_seq = __popcll(__ballot(lane < p.n_seq && to <= p.jobs));
+    if (n_seq == 0) return false;
+    const int wholes = __shfl(whole, n_seq - 1, 64);
+    const unsigned all = (unsigned)min((int64_t)(wholes + n_seq) * p.H, (int64_t)gridDim.x);
     if (b >= all) return false;
     const unsigned place = b < 256 || all > 512 ? b : all - 1 - (b - 256);
     const int k = place / p.H;
-    const int whole = sums_to(max(x - 1, 0)), wholes = __shfl(whole, 63, 64);
-    const int rest = lane < p.n_seq ? len - (x - 1) * p.seg : -1;
+    const int rest = lane < n_seq ? len - (x - 1) * p.seg : -1;
     int above = 0;
-    for (int m = 0; m < p.n_seq; ++m) {
+    for (int m = 0; m < n_seq; ++m) {
       const int y = __shfl(rest, m, 64);
       above += y > rest || (y == rest && m < lane);
     }
-    const uint64_t which = k < wholes ? __ballot(whole > k) : __ballot(lane < p.n_seq && above == k - wholes);
+    const uint64_t which = k < wholes ? __ballot(whole > k) : __ballot(lane < n_seq && above == k - wholes);
     if (!which) return false;
     const int l = __builtin_ctzll(which);
     j->n = l;
@@ -114,7 +118,7 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
     j->slot = __shfl(to, l, 64) - j->segments + j->s;
     j->h = place % p.H;
     lin_tokens(p, l, &j->first, &j->len);
-    return j->slot < p.jobs;
+    return true;
   }
   const int2 which = jobs_of(p)[b / p.H];
   if (which.x < 0) return false;
