@@ -164,6 +164,7 @@ struct LinPlan {
   const int32_t* accept;         // decode: S_T is the state after accept[n] tokens; nullptr: after all
   int seg;                       // prompts: tokens of a segment
   int jobs;                      // segments there may be at most, of all sequences
+  int slots;                     // those of sequences that have several, whose states lie in the workspace
   void* workspace;
   size_t tables;                 // packed prompts of many sequences: where their table lies in it
 };

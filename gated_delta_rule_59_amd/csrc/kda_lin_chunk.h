@@ -13,7 +13,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // What a workgroup walks: segment s of `segments` of sequence n, head h.
 struct Job {
   int n, s, segments, h;
-  int slot;        // segments of sequences before it, and of its own
+  int slot;        // its state's place in the workspace, where its sequence has several segments
   int64_t first;   // the sequence's first row
   int len;         // its tokens
 };
@@ -29,7 +29,10 @@ __device__ __forceinline__ int sums_to(int x) {
   return x;
 }
 
-// In the workspace behind the states and their decays, for more than 64 packed sequences: the segments of
+// Only sequences of several segments have states in the workspace, a slot for each segment; offsets that do not
+// overlap give at most 2 (T / seg) of them.
+//
+// In the workspace behind the states and their decays, for more than 64 packed sequences: the slots of
 // the sequences before each, and of each segment its sequence and its number there (-1: there is none).
 // (A walk over the offsets in every workgroup, which 64 sequences take, would take longer than the work
 // for thousands.)
@@ -40,9 +43,9 @@ __device__ __forceinline__ int2* jobs_of(const LinPlan& p) {
   return reinterpret_cast<int2*>(starts_of(p) + (p.n_seq + 1) / 2 * 2);
 }
 __global__ __launch_bounds__(1024) void lin_jobs_kernel(const LinPlan p) {
-  __shared__ int s_sum[16];
+  __shared__ int s_sum[16], s_slots[16];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  int64_t done = 0;
+  int64_t done = 0, slots = 0;
   for (int n0 = 0; n0 < p.n_seq; n0 += 1024) {
     const int n = n0 + t;
     int64_t first;
@@ -51,16 +54,17 @@ __global__ __launch_bounds__(1024) void lin_jobs_kernel(const LinPlan p) {
       lin_tokens(p, n, &first, &len);
       x = segments_of(p, len);
     }
-    const int to = sums_to(x);
-    if (lane == 63) s_sum[wave] = to;
+    const int several = x > 1 ? x : 0, to = sums_to(x), slots_to = sums_to(several);
+    if (lane == 63) s_sum[wave] = to, s_slots[wave] = slots_to;
     __syncthreads();
-    int64_t at = done + to - x;
+    int64_t at = done + to - x, slot = slots + slots_to - several;
     for (int w = 0; w < 16; ++w) {
-      if (w < wave) at += s_sum[w];
-      done += s_sum[w];
+      if (w < wave) at += s_sum[w], slot += s_slots[w];
+      done += s_sum[w], slots += s_slots[w];
     }
     __syncthreads();
-    if (n < p.n_seq) starts_of(p)[n] = (int)min(at, (int64_t)p.jobs);  // offsets that overlap give more
+    // offsets that overlap give more
+    if (n < p.n_seq) starts_of(p)[n] = (int)min(slot, (int64_t)p.slots);
     for (int s = 0; s < x && at + s < p.jobs; ++s) jobs_of(p)[at + s] = int2{n, s};
   }
   for (int64_t i = done + t; i < p.jobs; i += 1024) jobs_of(p)[i] = int2{-1, 0};
@@ -93,10 +97,13 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
       lin_tokens(p, lane, &first, &len);
       x = segments_of(p, len);
     }
-    // segments of the sequences up to each: whole segments, and one more of each sequence. Offsets that overlap
-    // give more than there is room for: from the first sequence that finds none on, nothing is done.
+    // segments and slots of the sequences up to each: whole segments, and one more of each sequence, or of each
+    // that has several. Offsets that overlap give more than there is room for: from the first sequence that
+    // finds none on, nothing is done.
     const int whole = sums_to(max(x - 1, 0)), to = whole + lane + 1;
-    const int n_seq = __popcll(__ballot(lane < p.n_seq && to <= p.jobs));
+    const uint64_t several = __ballot(x > 1);
+    const int slots = whole + __popcll(several & (~0ull >> (63 - lane)));
+    const int n_seq = __popcll(__ballot(lane < p.n_seq && to <= p.jobs && slots <= p.slots));
     if (n_seq == 0) return false;
     const int wholes = __shfl(whole, n_seq - 1, 64);
     const unsigned all = (unsigned)min((int64_t)(wholes + n_seq) * p.H, (int64_t)gridDim.x);
@@ -115,7 +122,7 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
     j->n = l;
     j->segments = __shfl(x, l, 64);
     j->s = k < wholes ? k - (__shfl(whole, l, 64) - (j->segments - 1)) : j->segments - 1;
-    j->slot = __shfl(to, l, 64) - j->segments + j->s;
+    j->slot = __shfl(slots, l, 64) - j->segments + j->s;
     j->h = place % p.H;
     lin_tokens(p, l, &j->first, &j->len);
     return true;
@@ -124,11 +131,11 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
   if (which.x < 0) return false;
   j->n = which.x;
   j->s = which.y;
-  j->slot = b / p.H;
   j->h = b % p.H;
   lin_tokens(p, j->n, &j->first, &j->len);
   j->segments = segments_of(p, j->len);
-  return true;
+  j->slot = j->segments > 1 ? starts_of(p)[j->n] + j->s : 0;
+  return j->segments == 1 || j->slot < p.slots;
 }
 
 // A barrier that orders the LDS only: rows of the next chunk stay on their way across it, and so do
@@ -174,11 +181,11 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 
 // A state in the workspace: [wave][key tile][value tile][lane] of four key rows each.
 template <typename Sh>
-__device__ __forceinline__ int64_t slot_of(const LinPlan& p, int64_t job, int h) {
-  return (job * p.H + h) * (Sh::kState / 4);
+__device__ __forceinline__ int64_t slot_of(const LinPlan& p, int64_t slot, int h) {
+  return (slot * p.H + h) * (Sh::kState / 4);
 }
 __device__ __forceinline__ float* decays_of(const LinPlan& p) {
-  return static_cast<float*>(p.workspace) + (int64_t)p.jobs * p.H * p.dk * p.dv;
+  return static_cast<float*>(p.workspace) + (int64_t)p.slots * p.H * p.dk * p.dv;
 }
 
 // From the sums of a sequence's segments to the states that enter them, in the sums' place. A thread
@@ -193,24 +200,25 @@ __global__ __launch_bounds__(256) void lin_entries_kernel(const LinPlan p) {
     const int part = (int)(item % kGroups), n = (int)(nh / p.H), h = (int)(nh % p.H);
     const int i = part * 256 + threadIdx.x;
     int64_t first;
-    int len, job = 0;
+    int len, slot = 0;
     lin_tokens(p, n, &first, &len);
     const int segments = segments_of(p, len);
     if (segments == 1) continue;
     if (!p.cu_seqlens) {
-      job = n * segments;
+      slot = n * segments;
     } else if (p.n_seq > 64) {
-      job = starts_of(p)[n];
+      slot = starts_of(p)[n];
     } else {
       const int m = threadIdx.x & 63;
       if (m < n) {
         lin_tokens(p, m, &first, &len);
-        job = segments_of(p, len);
+        const int x = segments_of(p, len);
+        slot = x > 1 ? x : 0;
       }
 #pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) job += __shfl_xor(job, d, 64);
+      for (int d = 32; d >= 1; d >>= 1) slot += __shfl_xor(slot, d, 64);
     }
-    const int there = min(segments, p.jobs - job);  // offsets that overlap give more segments than jobs
+    const int there = min(segments, p.slots - slot);  // offsets that overlap give more segments than slots
     if (i >= Sh::kState / 4) continue;
     floatx4 e{0.f, 0.f, 0.f, 0.f};
     if (p.S0) {
@@ -230,14 +238,14 @@ __global__ __launch_bounds__(256) void lin_entries_kernel(const LinPlan p) {
         z[s] = floatx4{0.f, 0.f, 0.f, 0.f};
         a[s] = 1.f;
         if (s0 + s < there && s0 + s + 1 < segments) {
-          z[s] = at[slot_of<Sh>(p, job + s0 + s, h)];
-          a[s] = decays[(int64_t)(job + s0 + s) * p.H + h];
+          z[s] = at[slot_of<Sh>(p, slot + s0 + s, h)];
+          a[s] = decays[(int64_t)(slot + s0 + s) * p.H + h];
         }
       }
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
         if (s0 + s < there) {
-          at[slot_of<Sh>(p, job + s0 + s, h)] = e;
+          at[slot_of<Sh>(p, slot + s0 + s, h)] = e;
           e = e * a[s] + z[s];
         }
       }

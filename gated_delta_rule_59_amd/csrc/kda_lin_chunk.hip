@@ -441,7 +441,8 @@ size_t plan_lin_chunk(LinPlan* p) {
   p->seg = (int)seg;
   const int64_t per = std::max<int64_t>(1, ((int64_t)p->T + p->seg - 1) / p->seg);
   p->jobs = (int)(p->cu_seqlens && p->T > p->seg ? p->T / p->seg + p->n_seq : per * p->n_seq);
-  const size_t states = p->T > p->seg ? sizeof(float) * (size_t)p->jobs * p->H * ((size_t)p->dk * p->dv + 1) : 0;
+  p->slots = p->T <= p->seg ? 0 : p->cu_seqlens ? std::min(p->jobs, 2 * (p->T / p->seg)) : p->jobs;
+  const size_t states = sizeof(float) * (size_t)p->slots * p->H * ((size_t)p->dk * p->dv + 1);
   if (!p->cu_seqlens || p->n_seq <= 64) return states;
   p->tables = (states + 15) / 16 * 16;
   return p->tables + sizeof(int) * (((size_t)p->n_seq + 1) / 2 * 2 + 2 * (size_t)p->jobs);
