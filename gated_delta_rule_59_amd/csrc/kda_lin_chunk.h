@@ -177,7 +177,28 @@ __device__ __forceinline__ void store4(uint16_t* p, const floatx4& x) {
   *reinterpret_cast<s16x4*>(p) = y;
 }
 
-__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+// 2^(x + rest), rest next to nothing. Rounding the exponent to 32 bits alone would leave a decay of 2^-30 off by 2^-20.5.
+__device__ __forceinline__ float exp2_of(float x, float rest) {
+  return __builtin_amdgcn_exp2f(x) * fmaf(rest, 0.693147181f, 1.f);
+}
+// A sum of logarithms in two parts.
+struct Log {
+  float hi, lo;
+  __device__ __forceinline__ explicit Log(double x) : hi((float)x), lo((float)(x - (double)hi)) {}
+};
+__device__ __forceinline__ float exp2_of(double x) {
+  const Log y(x);
+  return exp2_of(y.hi, y.lo);
+}
+__device__ __forceinline__ float lane_of(float x, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+// 2^((hi + lo) - (jhi + jlo)). What the difference of the first parts is rounded by is had back (exactly where |hi| is
+// not below |jhi|, as for sums of decays up to a token and up to one before it).
+__device__ __forceinline__ float exp2_between(float hi, float lo, float jhi, float jlo) {
+  const float x = hi - jhi;
+  return exp2_of(x, ((hi - x) - jhi) + (lo - jlo));
+}
 
 // A state in the workspace: [wave][key tile][value tile][lane] of four key rows each.
 template <typename Sh>

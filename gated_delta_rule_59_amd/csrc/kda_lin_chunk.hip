@@ -28,7 +28,8 @@
 // rounded rest of the one before. Decayed values go in three (2^-25: the state is a 32-bit result); two
 // would leave it off by 1.6e-6. So do the state and the weights (q_i . k_j) e^{G_i - G_j} where o is
 // fp32; where it is bf16, two (2^-17) are as good. G is summed in 64 bits and kept in two 32-bit parts, so
-// that a strong decay costs the differences after it nothing.
+// that a strong decay costs the differences after it nothing; exponents too have a second part, so that a decay of
+// 2^-30 is as exact as one of 2^-1.
 #include <algorithm>
 
 #include "kda_lin_chunk.h"
@@ -183,14 +184,16 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ?
     const float ln = __uint_as_float(p.gate_bf16 ? gate << 16 : gate);
     const double G = wave_sums(real ? (double)(ln < -1000.f ? -1000.f : ln) * 1.4426950408889634 : 0.0);
     const double all = lane_of(G, 63);
-    const float hi = (float)G;
-    s_hi[to][lane] = hi;
-    s_lo[to][lane] = (float)(G - (double)hi);
-    s_e[to][lane] = p.scale * exp2_of((float)(G + held));
+    const Log to_here(G), meant(G + held);
+    s_hi[to][lane] = to_here.hi;
+    s_lo[to][lane] = to_here.lo;
+    s_e[to][lane] = p.scale * exp2_of(meant.hi, meant.lo);
     const double next = held + all;
     const bool settle = !(fabs(next) <= kHeld);
-    s_w[to][lane] = real ? exp2_of((float)(settle ? all - G : -(held + G))) : 0.f;
-    if (lane == 0) s_settle[to] = settle ? exp2_of((float)next) : 1.f;
+    const float w = settle ? exp2_between(lane_of(to_here.hi, 63), lane_of(to_here.lo, 63), to_here.hi, to_here.lo)
+                           : exp2_of(-meant.hi, -meant.lo);
+    s_w[to][lane] = real ? w : 0.f;
+    if (lane == 0) s_settle[to] = settle ? exp2_of(next) : 1.f;
     held = lane_of(settle ? 0.0 : next, 0);
     if (SUM) total = lane_of(total + all, 0);
   };
@@ -266,7 +269,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ?
         float w[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const float z = d[y] * (p.scale * exp2_of((hi - jhi[y]) + (lo - jlo[y])));
+          const float z = d[y] * (p.scale * exp2_between(hi, lo, jhi[y], jlo[y]));
           w[y] = j0 + y <= i ? z : 0.f;
         }
         bf16x4 parts[NP];
@@ -374,7 +377,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ?
   }
 
   if (SUM || (last && p.S_T)) {
-    if (t == kGates * 64) s_held = exp2_of((float)held);
+    if (t == kGates * 64) s_held = exp2_of(held);
     lds_barrier();
     const float f = s_held;
 #pragma unroll
@@ -387,7 +390,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ?
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int c = 0; c < CT; ++c) slots[((wave * KT + kt) * CT + c) * 64 + lane] = S[kt][c];
-    if (t == kGates * 64) decays_of(p)[(int64_t)j.slot * p.H + h] = exp2_of((float)total);
+    if (t == kGates * 64) decays_of(p)[(int64_t)j.slot * p.H + h] = exp2_of(total);
   } else if (last && p.S_T) {
     float* out = p.S_T + ((int64_t)j.n * p.H + h) * Sh::kState;
 #pragma unroll

@@ -116,14 +116,15 @@ __global__ __launch_bounds__((ShapeF32<DK, DV>::kThreads), 2) void lin_walk_f32_
       const bool real = lane < C && c0 + lane < len;
       const double G = wave_sums(real ? (double)(gate < -1000.f ? -1000.f : gate) * 1.4426950408889634 : 0.0);
       const double all = lane_of(G, 63);
-      const float hi = (float)G;
+      const Log to_here(G);
+      const float all_hi = lane_of(to_here.hi, 63), all_lo = lane_of(to_here.lo, 63);
       if (lane < C) {
-        s_hi[lane] = hi;
-        s_lo[lane] = (float)(G - (double)hi);
-        s_e[lane] = p.scale * exp2_of((float)G);
-        s_w[lane] = real ? exp2_of((float)(all - G)) : 0.f;
+        s_hi[lane] = to_here.hi;
+        s_lo[lane] = to_here.lo;
+        s_e[lane] = p.scale * exp2_of(to_here.hi, to_here.lo);
+        s_w[lane] = real ? exp2_between(all_hi, all_lo, to_here.hi, to_here.lo) : 0.f;
       }
-      if (lane == 0) s_all = exp2_of((float)all);
+      if (lane == 0) s_all = exp2_of(all_hi, all_lo);
       if (SUM) total += all;
     }
     lds_barrier();
@@ -148,7 +149,7 @@ __global__ __launch_bounds__((ShapeF32<DK, DV>::kThreads), 2) void lin_walk_f32_
         floatx4 w;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const float z = d[y] * (p.scale * exp2_of((hi - jhi[y]) + (lo - jlo[y])));
+          const float z = d[y] * (p.scale * exp2_between(hi, lo, jhi[y], jlo[y]));
           w[y] = j0 + y <= i ? z : 0.f;
         }
         s_p[n][lane] = w;
@@ -231,7 +232,7 @@ __global__ __launch_bounds__((ShapeF32<DK, DV>::kThreads), 2) void lin_walk_f32_
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int c = 0; c < CT; ++c) slots[((wave * KT + kt) * CT + c) * 64 + lane] = S[kt][c];
-    if (t == 0) decays_of(p)[(int64_t)j.slot * p.H + h] = exp2_of((float)total);
+    if (t == 0) decays_of(p)[(int64_t)j.slot * p.H + h] = exp2_of(total);
   } else if (last && p.S_T) {
     float* out = p.S_T + ((int64_t)j.n * p.H + h) * Sh::kState;
 #pragma unroll
