@@ -8,7 +8,7 @@
 //
 // which are matrix products but for the factors. A workgroup walks chunk after chunk through one
 // segment of one (sequence, head), the state in its accumulators. Segments of a sequence run in
-// parallel: lin_walk_kernel<..., 0> sums up each segment but the last from a state of zeros, and
+// parallel: lin_walk_kernel<..., true, ...> sums up each segment but the last from a state of zeros, and
 // lin_entries_kernel turns that into the states that enter the segments (S <- e^{G} S + Z from one to
 // the next); then the others do the walk proper. Without segments only the last is
 // launched.
@@ -25,9 +25,9 @@
 // exchanged between the waves through LDS.
 //
 // Precision. bf16 inputs go into products as they are. What is no bf16 number goes in parts, each the
-// rounded rest of the one before. Decayed values go in three (2^-25: the state is a 32-bit result); two
-// would leave it off by 1.6e-6. So do the state and the weights (q_i . k_j) e^{G_i - G_j} where o is
-// fp32; where it is bf16, two (2^-17) are as good. G is summed in 64 bits and kept in two 32-bit parts, so
+// rounded rest of the one before: decayed values, the state and the weights (q_i . k_j) e^{G_i - G_j} in three, which
+// hold their 24 bits, whatever o's type. (With two parts of state and weights long prompts with bf16 results took
+// 1.30 ms instead of 1.49, but results whose terms cancel were off by 2^-18 of the terms.) G is summed in 64 bits and kept in two 32-bit parts, so
 // that a strong decay costs the differences after it nothing; exponents too have a second part, so that a decay of
 // 2^-30 is as exact as one of 2^-1.
 #include <algorithm>
@@ -98,13 +98,14 @@ struct Shape {
   static __device__ __forceinline__ int key(int p, int e, int r) { return 32 * p + 8 * (r >> 2) + 4 * e + (r & 3); }
 };
 
-// PARTS: bf16 parts of states and weights in what becomes o; 0: sums of segments only.
-template <int DK, int DV, int PARTS, typename O>
+constexpr int kParts = 3;  // bf16 parts of what is a 32-bit number: its 24 bits
+
+// SUM: sums of segments only.
+template <int DK, int DV, bool SUM, typename O>
 __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ? 1 : 2)) void lin_walk_kernel(
     const LinPlan p) {
   using Sh = Shape<DK, DV>;
-  constexpr bool SUM = PARTS == 0;
-  constexpr int NP = SUM ? 1 : PARTS;
+  constexpr int NP = SUM ? 1 : kParts;
   constexpr int NT = Sh::kThreads, NW = Sh::kWaves, CT = Sh::kTiles, KT = DK / 16;
   constexpr int QL = kC * DK / 8 / NT, VL = kC * DV / 8 / NT;  // 16-byte pieces per thread
   __shared__ __align__(16) uint16_t s_q[SUM ? 8 : kC * DK], s_k[kC * DK], s_v[kC * DV];
@@ -345,7 +346,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ?
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      bf16x8 vw[CT][3];
+      bf16x8 vw[CT][kParts];
       const floatx4 w0 = *reinterpret_cast<const floatx4*>(&s_w[now][32 * s + 4 * g]);
       const floatx4 w1 = *reinterpret_cast<const floatx4*>(&s_w[now][32 * s + 16 + 4 * g]);
 #pragma unroll
@@ -353,7 +354,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ?
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(v[s][c][i]) * (i < 4 ? w0[i] : w1[i - 4]);
-        parts_of<3, 8>(x, vw[c]);
+        parts_of<kParts, 8>(x, vw[c]);
       }
       constexpr int kAtOnce = KT < 4 ? KT : 4;
 #pragma unroll
@@ -367,7 +368,7 @@ __global__ __launch_bounds__((Shape<DK, DV>::kThreads), (DK == 128 && DV == 32 ?
           k[x] = pair(read_tr(at), read_tr(at + 16 * DK));
         }
 #pragma unroll
-        for (int y = 0; y < 3; ++y)
+        for (int y = 0; y < kParts; ++y)
 #pragma unroll
           for (int x = 0; x < kAtOnce; ++x)
 #pragma unroll
@@ -408,11 +409,11 @@ hipError_t launch(const LinPlan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.jobs * p.H));
   constexpr int threads = Shape<DK, DV>::kThreads;
   launch_before<Shape<DK, DV>>(
-      p, stream, [&] { lin_walk_kernel<DK, DV, 0, float><<<sums_grid(p), threads, 0, stream>>>(p); });
+      p, stream, [&] { lin_walk_kernel<DK, DV, true, float><<<sums_grid(p), threads, 0, stream>>>(p); });
   if (p.out_bf16)
-    lin_walk_kernel<DK, DV, 2, uint16_t><<<grid, threads, 0, stream>>>(p);
+    lin_walk_kernel<DK, DV, false, uint16_t><<<grid, threads, 0, stream>>>(p);
   else
-    lin_walk_kernel<DK, DV, 3, float><<<grid, threads, 0, stream>>>(p);
+    lin_walk_kernel<DK, DV, false, float><<<grid, threads, 0, stream>>>(p);
   return hipGetLastError();
 }
 

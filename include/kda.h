@@ -455,7 +455,7 @@ kda_status kda_verify_drafts(const kda_verify_args* args, void* hip_stream);
  *   act_dtype  of q, k, v: KDA_F32 or KDA_BF16. gate_dtype of g, out_dtype of o: either. With
  *              KDA_BF16 activations products that need more than bf16 holds (states, weights, and
  *              values times decays) go in several bf16 parts. In prompts o is off by its own rounding
- *              and 2^-18 of its largest terms (KDA_BF16 o: 2^-16), S by 2^-18, beside what sums in 32
+ *              and 2^-18 of its largest terms, S by 2^-18, beside what sums in 32
  *              bits are rounded by; a prompt of one chunk (64 tokens): 2^-20 each; terms that live
  *              through more than 384 tokens: 2^-21 more for each further 128.
  *   q, k, v    [B, T, heads, d] (decode: [N, m, heads, d]): token t = b * T + j of head h begins at

@@ -17,7 +17,7 @@ from tests.test_gpu_lin import dev, rounded
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
-TYPES = [("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")]
+TYPES = [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")]
 
 
 def one_channel_each(seed, T, H, dk, dv, n_seq, act, powers):
