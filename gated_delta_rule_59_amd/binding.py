@@ -565,8 +565,8 @@ def adjust_logits(logits, *, history=None, history_lens=None, prompt_lens=None, 
                   stream=None):
     """Penalties, biases, a grammar's mask and a temperature on logits [N, R, V] (fp32 or bf16, rows
     contiguous; row j for the token after j drafts); with probs also the softmax, the p or q of
-    verify_drafts. history int32 [N, ids] with history_lens and prompt_lens int32 [N], drafts int32
-    [N, R - 1]: what repetition (history and drafts) and frequency and presence (all but the prompt), fp32
+    verify_drafts. history int32 [N, ids] (one expanded over sequences will do) with history_lens and prompt_lens
+    int32 [N], drafts int32 [N, R - 1]: what repetition (history and drafts) and frequency and presence (all but the prompt), fp32
     [N] each, go by. bias_ids int32, bias fp32 [N, entries], bias_counts int32 [N]. mask int32
     [N, R, ceil(V / 32)] (a view expanded over rows or sequences will do): bit i % 32 of word i / 32 is 1
     where token i is allowed. temperature fp32 [N]; 0 stands for the likeliest token. Returns out

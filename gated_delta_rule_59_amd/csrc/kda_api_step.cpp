@@ -259,8 +259,8 @@ kda_status kda_adjust_logits(const kda_logits_args* a, void* hip_stream) {
     return fail(KDA_ERR_NULL_PTR, "history goes with history_lens and max_history >= 1; prompt_lens needs it");
   if ((a->bias_ids != nullptr) != (a->bias != nullptr) || (a->bias_ids ? a->max_bias < 1 : a->bias_counts != nullptr))
     return fail(KDA_ERR_NULL_PTR, "bias_ids and bias go together, with max_bias >= 1; bias_counts needs them");
-  if (a->history && (a->max_history > (1 << 30) || a->history_stride < a->max_history))
-    return fail(KDA_ERR_BAD_SHAPE, "max_history must be at most 2^30, history_stride no less than it");
+  if (a->history && (a->max_history > (1 << 30) || (a->history_stride && a->history_stride < a->max_history)))
+    return fail(KDA_ERR_BAD_SHAPE, "max_history must be at most 2^30, history_stride no less than it, or 0");
   if (a->drafts && a->R < 2) return fail(KDA_ERR_BAD_SHAPE, "drafts need R >= 2 (got %d)", a->R);
   const int64_t most = int64_t(1) << 42;  // elements: keeps every offset below 2^63
   auto rows_ok = [&](int64_t seq, int64_t row) {

@@ -598,9 +598,9 @@ typedef struct {
  *   logits     row (n, j) begins at n * seq_stride + j * row_stride (elements), as the row of out does
  *              by its strides. out may be logits itself where types and strides are the same; otherwise
  *              they do not overlap. Rows of out do not overlap each other.
- *   history    int32: id t of sequence n at n * history_stride + t, t < history_lens[n] (device int32
- *              [N], taken as within [0, max_history]); the first prompt_lens[n] (device int32 [N] or
- *              NULL: 0) are its prompt. NULL: none. Ids outside [0, V) are no token's.
+ *   history    int32: id t of sequence n at n * history_stride + t (0 to share one), t < history_lens[n]
+ *              (device int32 [N], taken as within [0, max_history]); the first prompt_lens[n] (device
+ *              int32 [N] or NULL: 0) are its prompt. NULL: none. Ids outside [0, V) are no token's.
  *   drafts     int32 [N, R - 1], or NULL: none count.
  *   repetition, frequency, presence
  *              fp32 [N] each, or NULL for 1, 0, 0. repetition within 2^-126 .. 2^126.
