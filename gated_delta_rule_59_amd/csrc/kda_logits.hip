@@ -22,12 +22,13 @@
 
 #include "kda_device.h"
 #include "kda_internal.h"
+#include "kda_logits_plan.h"
 
 namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256, kE = 4;  // a thread takes kE neighbouring tokens at a time
+constexpr int kThreads = kLogitsThreads, kE = kLogitsEach;
 constexpr unsigned kThere = 0x80000000u;
 
 struct Stat {   // of a wave's part of a row
@@ -429,21 +430,10 @@ __global__ __launch_bounds__(kThreads, STEPS == 4 ? 5 : 1) void logits_kernel(co
   }
 }
 
-// Blocks of 1,024 tokens while there are no more than six to a CU, else of 4,096: small ones take less time
-// each, but every one goes through the whole history. (Histories of 2,000, one of 32,000 tokens: 9.5 us,
-// with blocks of 4,096 15.9; 48 of them, the rule's last: 15.3, 17.0; 64: 18.6, 17.4; 128: 29.3, 21.1. Five
-// rows of 131,072: 13.8, 15.3; 15 of them: 22.9, 15.9.)
-int steps_of(int N, int R, int V) { return (int64_t)N * R * ((V + 1023) / 1024) <= 1536 ? 1 : 4; }
-int block_of(int N, int R, int V) { return steps_of(N, R, V) * kThreads * kE; }
-
 template <typename T, typename O, Mode MODE, int STEPS>
 hipError_t launch(const LogitsPlan& p, hipStream_t stream) {
   constexpr int kBlock = STEPS * kThreads * kE;
-  const int blocks = (p.V + kBlock - 1) / kBlock;
-  // One row of a sequence to a workgroup while all rows' blocks fit the card's places at once, else all, which
-  // count the history once. (Five rows of 131,072 each, one sequence: 13.8 us, together 29.6; 8 sequences:
-  // 27.4, 32.6; 12, the rule's last: 33.1, 33.2; 16: 41.5, 33.9; 32: 74.4, 45.6.)
-  const int splits = (int64_t)p.N * p.R * blocks <= 2048 ? p.R : 1;
+  const int blocks = (int)logits_blocks(p.V, STEPS), splits = logits_splits(p.N, p.R, blocks);
   const size_t lds = sizeof(unsigned) * kBlock * (p.history || p.drafts ? 2 : p.bias_ids ? 1 : 0);
   logits_kernel<T, O, MODE, STEPS>
       <<<dim3((unsigned)((int64_t)p.N * splits * blocks)), kThreads, lds, stream>>>(p, blocks, splits);
@@ -471,14 +461,13 @@ hipError_t launch_steps(const LogitsPlan& p, hipStream_t stream) {
 
 template <typename T, typename O>
 hipError_t launch_all(const LogitsPlan& p, hipStream_t stream) {
-  return steps_of(p.N, p.R, p.V) == 1 ? launch_steps<T, O, 1>(p, stream) : launch_steps<T, O, 4>(p, stream);
+  return logits_steps(p.N, p.R, p.V) == 1 ? launch_steps<T, O, 1>(p, stream) : launch_steps<T, O, 4>(p, stream);
 }
 
 }  // namespace
 
 size_t logits_workspace_bytes(int N, int R, int V) {
-  const int block = block_of(N, R, V);
-  return sizeof(Stat) * (kThreads / 64) * (size_t)N * R * (((int64_t)V + block - 1) / block);
+  return sizeof(Stat) * (kThreads / 64) * (size_t)N * R * logits_blocks(V, logits_steps(N, R, V));
 }
 
 hipError_t launch_logits(const LogitsPlan& p, hipStream_t stream) {
