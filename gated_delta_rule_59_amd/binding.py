@@ -433,7 +433,8 @@ def check_gates(g, beta, stream=None, counts=None) -> int:
 
 
 # ---- the layers beside KDA: a paged key/value cache, the verification of drafts, linear attention with a
-#      decay for each head, the plan of a step's pages, and logits to probabilities. The tensors are marshalled in csrc/torch/marshal.cpp (built as _marshal.so). With a stream given, a call runs there
+#      decay for each head, the plan of a step's pages, and logits to probabilities. The tensors are
+#      marshalled in csrc/torch/marshal.cpp (built as _marshal.so). With a stream given, a call runs there
 #      (the caller orders it after what wrote its tensors), what it allocates is that stream's memory,
 #      and results may be used on the current stream once that has waited for it.
 
@@ -551,9 +552,10 @@ def page_plan(block_table, held, lens, new_lens, free_pages, ring, *, page_size,
     place; held [N]: pages of each sequence; lens [N]: its tokens that stand (`start` of kv_append);
     new_lens [N]: its tokens of this step, below 0 where it has ended and gives its pages back; ring [2]:
     head and number of the free pages. Returns (held, ring, both after the call; seq_lens [N];
-    cu_seqlens [N + 1]; slots [max_tokens]; positions [max_tokens]), in new tensors (parts of one
-    allocation) where none are given. A sequence that the pages or max_tokens do not suffice for gets no tokens in this step (see
-    kda_page_plan_args)."""
+    cu_seqlens [N + 1]; slots [max_tokens]; positions [max_tokens]), in new tensors where none are given.
+    Those are parts of one allocation, which lives as long as any of them: held and ring, which a caller
+    keeps, keep 12 bytes per token of max_tokens with them, unless held_out and ring_out are given. A sequence that the pages or max_tokens do not suffice for gets no tokens in
+    this step (see kda_page_plan_args)."""
     return (_ops or _marshal()).page_plan(block_table, held, lens, new_lens, free_pages, ring, page_size,
                                           max_tokens, held_out, ring_out, seq_lens, cu_seqlens, slots,
                                           positions, stream)
