@@ -75,7 +75,7 @@ __global__ __launch_bounds__(1024) void lin_jobs_kernel(const LinPlan p) {
 // Workgroups b and b + 256 share a CU, where the earlier goes first. Up to 64 packed sequences are taken
 // by length: whole segments, then the sequences' last ones from long to short, and where no more than
 // 512 workgroups have work, the second half backwards, so that long ones share with short ones (512 pairs of
-// 994 .. 15,902 tokens: in the sequences' order from short to long 1.51 ms, so 1.33 ms). Where heads share
+// 994 .. 15,902 tokens: with the second half forwards 1.60 ms, so 1.46 ms). Where heads share
 // queries and keys, an XCD (b mod 8) takes neighbouring ones of a dense batch.
 __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
   if (!p.cu_seqlens) {
@@ -139,7 +139,8 @@ __device__ __forceinline__ bool lin_job(const LinPlan& p, unsigned b, Job* j) {
 }
 
 // A barrier that orders the LDS only: rows of the next chunk stay on their way across it, and so do
-// results. (__syncthreads waits for both: 14 us per chunk where this takes 10.)
+// results. (__syncthreads, which waits for both, takes as long where a chunk's work covers them: 16 prompts of 994 ..
+// 15,902 tokens 1.45 ms with either.)
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(256) void lin_entries_kernel(const LinPlan p) {
 }
 
 // Workgroups that sum up segments. Up to 64 packed sequences give whole segments the first places, of which
-// there are no more than T / seg. (64 sequences of 4,096 tokens together, 32 heads: 125 us, so 111.)
+// there are no more than T / seg. (64 sequences of 4,096 tokens together, 32 heads: 146 us, so 133.)
 inline dim3 sums_grid(const LinPlan& p) {
   return dim3((unsigned)((int64_t)(p.cu_seqlens && p.n_seq <= 64 ? p.T / p.seg : p.jobs) * p.H));
 }
@@ -290,7 +291,7 @@ void launch_before(const LinPlan& p, hipStream_t stream, Sum sum) {
   constexpr int groups = (Sh::kState / 4 + 255) / 256;
   const int64_t items = (int64_t)p.n_seq * p.H * groups;
   // 2,048 are the card's places; sequences of one segment, which have nothing here, would cost a workgroup each
-  // part (300 packed sequences of 32 heads: 438 us, so 382).
+  // part (300 packed sequences of 32 heads: 455 us, so 396).
   lin_entries_kernel<Sh><<<dim3((unsigned)(items < 2048 ? items : 2048)), 256, 0, stream>>>(p);
 }
 

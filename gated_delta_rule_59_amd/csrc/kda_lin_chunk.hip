@@ -27,9 +27,9 @@
 // Precision. bf16 inputs go into products as they are. What is no bf16 number goes in parts, each the
 // rounded rest of the one before: decayed values, the state and the weights (q_i . k_j) e^{G_i - G_j} in three, which
 // hold their 24 bits, whatever o's type. (With two parts of state and weights long prompts with bf16 results took
-// 1.30 ms instead of 1.49, but results whose terms cancel were off by 2^-18 of the terms.) G is summed in 64 bits and kept in two 32-bit parts, so
-// that a strong decay costs the differences after it nothing; exponents too have a second part, so that a decay of
-// 2^-30 is as exact as one of 2^-1.
+// 1.30 ms instead of 1.49, but results whose terms cancel were off by 2^-18 of the terms.) G is summed in 64 bits
+// and kept in two 32-bit parts, so that a strong decay costs the differences after it nothing; exponents too have a
+// second part, so that a decay of 2^-30 is as exact as one of 2^-1.
 #include <algorithm>
 
 #include "kda_lin_chunk.h"
@@ -48,7 +48,7 @@ constexpr double kHeld = 24.0;  // most that a state may be off by in the accumu
 // Where channel c of row r lies in an LDS tile of rows of D. 16-byte pieces of a row change places with
 // the row, so that 16 lanes that read one piece of 16 rows, and 16 lanes that read a quarter of a
 // 32-channel block of each of four rows, meet all 64 banks. (Padded rows do the first only: 46 % of the
-// LDS's time went to conflicts of the second.)
+// LDS's cycles went to conflicts, of which 35 % are left, all accesses together.)
 template <int D>
 __device__ __forceinline__ int tile_at(int r, int c) {
   constexpr int kLog = D == 128 ? 0 : D == 64 ? 1 : 2;  // rows of 64 banks
@@ -426,11 +426,11 @@ hipError_t launch_dk(const LinPlan& p, hipStream_t stream) {
 
 size_t plan_lin_chunk(LinPlan* p) {
   // Workgroups: two fit a CU and there are 256 CUs. With 256 pairs of sequence and head there are no
-  // segments (8 x 32 pairs of 8,448 tokens: 674 us, in two segments each 772: a segment's sum is work
+  // segments (8 x 32 pairs of 8,448 tokens: 727 us, in two segments each 804: a segment's sum is work
   // that the walk proper does again). Below, segments of 512 tokens or more for 512 workgroups (16 pairs of
-  // 16,384 tokens: 122 us, with 256 workgroups 138), shorter ones, of 128 at least, for 256, which are
-  // done sooner each (16 pairs of 4,096: 52 us, with 512 workgroups 57; 8 pairs of 1,024: 28 us in segments of 128,
-  // 38 of 256, 70 in one). Packed sequences, whose lengths the host does not know, are cut as if
+  // 16,384 tokens: 132 us, with 256 workgroups 142), shorter ones, of 128 at least, for 256, which are
+  // done sooner each (16 pairs of 4,096: 51 us, with 512 workgroups 56; 8 pairs of 1,024: 28.6 us in segments of 128,
+  // 40 of 256). Packed sequences, whose lengths the host does not know, are cut as if
   // all tokens were one sequence.
   //
   // Those are bf16 of 128 x 128. Other shapes, whose workgroups are smaller, take the same cut; halved and doubled:

@@ -4,15 +4,15 @@
 //
 // for the new token or the drafts of each sequence. The state is read once and written once, 4 dk dv
 // bytes each way per (sequence, head), beside which a token's own rows are nothing: HBM bounds it. (512
-// sequences of 32 heads of 128 x 128, 2.15 GB: 375 us, torch's product in place 359; verification,
-// which only reads: 163 us.)
+// sequences of 32 heads of 128 x 128, 2.15 GB: 374 us, torch's product in place 358; verification,
+// which only reads: 161 us.)
 //
 // One 256-thread workgroup per (n, h). Thread t owns value columns 4 (t % CG) .. + 3 (CG = DV / 4) and
 // key rows t / CG + RG i (RG = 256 / CG): 16 bytes at t plus 4 KiB per i, so a wave reads 1 KiB pieces,
 // the state stays in registers between the read and the write, and the addresses take one register.
 // Fewer registers for more workgroups at a time cost more in spills than they bring (at most 96: 5 us
 // more, 72: 96 us). A call of one token has a kernel of its own, which writes a row as soon as it
-// is done (412 us as drafts are done). Drafts come four at a time through LDS; their results are summed over
+// is done (385 us as drafts are done). Drafts come four at a time through LDS; their results are summed over
 // the row groups there.
 //
 // All in 32 bits. The state after `accept` tokens is written when it is reached, and the tokens

@@ -3,10 +3,10 @@
 //
 // Every logit is read (twice for probabilities: once for the row's maximum and sum, once for the
 // values; of a few rows the second pass reads what the first made of them) and every result written once;
-// the second read comes from the caches where the batch fits them. The launches bound one row (7.8 us for
+// the second read comes from the caches where the batch fits them. The launches bound one row (4.9 and 3.4 us for
 // 32,000 tokens). For 256 sequences of five rows of 131,072, bf16 to fp32, with everything there is, the first
-// pass takes 151 us, which its instructions bound (about 75 where nothing is adjusted), the second 226, of
-// which 180 go to reading and writing 1 GB.
+// pass takes 150 us, which its instructions bound (75 where nothing is adjusted), the second 228, of
+// which 181 go to reading and writing 1 GB.
 //
 // A workgroup takes a block of tokens of one sequence, for all of its rows or for one, and has the next
 // row's logits on their way while it works on this one's. It first counts in LDS what the history holds of
@@ -172,8 +172,8 @@ __device__ __forceinline__ Stat join(Stat mine, const Stat* s, int n, bool greed
 }
 
 // Where the first pass may leave the adjusted logits in out for the second: fp32 results of a few rows, which
-// stay in the caches (with a history, one row of 32,000 tokens: 9.5 us, so 7.8; five of 131,072: 14.0, 12.5; 48 of
-// 32,000: 15.7, 14.4). Large batches would pay for the bytes (16 x 5 of 131,072: 33.9, so 42.5).
+// stay in the caches (with a history, one row of 32,000 tokens: 9.5 us, so 9.3; five of 131,072: 13.9, 12.6; 48 of
+// 32,000: 16.0, 14.8). Large batches would pay for the bytes (16 x 5 of 131,072: 33.9, so 42.5).
 template <typename O, int STEPS>
 constexpr bool kKeeps = STEPS == 1 && sizeof(O) == sizeof(float);
 
